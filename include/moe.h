@@ -317,6 +317,146 @@ moe_status_t moe_forward_noalloc(const moe_config_t* cfg, int64_t T, const void*
                                  int32_t* topk_idx_out, float* topk_w_out, int32_t* expert_counts_out,
                                  void* stream);
 
+/* ---- Training the experts -----------------------------------------------------------------
+ * The operators of a training step beside the forward: products grouped by expert whose
+ * operands and results stay with the caller (forward, input gradient, weight gradient), the
+ * SwiGLU activation with its gradient, and the AdamW step.  One layer, positions p in
+ * moe_dispatch's order, topk_w [T,K] and inv_perm [T,K] flattened:
+ *   g = moe_grouped_gemm(x by sorted_token, gate)     u = the same with up          (bf16)
+ *   h = moe_swiglu(g, u; row_w = topk_w, pos = inv_perm)                            (bf16)
+ *   y_sorted = moe_grouped_gemm(h, down) (fp32);  out = moe_combine(y_sorted, ones): the
+ *     routing weights are in h already
+ *   dh = moe_grouped_gemm_dgrad(dout by sorted_token, down)                         (bf16)
+ *   d_down = moe_grouped_gemm_wgrad(dout by sorted_token, h)
+ *   dg, du, d_topk_w = moe_swiglu_backward(g, u, dh; topk_w, inv_perm)
+ *   dx_sorted = moe_grouped_gemm_dgrad(dg, gate, du, up) (fp32); dx = moe_combine(dx_sorted, ones)
+ *   d_gate = moe_grouped_gemm_wgrad(dg, x by sorted_token); d_up likewise
+ *   moe_adamw_step on the expert weights; moe_update_expert_bias on the selection bias
+ * (The shared expert is a call with groups = 1 and offsets = expert_offsets + E.) */
+typedef enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_FP32 = 1 } moe_dtype_t;
+
+/* Groups of positions: group g holds positions offsets[g] <= p < offsets[g+1] (the first
+ * groups + 1 entries of moe_dispatch's expert_offsets, or that many from expert e on), each
+ * group with its own [out_features, in_features] weight.  Offsets are read on the device and
+ * taken as clamped to [0, rows]; a group may be empty. */
+typedef struct {
+  int32_t groups;         /* 1..1025 */
+  int32_t out_features;   /* N: multiple of 8, at most 65536 */
+  int32_t in_features;    /* K: multiple of 8, at most 65536 */
+  int64_t rows;           /* positions; below 2^31 - 4096 */
+  const int32_t* offsets; /* device [groups + 1], 4-byte aligned, not decreasing */
+} moe_groups_t;
+
+/* A bf16 operand by position: position p is row row_map[p] of the matrix (device int32 [rows],
+ * 4-byte aligned; moe_dispatch's sorted_token), or row p with row_map NULL.  A position whose
+ * row lies outside [0, rows) counts as a row of zeros and is never read. */
+typedef struct {
+  const void* data;       /* device bf16, row stride ld; NULL only with rows 0 */
+  int64_t rows;           /* rows of the matrix; with row_map NULL at least the positions */
+  int64_t ld;             /* values between rows: at least the columns, multiple of 8 */
+  const int32_t* row_map;
+} moe_rows_t;
+
+/* y[p] = w_g x[p] (fp32 accumulation) for every position p of every group g.
+ *   x  [.., in_features]; w device bf16 [groups, out_features, in_features]
+ *   y  device bf16 or fp32 (y_dtype) [rows, out_features], row stride ldy (multiple of 8).  Rows
+ *      of no group are left as they are.  accumulate != 0 adds to y (fp32 only).
+ * No workspace; results do not depend on the launch (no atomics).  An infinity or NaN of one row
+ * or group reaches that row's or group's results only. */
+moe_status_t moe_grouped_gemm(const moe_groups_t* groups, const moe_rows_t* x, const void* w, void* y, int64_t ldy,
+                              int32_t y_dtype, int32_t accumulate, void* stream);
+
+/* Input gradient: dx[p] = dy[p] w_g (+ dy2[p] w2_g, both or neither), summed in fp32 and rounded
+ * once.  dy, dy2 [.., out_features]; w, w2 as above; dx bf16 or fp32 [rows, in_features]. */
+moe_status_t moe_grouped_gemm_dgrad(const moe_groups_t* groups, const moe_rows_t* dy, const void* w,
+                                    const moe_rows_t* dy2, const void* w2, void* dx, int64_t lddx, int32_t dx_dtype,
+                                    int32_t accumulate, void* stream);
+
+/* Weight gradient: dw_g = sum over the group's positions of dy[p]^T x[p]; an empty group's is
+ * zero (or unchanged with accumulate != 0, which adds to dw; fp32 only).  A position counts only
+ * if its rows exist in both operands.
+ *   dw device bf16 or fp32 [groups, out_features, in_features] */
+moe_status_t moe_grouped_gemm_wgrad(const moe_groups_t* groups, const moe_rows_t* dy, const moe_rows_t* x, void* dw,
+                                    int32_t dw_dtype, int32_t accumulate, void* stream);
+
+/* SwiGLU with clamp and routing weight over stored products: for i < n and row r = pos[i] (i
+ * with pos NULL),  h[r] = row_w[i] * clamp(silu(gate[r]) * up[r], -limit, limit), rounded once.
+ *   gate, up  device bf16 [mat_rows, cols], row stride ld; h likewise with ldh; cols a multiple
+ *             of 8, strides multiples of 8
+ *   limit     > 0: clamp; 0, negative or infinite: none
+ *   row_w     device fp32 [n] or NULL (1);  pos device int32 [n] or NULL, entries distinct; an
+ *             entry outside [0, mat_rows) is skipped (moe_dispatch's -1)
+ * Rows that no entry names are left as they are. */
+moe_status_t moe_swiglu(int64_t n, int64_t mat_rows, int32_t cols, float limit, const void* gate, const void* up,
+                        int64_t ld, const float* row_w, const int32_t* pos, void* h, int64_t ldh, void* stream);
+
+/* Its gradient from dh: dgate, dup device bf16 [mat_rows, cols] (row stride ldd) and, unless NULL,
+ * drow_w device fp32 [n] (0 for a skipped entry).  A value that the clamp cuts, |silu(g) u| >
+ * limit, passes no gradient to gate and up. */
+moe_status_t moe_swiglu_backward(int64_t n, int64_t mat_rows, int32_t cols, float limit, const void* gate,
+                                 const void* up, int64_t ld, const void* dh, int64_t lddh, const float* row_w,
+                                 const int32_t* pos, void* dgate, void* dup, int64_t ldd, float* drow_w, void* stream);
+
+/* AdamW over many tensors in one launch:
+ *   m' = beta1 m + (1 - beta1) g;  v' = beta2 v + (1 - beta2) g^2      (each operation rounded
+ *        to fp32; g = grad, times *grad_scale if that is given)
+ *   p' = p (1 - lr weight_decay) - lr m' / (1 - beta1^step) / (sqrt(v' / (1 - beta2^step)) + eps)
+ * Parameters and gradients are bf16 or fp32; with bf16 parameters an fp32 master copy may hold
+ * the exact values (then the parameters are its rounding).  States are fp32, or 8 bits:
+ * MOE_STATE_8BIT keeps blocks of 128 consecutive values of a tensor as one code byte each and an
+ * fp32 scale, the block's largest magnitude / 1.875:
+ *   exp_avg     code = sign << 7 | e << 3 | f: (1 + f/8) 2^(e-15) scale, zero for e = f = 0
+ *   exp_avg_sq  code = e << 3 | f:             (1 + f/8) 2^(e-31) scale
+ * rounded stochastically by a hash of (seed, step, tensor's index in the plan, value's index):
+ * the same call gives the same codes.  Both moments start as zero codes with zero scales.  A block
+ * with an infinite or NaN value, which has no code, reads back as not finite. */
+typedef enum { MOE_STATE_FP32 = 0, MOE_STATE_8BIT = 1 } moe_state_format_t;
+
+typedef struct {           /* device arrays of one tensor, 16-byte aligned (scales 4-byte) */
+  void* param;             /* [numel] param_dtype, updated */
+  float* master;           /* [numel] fp32, updated; NULL for all tensors or for none */
+  const void* grad;        /* [numel] grad_dtype */
+  void* exp_avg;           /* [numel] fp32 or codes, updated */
+  void* exp_avg_sq;
+  float* exp_avg_scale;    /* [ceil(numel / 128)] fp32, MOE_STATE_8BIT only */
+  float* exp_avg_sq_scale;
+  int64_t numel;           /* may be 0 */
+  float weight_decay;
+  int32_t reserved;
+} moe_adamw_tensor_t;
+
+typedef struct {
+  int64_t n_tensors, n_chunks;
+  uint64_t flags;
+  size_t image_bytes;      /* size of the plan's image */
+} moe_adamw_plan_t;
+
+typedef struct {
+  double lr, beta1, beta2, eps;
+  int64_t step;            /* 1 for the first step */
+  uint32_t seed;           /* of the stochastic rounding */
+  const float* lr_ptr;     /* device; if given, read when the step runs instead of lr */
+  const int64_t* step_ptr; /* device; likewise for step (a captured step can then be replayed) */
+  const float* grad_scale; /* device; if given, multiplies every gradient */
+} moe_adamw_config_t;
+
+/* Host call: fills *plan and, with image (host memory, plan->image_bytes), the table that the
+ * step reads.  The caller copies the image to device memory once (16-byte aligned) and keeps it as
+ * long as the arrays stay where they are.  Arrays that the step writes must overlap no other. */
+moe_status_t moe_adamw_plan(int64_t n_tensors, const moe_adamw_tensor_t* tensors, int32_t param_dtype,
+                            int32_t grad_dtype, int32_t state_format, moe_adamw_plan_t* plan, void* image,
+                            size_t image_bytes);
+
+/* One step.  image: the device copy of the plan's image; an image that is not this plan's is
+ * recognised by the kernel, which then writes nothing. */
+moe_status_t moe_adamw_step(const moe_adamw_config_t* cfg, const moe_adamw_plan_t* plan, const void* image,
+                            void* stream);
+
+/* Values of an 8-bit state array: out[i] (device fp32) = the value that codes[i] stands for.
+ * is_signed != 0: exp_avg's codes, 0: exp_avg_sq's. */
+moe_status_t moe_adamw_dequantise(const uint8_t* codes, const float* scales, int64_t numel, int32_t is_signed,
+                                  float* out, void* stream);
+
 /* Static text for a status code. */
 const char* moe_status_string(moe_status_t status);
 

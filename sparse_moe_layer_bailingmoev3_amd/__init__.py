@@ -22,6 +22,9 @@ __all__ = ["MoEConfig", "MoEExpertWeights", "MoEError", "lib_path", "load_librar
            "MOE_WEIGHTS_BF16", "MOE_WEIGHTS_MXFP4", "MOE_WEIGHTS_MXFP8", "MOE_WEIGHTS_MXFP4_TILED",
            "MOE_WEIGHTS_MXFP8_TILED",
            "MOE_ACT_BF16", "MOE_ACT_MXFP8",
+           "MOE_DTYPE_BF16", "MOE_DTYPE_FP32", "MOE_STATE_FP32", "MOE_STATE_8BIT",
+           "moe_grouped_gemm", "moe_grouped_gemm_dgrad", "moe_grouped_gemm_wgrad", "moe_swiglu", "moe_swiglu_backward",
+           "MoEAdamWPlan", "moe_adamw_step", "moe_adamw_dequantise",
            "EXPORTED_SYMBOLS"]
 
 MOE_WEIGHTS_BF16 = 0
@@ -31,11 +34,17 @@ MOE_WEIGHTS_MXFP4_TILED = 3
 MOE_WEIGHTS_MXFP8_TILED = 4
 MOE_ACT_BF16 = 0
 MOE_ACT_MXFP8 = 1
+MOE_DTYPE_BF16 = 0
+MOE_DTYPE_FP32 = 1
+MOE_STATE_FP32 = 0
+MOE_STATE_8BIT = 1
 
 EXPORTED_SYMBOLS = ("moe_workspace_size", "moe_route", "moe_dispatch", "moe_expert_ffn", "moe_combine",
                     "moe_forward", "moe_forward_traced", "moe_forward_timed", "moe_update_expert_bias",
                     "moe_dense_ffn_workspace_size", "moe_dense_ffn", "moe_forward_noalloc", "moe_quantise_mxfp8",
-                    "moe_pack_mxfp4", "moe_pack_mxfp8", "moe_status_string", "moe_last_error")
+                    "moe_pack_mxfp4", "moe_pack_mxfp8", "moe_grouped_gemm", "moe_grouped_gemm_dgrad",
+                    "moe_grouped_gemm_wgrad", "moe_swiglu", "moe_swiglu_backward", "moe_adamw_plan", "moe_adamw_step",
+                    "moe_adamw_dequantise", "moe_status_string", "moe_last_error")
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 
@@ -58,6 +67,32 @@ class MoEConfig(ctypes.Structure):
 class _Weights(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("gate", "up", "down", "gate_scale", "up_scale", "down_scale",
                                                 "shared_gate", "shared_up", "shared_down")]
+
+
+class _Groups(ctypes.Structure):
+    _fields_ = [("groups", ctypes.c_int32), ("out_features", ctypes.c_int32), ("in_features", ctypes.c_int32),
+                ("rows", ctypes.c_int64), ("offsets", ctypes.c_void_p)]
+
+
+class _Rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("rows", ctypes.c_int64), ("ld", ctypes.c_int64), ("row_map", ctypes.c_void_p)]
+
+
+class _AdamWTensor(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("param", "master", "grad", "exp_avg", "exp_avg_sq", "exp_avg_scale",
+                                                "exp_avg_sq_scale")] + [
+        ("numel", ctypes.c_int64), ("weight_decay", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+class _AdamWPlan(ctypes.Structure):
+    _fields_ = [("n_tensors", ctypes.c_int64), ("n_chunks", ctypes.c_int64), ("flags", ctypes.c_uint64),
+                ("image_bytes", ctypes.c_size_t)]
+
+
+class _AdamWConfig(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_double),
+                ("step", ctypes.c_int64), ("seed", ctypes.c_uint32), ("lr_ptr", ctypes.c_void_p),
+                ("step_ptr", ctypes.c_void_p), ("grad_scale", ctypes.c_void_p)]
 
 
 class MoEExpertWeights:
@@ -89,6 +124,7 @@ def load_library():
     P, I64, SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t
     C = ctypes.POINTER(MoEConfig)
     W = ctypes.POINTER(_Weights)
+    I32, GR, RW = ctypes.c_int32, ctypes.POINTER(_Groups), ctypes.POINTER(_Rows)
     sigs = {
         "moe_workspace_size": [C, I64, ctypes.POINTER(SZ)],
         "moe_route": [C, I64, P, P, P, P, P, P, SZ, P],
@@ -106,6 +142,14 @@ def load_library():
         "moe_quantise_mxfp8": [P, I64, ctypes.c_int32, P, P, P],
         "moe_pack_mxfp4": [P, P, I64, ctypes.c_int32, ctypes.c_int32, P, P, P],
         "moe_pack_mxfp8": [P, P, I64, ctypes.c_int32, ctypes.c_int32, P, P, P],
+        "moe_grouped_gemm": [GR, RW, P, P, I64, I32, I32, P],
+        "moe_grouped_gemm_dgrad": [GR, RW, P, RW, P, P, I64, I32, I32, P],
+        "moe_grouped_gemm_wgrad": [GR, RW, RW, P, I32, I32, P],
+        "moe_swiglu": [I64, I64, I32, ctypes.c_float, P, P, I64, P, P, P, I64, P],
+        "moe_swiglu_backward": [I64, I64, I32, ctypes.c_float, P, P, I64, P, I64, P, P, P, P, I64, P, P],
+        "moe_adamw_plan": [I64, P, I32, I32, I32, ctypes.POINTER(_AdamWPlan), P, SZ],
+        "moe_adamw_step": [ctypes.POINTER(_AdamWConfig), ctypes.POINTER(_AdamWPlan), P, P],
+        "moe_adamw_dequantise": [P, P, I64, I32, P, P],
     }
     for name, args in sigs.items():
         fn = getattr(lib, name)
@@ -258,3 +302,270 @@ def moe_quantise_mxfp8(x, rows, cols, codes, scales, stream=None):
     """bf16 [rows, cols] -> MXFP8 E4M3 codes [rows, cols] and e8m0 scales [rows, cols/32] (the
     rounding the MXFP8-activation path applies to x)."""
     _check(load_library().moe_quantise_mxfp8(_ptr(x), rows, cols, _ptr(codes), _ptr(scales), _stream(stream)))
+
+
+# ---- training the experts ------------------------------------------------------------------------
+# These take their sizes from the tensors, so what a wrong tensor would make a kernel read is found
+# here: types, shapes, unit strides, one device.  A refused argument raises MoEError like one that
+# the library refuses.
+
+_ERR_INVALID, _ERR_UNSUPPORTED = -1, -2
+
+
+def _require(ok, message, status=_ERR_INVALID):
+    if not ok:
+        raise MoEError(status, message)
+
+
+class _on_device:
+    """The device that all tensors lie on, made current for the call; its current stream unless one
+    is given (which must belong to it)."""
+
+    def __init__(self, tensors, stream):
+        import torch
+        devices = {t.device for t in tensors if t is not None}
+        _require(len(devices) == 1, f"tensors lie on several devices: {sorted(map(str, devices))}")
+        self._dev = devices.pop()
+        _require(self._dev.type == "cuda", f"tensors must lie on a GPU, not on {self._dev}")
+        given = getattr(stream, "device", None)
+        _require(given is None or given == self._dev, f"stream belongs to {given}, tensors lie on {self._dev}")
+        self._guard = torch.cuda.device(self._dev)
+        self._stream = stream
+
+    def __enter__(self):
+        self._guard.__enter__()
+        return _stream(self._stream)
+
+    def __exit__(self, *exc):
+        return self._guard.__exit__(*exc)
+
+
+def _dtype_code(t, name):
+    import torch
+    codes = {torch.bfloat16: MOE_DTYPE_BF16, torch.float32: MOE_DTYPE_FP32}
+    _require(t.dtype in codes, f"{name} must be bfloat16 or float32, not {t.dtype}", _ERR_UNSUPPORTED)
+    return codes[t.dtype]
+
+
+def _typed(t, name, dtype, dim):
+    import torch
+    _require(isinstance(t, torch.Tensor), f"{name} must be a tensor")
+    _require(dtype is None or t.dtype == dtype, f"{name} must be {dtype}, not {t.dtype}")
+    _require(t.dim() == dim, f"{name} must have {dim} dimension(s), not {t.dim()}")
+    return t
+
+
+def _matrix(t, name, dtype=None):
+    """A [rows, columns] tensor whose columns lie side by side; returns it and its row stride."""
+    _typed(t, name, dtype, 2)
+    _require(t.shape[1] <= 1 or t.stride(1) == 1, f"{name}: the values of a row must lie side by side")
+    return t, t.stride(0) if t.shape[0] > 1 else max(t.stride(0), (t.shape[1] + 7) // 8 * 8)
+
+
+def _vector(t, name, dtype, n=None):
+    if t is None:
+        return None
+    _typed(t, name, dtype, 1)
+    _require(t.numel() <= 1 or t.stride(0) == 1, f"{name} must be contiguous")
+    _require(n is None or t.numel() == n, f"{name} has {t.numel()} entries, {n} needed")
+    return t
+
+
+def _weights3(t, name):
+    import torch
+    _typed(t, name, torch.bfloat16, 3)
+    _require(t.is_contiguous(), f"{name} must be contiguous")
+    return t
+
+
+def _groups(offsets, groups, n, k, rows):
+    import torch
+    _vector(offsets, "offsets", torch.int32, groups + 1)
+    return _Groups(groups, n, k, rows, _ptr(offsets))
+
+
+def _operand(t, name, cols, row_map, positions):
+    import torch
+    t, ld = _matrix(t, name, torch.bfloat16)
+    _require(t.shape[1] == cols, f"{name} has {t.shape[1]} columns, {cols} needed")
+    _vector(row_map, f"the row map of {name}", torch.int32, positions)
+    return _Rows(_ptr(t) if t.shape[0] else None, t.shape[0], ld, _ptr(row_map))
+
+
+def moe_grouped_gemm(x, w, offsets, y, row_map=None, accumulate=False, stream=None):
+    """y[p] = w[g] x[row_map[p]] for the positions offsets[g] <= p < offsets[g+1] of every group g:
+    x bf16 [.., in], w bf16 [G, out, in], offsets int32 [G+1], y bf16 or fp32 [P, out] (added to
+    with accumulate, fp32 only), row_map int32 [P] (None: position p is row p)."""
+    _weights3(w, "w")
+    y, ldy = _matrix(y, "y")
+    G, N, K = w.shape
+    _require(y.shape[1] == N, f"y has {y.shape[1]} columns, w makes {N}")
+    P = y.shape[0]
+    g, a = _groups(offsets, G, N, K, P), _operand(x, "x", K, row_map, P)
+    with _on_device((x, w, offsets, y, row_map), stream) as s:
+        _check(load_library().moe_grouped_gemm(ctypes.byref(g), ctypes.byref(a), _ptr(w), _ptr(y), ldy, _dtype_code(y, "y"),
+                                               int(bool(accumulate)), s))
+
+
+def moe_grouped_gemm_dgrad(dy, w, offsets, dx, row_map=None, dy2=None, w2=None, accumulate=False, stream=None):
+    """dx[p] = dy[row_map[p]] w[g] (+ dy2[row_map[p]] w2[g]): dy bf16 [.., out], w bf16 [G, out, in],
+    dx bf16 or fp32 [P, in]."""
+    _weights3(w, "w")
+    dx, lddx = _matrix(dx, "dx")
+    G, N, K = w.shape
+    _require(dx.shape[1] == K, f"dx has {dx.shape[1]} columns, w makes {K}")
+    _require((dy2 is None) == (w2 is None), "dy2 and w2 must be given together")
+    P = dx.shape[0]
+    g, a, b = _groups(offsets, G, N, K, P), _operand(dy, "dy", N, row_map, P), None
+    if w2 is not None:
+        _weights3(w2, "w2")
+        _require(w2.shape == w.shape, f"w2 is {tuple(w2.shape)}, w is {tuple(w.shape)}")
+        b = ctypes.byref(_operand(dy2, "dy2", N, row_map, P))
+    with _on_device((dy, w, offsets, dx, row_map, dy2, w2), stream) as s:
+        _check(load_library().moe_grouped_gemm_dgrad(ctypes.byref(g), ctypes.byref(a), _ptr(w), b, _ptr(w2), _ptr(dx), lddx,
+                                                     _dtype_code(dx, "dx"), int(bool(accumulate)), s))
+
+
+def moe_grouped_gemm_wgrad(dy, x, offsets, dw, dy_map=None, x_map=None, accumulate=False, stream=None):
+    """dw[g] = sum over group g's positions of dy[dy_map[p]]^T x[x_map[p]]: dy bf16 [.., out], x bf16
+    [.., in], dw bf16 or fp32 [G, out, in] (added to with accumulate, fp32 only)."""
+    _typed(dw, "dw", None, 3)
+    _require(dw.is_contiguous(), "dw must be contiguous")
+    G, N, K = dw.shape
+    sizes = {m.shape[0] if m is not None else t.shape[0] for t, m in ((dy, dy_map), (x, x_map))}
+    _require(len(sizes) == 1, f"dy and x cover different numbers of positions: {sorted(sizes)}")
+    P = sizes.pop()
+    g = _groups(offsets, G, N, K, P)
+    a, b = _operand(dy, "dy", N, dy_map, P), _operand(x, "x", K, x_map, P)
+    with _on_device((dy, x, offsets, dw, dy_map, x_map), stream) as s:
+        _check(load_library().moe_grouped_gemm_wgrad(ctypes.byref(g), ctypes.byref(a), ctypes.byref(b), _ptr(dw),
+                                                     _dtype_code(dw, "dw"), int(bool(accumulate)), s))
+
+
+def _like(first, /, **named):
+    """Row stride that the named matrices of the first one's shape share."""
+    import torch
+    strides = set()
+    for name, t in named.items():
+        t, ld = _matrix(t, name, torch.bfloat16)
+        _require(t.shape == first.shape, f"{name} is {tuple(t.shape)}, gate is {tuple(first.shape)}")
+        strides.add(ld)
+    _require(len(strides) == 1, f"{' and '.join(named)} must have the same row stride")
+    return strides.pop()
+
+
+def _pairs(row_w, pos, rows):
+    """Number of rows handled: that of the positions or weights given, else all."""
+    import torch
+    n = pos.numel() if pos is not None else row_w.numel() if row_w is not None else rows
+    _vector(pos, "pos", torch.int32, n)
+    _vector(row_w, "row_w", torch.float32, n)
+    return n
+
+
+def moe_swiglu(gate, up, h, limit=0.0, row_w=None, pos=None, stream=None):
+    """h[pos[i]] = row_w[i] * clamp(silu(gate[pos[i]]) * up[pos[i]], -limit, limit): gate, up, h bf16
+    [R, C]; row_w fp32 [n] (None: 1), pos int32 [n], distinct (None: row i), entries outside [0, R)
+    skipped; limit <= 0: no clamp."""
+    ld, ldh = _like(gate, gate=gate, up=up), _like(gate, h=h)
+    R, C = gate.shape
+    n = _pairs(row_w, pos, R)
+    with _on_device((gate, up, h, row_w, pos), stream) as s:
+        _check(load_library().moe_swiglu(n, R, C, float(limit), _ptr(gate), _ptr(up), ld, _ptr(row_w), _ptr(pos), _ptr(h), ldh, s))
+
+
+def moe_swiglu_backward(gate, up, dh, dgate, dup, limit=0.0, row_w=None, pos=None, drow_w=None, stream=None):
+    """Gradients of moe_swiglu from dh: dgate, dup bf16 [R, C], drow_w fp32 [n] (None: not wanted)."""
+    import torch
+    ld, lddh, ldd = _like(gate, gate=gate, up=up), _like(gate, dh=dh), _like(gate, dgate=dgate, dup=dup)
+    R, C = gate.shape
+    n = _pairs(row_w, pos, R)
+    _vector(drow_w, "drow_w", torch.float32, n)
+    with _on_device((gate, up, dh, dgate, dup, row_w, pos, drow_w), stream) as s:
+        _check(load_library().moe_swiglu_backward(n, R, C, float(limit), _ptr(gate), _ptr(up), ld, _ptr(dh), lddh, _ptr(row_w),
+                                                  _ptr(pos), _ptr(dgate), _ptr(dup), ldd, _ptr(drow_w), s))
+
+
+class MoEAdamWPlan:
+    """The table of an AdamW step over many tensors (moe_adamw_plan): built once, kept with its
+    tensors, which must stay where they are.  All arguments are equally long lists of contiguous
+    tensors on one device: params and grads bf16 or fp32 (one type each), exp_avg and exp_avg_sq
+    fp32, or uint8 codes with their fp32 scales ([ceil(numel / 128)]), master fp32 copies of bf16
+    params; weight_decay a number or one for each tensor."""
+
+    def __init__(self, params, grads, exp_avg, exp_avg_sq, master=None, exp_avg_scale=None, exp_avg_sq_scale=None,
+                 weight_decay=0.0):
+        import torch
+        cols = {"params": list(params), "grads": list(grads), "exp_avg": list(exp_avg), "exp_avg_sq": list(exp_avg_sq)}
+        n = len(cols["params"])
+        _require(n > 0, "params must not be empty")
+        eight = len(cols["exp_avg"]) > 0 and cols["exp_avg"][0].dtype == torch.uint8
+        _require((exp_avg_scale is not None) == eight and (exp_avg_sq_scale is not None) == eight,
+                 "scales belong to uint8 states, and both must be given")
+        for name, t in (("master", master), ("exp_avg_scale", exp_avg_scale), ("exp_avg_sq_scale", exp_avg_sq_scale)):
+            if t is not None:
+                cols[name] = list(t)
+        state = torch.uint8 if eight else torch.float32
+        types = {"params": cols["params"][0].dtype, "grads": cols["grads"][0].dtype if cols["grads"] else None,
+                 "exp_avg": state, "exp_avg_sq": state, "master": torch.float32, "exp_avg_scale": torch.float32,
+                 "exp_avg_sq_scale": torch.float32}
+        for name, ts in cols.items():
+            _require(len(ts) == n, f"{name} has {len(ts)} tensors, params {n}")
+            for i, t in enumerate(ts):
+                _require(t.dtype == types[name], f"{name}[{i}] must be {types[name]}, not {t.dtype}")
+                _require(t.is_contiguous(), f"{name}[{i}] must be contiguous")
+                want = cols["params"][i].numel()
+                want = -(-want // 128) if name.endswith("scale") else want
+                _require(t.numel() == want, f"{name}[{i}] has {t.numel()} values, {want} needed")
+        decay = list(weight_decay) if hasattr(weight_decay, "__len__") else [weight_decay] * n
+        _require(len(decay) == n, f"weight_decay has {len(decay)} entries, params {n}")
+        self._keep = cols
+        with _on_device([t for ts in cols.values() for t in ts], None):
+            self.device = cols["params"][0].device
+            table = (_AdamWTensor * n)()
+            field = {"params": "param", "grads": "grad"}
+            for name, ts in cols.items():
+                for i, t in enumerate(ts):
+                    setattr(table[i], field.get(name, name), _ptr(t) or None)
+            for i, t in enumerate(cols["params"]):
+                table[i].numel, table[i].weight_decay = t.numel(), float(decay[i])
+            self.struct = _AdamWPlan()
+            args = (n, ctypes.byref(table), _dtype_code(cols["params"][0], "params"), _dtype_code(cols["grads"][0], "grads"),
+                    MOE_STATE_8BIT if eight else MOE_STATE_FP32, ctypes.byref(self.struct))
+            lib = load_library()
+            _check(lib.moe_adamw_plan(*args, None, 0))
+            host = torch.empty(self.struct.image_bytes, dtype=torch.uint8)
+            _check(lib.moe_adamw_plan(*args, _ptr(host), host.numel()))
+            self.image = host.to(self.device)
+
+
+def moe_adamw_step(plan: MoEAdamWPlan, lr, step, betas=(0.9, 0.999), eps=1e-8, seed=0, grad_scale=None, stream=None):
+    """One AdamW step over the plan's tensors, in place.  lr and step (1 for the first) are numbers,
+    or device tensors (fp32, int64) read when the step runs; grad_scale an fp32 device tensor that
+    multiplies every gradient; seed that of the 8-bit states' stochastic rounding."""
+    import torch
+    cfg = _AdamWConfig(beta1=betas[0], beta2=betas[1], eps=eps, seed=seed & 0xFFFFFFFF)
+    given = [plan.image]
+    for name, v, dtype in (("lr", lr, torch.float32), ("step", step, torch.int64), ("grad_scale", grad_scale, torch.float32)):
+        if isinstance(v, torch.Tensor):
+            _require(v.dtype == dtype and v.numel() == 1, f"{name} must hold one {dtype} value")
+            given.append(v)
+            setattr(cfg, name if name == "grad_scale" else name + "_ptr", _ptr(v))
+        elif name != "grad_scale":
+            setattr(cfg, name, v)
+        else:
+            _require(v is None, "grad_scale must be a device tensor")
+    with _on_device(given, stream) as s:
+        _check(load_library().moe_adamw_step(ctypes.byref(cfg), ctypes.byref(plan.struct), _ptr(plan.image), s))
+
+
+def moe_adamw_dequantise(codes, scales, out, signed, stream=None):
+    """Values of an 8-bit state array: codes uint8 [n], scales fp32 [ceil(n / 128)] -> out fp32 [n];
+    signed: exp_avg's codes, else exp_avg_sq's."""
+    import torch
+    _vector(codes, "codes", torch.uint8)
+    n = codes.numel()
+    _vector(scales, "scales", torch.float32, -(-n // 128))
+    _vector(out, "out", torch.float32, n)
+    with _on_device((codes, scales, out), stream) as s:
+        _check(load_library().moe_adamw_dequantise(_ptr(codes), _ptr(scales), n, int(bool(signed)), _ptr(out), s))

@@ -279,6 +279,10 @@ moe_status_t do_combine(const moe_config_t* c, int64_t T, const void* y, const i
 
 }  // namespace
 
+namespace moe {
+void set_last_error(const char* msg) { g_last_error = msg; }
+}  // namespace moe
+
 extern "C" {
 
 const char* moe_status_string(moe_status_t st) {

@@ -23,6 +23,13 @@ __device__ __forceinline__ uint32_t f32_to_bf16_bits(float f) {
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return f32_to_bf16_bits(lo) | (f32_to_bf16_bits(hi) << 16);
 }
+// two fp32 -> two bf16, round to nearest even, low half first, by the hardware conversion: NaN
+// stays NaN and infinities stay (gfx950's packed conversion)
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float floatx2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t f32x2_to_bf16x2(float lo, float hi) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(floatx2{lo, hi}, bf16x2));
+}
 // two fp32 -> two fp16 (round to nearest even), saturated at +-65504 (finite inputs), low
 // half first
 __device__ __forceinline__ uint32_t pack_f16x2_sat(float lo, float hi) {

@@ -185,6 +185,75 @@ hipError_t launch_dense_ffn_small(const uint16_t* x, const uint16_t* gate, const
                                   int T, int H, int I, float limit, uint16_t* h_hi, uint16_t* h_lo, uint16_t* out,
                                   hipStream_t s);
 
+// compute units of the current device (asked once per device); 0 if there is none
+int device_cu_count();
+
+// records `msg` as the calling thread's last error (moe_last_error) and returns nothing
+void set_last_error(const char* msg);
+
+// ---- products grouped by expert (grouped.hip) ------------------------------------
+// rows of a bf16 matrix: row r at data + r * ld, taken through `map` (NULL: the position itself)
+struct RowsArg {
+  const uint16_t* data;
+  int32_t rows;
+  int64_t ld;
+  const int32_t* map;
+};
+struct GroupedArgs {
+  const int32_t* offsets;  // [groups + 1]
+  int groups, rows;        // rows: positions
+  int N, K;                // out_features, in_features of a group's weights [N,K]
+  RowsArg x0, x1;          // forward: x; dgrad: dy, dy2; wgrad: dy, x
+  const uint16_t* w0;      // forward, dgrad: weights [groups,N,K]
+  const uint16_t* w1;      // dgrad: the second product's weights, or NULL
+  void* out;               // forward [rows,N], dgrad [rows,K] (row stride ldo); wgrad [groups,N,K]
+  int64_t ldo;
+  int out_f32, accumulate;
+};
+hipError_t launch_grouped_rows(const GroupedArgs& a, bool dgrad, hipStream_t s);
+hipError_t launch_grouped_wgrad(const GroupedArgs& a, hipStream_t s);
+
+// ---- SwiGLU with routing weights (swiglu.hip) --------------------------------------
+struct SwigluArgs {
+  int64_t n;               // rows handled: row i is matrix row pos[i] (NULL: i)
+  int64_t mat_rows;
+  int cols;
+  float limit;
+  const uint16_t* gate; const uint16_t* up; int64_t ld;
+  const float* row_w;      // [n] or NULL (1)
+  const int32_t* pos;
+  uint16_t* h; int64_t ldh;                                 // forward
+  const uint16_t* dh;                                       // backward (row stride ldh)
+  uint16_t* dgate; uint16_t* dup; int64_t ldd;
+  float* drow_w;           // [n] or NULL
+};
+hipError_t launch_swiglu(const SwigluArgs& a, bool backward, hipStream_t s);
+
+// ---- AdamW over many tensors (adamw.hip) --------------------------------------------
+constexpr int ADAMW_BLOCK = 128;    // values that share a scale of the 8-bit states
+constexpr int ADAMW_CHUNK = 8192;   // values of one workgroup
+constexpr uint64_t ADAMW_MAGIC = 0x314d414441454f4dull;
+struct AdamWHeader { uint64_t magic; int64_t n_tensors, n_chunks; uint64_t flags; };  // plan image: header, tensors, chunks
+struct AdamWTensor {
+  void* param; float* master; const void* grad; void* m; void* v; float* ms; float* vs;
+  int64_t numel;
+  float weight_decay; int32_t pad;
+};
+struct AdamWChunk { int32_t tensor, chunk; };
+struct AdamWArgs {
+  const uint8_t* image;
+  int64_t n_tensors, n_chunks;
+  uint64_t flags;
+  float lr, b1, omb1, b2, omb2, eps, inv_c1, inv_c2;  // inv_c: 1 / (1 - beta^step)
+  double beta1, beta2;
+  uint32_t seed, step;
+  const float* lr_ptr; const int64_t* step_ptr; const float* grad_scale;
+};
+enum { ADAMW_PARAM_F32 = 1, ADAMW_GRAD_F32 = 2, ADAMW_EIGHT = 4, ADAMW_MASTER = 8 };
+hipError_t launch_adamw(const AdamWArgs& a, hipStream_t s);
+hipError_t launch_adamw_dequantise(const uint8_t* codes, const float* scales, int64_t n, bool is_signed, float* out,
+                                   hipStream_t s);
+
 // ---- combine -----------------------------------------------------------------
 // y16: y_sorted holds fp16 values (the tile kernels' y16 output) instead of fp32
 hipError_t launch_combine(const void* y_sorted, const int32_t* inv_perm, const float* topk_w, int T,

@@ -1,0 +1,401 @@
+"""The operators that train a layer's experts on the GPU, against their float64 definitions.
+
+Tolerances.  A product summed in fp32 over n terms is off by at most n 2^-24 times the sum of the
+terms' magnitudes whatever the order (every addition rounds by at most 2^-24 of a partial sum that
+these bound; the matrix instruction's own inner sums are counted twice over by taking 2n), and one
+rounding to bf16 adds 2^-8 of the value.
+"""
+import numpy as np
+import pytest
+import torch
+
+import sparse_moe_layer_bailingmoev3_amd as moe
+from oracle import train_oracle as orc
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+HALF_BF16 = 2.0 ** -8
+U32 = 2.0 ** -24
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def randn(g, *shape, dtype=BF, scale=1.0):
+    return (torch.randn(*shape, generator=g) * scale).to(dtype).cuda()
+
+
+def gen(seed):
+    g = torch.Generator()
+    g.manual_seed(seed)
+    return g
+
+
+def offsets_of(counts, first=0):
+    return torch.tensor([first] + list(first + np.cumsum(counts)), dtype=torch.int32).cuda()
+
+
+def check(got, want, mag, n, bf16):
+    tol = 2 * n * U32 * mag + (HALF_BF16 * np.abs(want) if bf16 else U32 * np.abs(want)) + 1e-37
+    err = np.abs(f64(got) - want)
+    bad = err > tol
+    assert not bad.any(), f"{bad.sum()} of {bad.size} off, first at {np.argwhere(bad)[0]}, err/tol {np.max(err / tol):.2f}"
+
+
+COUNTS = {
+    "one_row": [1],
+    "one_row_of_many": [0, 0, 1, 0],
+    "ragged": [3, 0, 17, 1, 64, 0, 5],
+    "long": [300, 1, 0, 129],
+    "tiles": [128, 256, 127],
+    "empty": [0, 0, 0],
+}
+DIMS = [(128, 128), (136, 264), (8, 8), (768, 72), (40, 520)]
+
+
+@pytest.mark.parametrize("dims", DIMS, ids=str)
+@pytest.mark.parametrize("counts", list(COUNTS))
+@pytest.mark.parametrize("kind", ["bf16", "fp32", "acc", "mapped"])
+def test_forward(counts, dims, kind):
+    g = gen(1)
+    c, (N, K) = COUNTS[counts], dims
+    first, tail = 2, 3            # rows of no group on both sides
+    off, P = offsets_of(c, first), first + sum(c) + tail
+    T = 11 if kind == "mapped" else P
+    x, w = randn(g, T, K), randn(g, len(c), N, K)
+    m = torch.randint(-1, T + 1, (P,), generator=g, dtype=torch.int32).cuda() if kind == "mapped" else None
+    y = randn(g, P, N, dtype=BF if kind in ("bf16", "mapped") else F32)
+    before = f64(y)
+    moe.moe_grouped_gemm(x, w, off, y, row_map=m, accumulate=kind == "acc")
+    want, mag = orc.grouped_forward(f64(x), f64(w), off.cpu().numpy(), before, None if m is None else m.cpu().numpy(), kind == "acc")
+    check(y, want, mag, K, y.dtype == BF)
+    assert np.array_equal(f64(y)[:first], before[:first]) and np.array_equal(f64(y)[P - tail:], before[P - tail:])
+
+
+@pytest.mark.parametrize("dims", DIMS, ids=str)
+@pytest.mark.parametrize("counts", list(COUNTS))
+@pytest.mark.parametrize("kind", ["bf16", "pair", "acc_pair", "mapped"])
+def test_dgrad(counts, dims, kind):
+    g = gen(2)
+    c, (N, K) = COUNTS[counts], dims
+    first, tail = 1, 2
+    off, P = offsets_of(c, first), first + sum(c) + tail
+    T = 9 if kind == "mapped" else P
+    pair = "pair" in kind
+    dy, w = randn(g, T, N), randn(g, len(c), N, K)
+    dy2, w2 = (randn(g, T, N), randn(g, len(c), N, K)) if pair else (None, None)
+    m = torch.randint(-1, T + 1, (P,), generator=g, dtype=torch.int32).cuda() if kind == "mapped" else None
+    dx = randn(g, P, K, dtype=F32 if pair else BF)
+    before = f64(dx)
+    moe.moe_grouped_gemm_dgrad(dy, w, off, dx, row_map=m, dy2=dy2, w2=w2, accumulate=kind == "acc_pair")
+    want, mag = orc.grouped_dgrad(f64(dy), f64(w), off.cpu().numpy(), before, None if m is None else m.cpu().numpy(),
+                                  f64(dy2) if pair else None, f64(w2) if pair else None, kind == "acc_pair")
+    check(dx, want, mag, 2 * N, dx.dtype == BF)
+    assert np.array_equal(f64(dx)[:first], before[:first]) and np.array_equal(f64(dx)[P - tail:], before[P - tail:])
+
+
+@pytest.mark.parametrize("dims", DIMS, ids=str)
+@pytest.mark.parametrize("counts", list(COUNTS))
+@pytest.mark.parametrize("kind", ["bf16", "fp32", "acc", "mapped_x", "mapped_both"])
+def test_wgrad(counts, dims, kind):
+    g = gen(3)
+    c, (N, K) = COUNTS[counts], dims
+    first, tail = 1, 2
+    off, P = offsets_of(c, first), first + sum(c) + tail
+    T = 13
+    mx = torch.randint(-1, T + 1, (P,), generator=g, dtype=torch.int32).cuda() if kind.startswith("mapped") else None
+    md = torch.randint(-1, T + 1, (P,), generator=g, dtype=torch.int32).cuda() if kind == "mapped_both" else None
+    dy, x = randn(g, T if md is not None else P, N), randn(g, T if mx is not None else P, K)
+    dw = randn(g, len(c), N, K, dtype=F32 if kind in ("fp32", "acc") else BF)
+    before = f64(dw)
+    moe.moe_grouped_gemm_wgrad(dy, x, off, dw, dy_map=md, x_map=mx, accumulate=kind == "acc")
+    num = lambda t: None if t is None else t.cpu().numpy()  # noqa: E731
+    want, mag = orc.grouped_wgrad(f64(dy), f64(x), off.cpu().numpy(), before, num(md), num(mx), kind == "acc")
+    check(dw, want, mag, max(c) + 1, dw.dtype == BF)
+
+
+def test_grouped_strided_operands():
+    """Operands and results that are columns of wider buffers."""
+    g = gen(4)
+    c, N, K = [5, 130, 0, 33], 72, 136
+    off, P = offsets_of(c), sum(c)
+    wide, w = randn(g, P, K + N + 24), randn(g, len(c), N, K)
+    x, dy = wide[:, 8:8 + K], wide[:, 16 + K:16 + K + N]
+    ybuf = torch.zeros(P, N + 40, dtype=F32, device="cuda")
+    y = ybuf[:, 16:16 + N]
+    moe.moe_grouped_gemm(x, w, off, y)
+    o = off.cpu().numpy()
+    want, mag = orc.grouped_forward(f64(x), f64(w), o, np.zeros((P, N)))
+    check(y, want, mag, K, False)
+    assert not ybuf[:, :16].any() and not ybuf[:, 16 + N:].any()
+    dxbuf = torch.zeros(P, K + 8, dtype=BF, device="cuda")
+    moe.moe_grouped_gemm_dgrad(dy, w, off, dxbuf[:, :K])
+    want, mag = orc.grouped_dgrad(f64(dy), f64(w), o, np.zeros((P, K)))
+    check(dxbuf[:, :K], want, mag, N, True)
+    assert not dxbuf[:, K:].any()
+    dw = torch.empty(len(c), N, K, dtype=F32, device="cuda")
+    moe.moe_grouped_gemm_wgrad(dy, x, off, dw)
+    want, mag = orc.grouped_wgrad(f64(dy), f64(x), o, np.zeros(dw.shape))
+    check(dw, want, mag, max(c), False)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_grouped_nonfinite_stays_where_it_is(bad):
+    """Values outside a group, its rows and its columns never reach a sum."""
+    g = gen(5)
+    c, N, K = [3, 5, 0, 70], 40, 72
+    off, P = offsets_of(c, 4), 4 + sum(c) + 4
+    x, w, dy = randn(g, P + 8, K), randn(g, len(c), N, K), randn(g, P + 8, N)
+    o = off.cpu().numpy()
+    for t in (x, dy):                     # rows of no group, and the rows behind the matrix
+        t[:4] = bad
+        t[P - 4:] = bad
+    w[2] = bad                            # the empty group's weights
+    x, dy = x[:P], dy[:P]
+    y = torch.zeros(P, N, dtype=F32, device="cuda")
+    dx = torch.zeros(P, K, dtype=F32, device="cuda")
+    dw = torch.zeros(len(c), N, K, dtype=F32, device="cuda")
+    moe.moe_grouped_gemm(x, w, off, y)
+    moe.moe_grouped_gemm_dgrad(dy, w, off, dx)
+    moe.moe_grouped_gemm_wgrad(dy, x, off, dw)
+    assert torch.isfinite(y).all() and torch.isfinite(dx).all() and torch.isfinite(dw).all()
+    assert not dw[2].any()
+    x[5] = bad                            # one row of group 0: its own results only
+    moe.moe_grouped_gemm(x, w, off, y)
+    fin = torch.isfinite(y).all(1)
+    assert not fin[5] and fin[:5].all() and fin[6:].all()
+    moe.moe_grouped_gemm_wgrad(dy, x, off, dw)
+    assert not torch.isfinite(dw[0]).any() and torch.isfinite(dw[1:]).all()
+    assert o[0] == 4
+
+
+def test_wgrad_skipped_row_may_hold_anything():
+    """A position without a row in one operand does not count, whatever the other holds there."""
+    g = gen(6)
+    off = offsets_of([6])
+    dy, x = randn(g, 4, 16), randn(g, 6, 24)
+    md = torch.tensor([0, -1, 2, 4, 3, 1], dtype=torch.int32).cuda()
+    x[1] = float("nan")
+    x[3] = float("inf")
+    dw = torch.empty(1, 16, 24, dtype=F32, device="cuda")
+    moe.moe_grouped_gemm_wgrad(dy, x, off, dw, dy_map=md)
+    keep = [0, 2, 4, 5]
+    want = f64(dy)[md.cpu().numpy()[keep]].T @ f64(x)[keep]
+    assert np.allclose(f64(dw)[0], want, rtol=1e-5, atol=1e-5)
+
+
+# ---- SwiGLU --------------------------------------------------------------------------------------
+
+def swiglu_inputs(g, R, C, n, skip):
+    gate, up, dh = randn(g, R, C, scale=3.0), randn(g, R, C, scale=2.0), randn(g, R, C)
+    pos = torch.randperm(R, generator=g)[:n].to(torch.int32)
+    if skip:
+        pos[::3] = -1
+        pos[1::7] = R
+    return gate, up, dh, pos.cuda(), (torch.rand(n, generator=g) + 0.1).cuda()
+
+
+@pytest.mark.parametrize("cols", [8, 136, 768, 1032])
+@pytest.mark.parametrize("rows,n,skip", [(1, 1, False), (37, 37, False), (50, 30, True)])
+@pytest.mark.parametrize("limit", [0.0, 4.0])
+def test_swiglu(cols, rows, n, skip, limit):
+    g = gen(7)
+    gate, up, dh, pos, w = swiglu_inputs(g, rows, cols, n, skip)
+    h = randn(g, rows, cols)
+    dgate, dup = randn(g, rows, cols), randn(g, rows, cols)
+    keep = [f64(t) for t in (h, dgate, dup)]
+    drow = torch.full((n,), 7.0, device="cuda")
+    moe.moe_swiglu(gate, up, h, limit=limit, row_w=w, pos=pos)
+    moe.moe_swiglu_backward(gate, up, dh, dgate, dup, limit=limit, row_w=w, pos=pos, drow_w=drow)
+    p = pos.cpu().numpy()
+    ok = (p >= 0) & (p < rows)
+    r = p[ok]
+    G, U, DH, W = f64(gate)[r], f64(up)[r], f64(dh)[r], f64(w)[ok]
+    sig, _, free, s = orc.swiglu(G, U, limit)
+    # the fp32 sigmoid: exp of an argument rounded by |g| 2^-24, and three more operations
+    rel = (np.abs(G) + 8) * 2 * U32
+    want = s * W[:, None]
+    assert (np.abs(f64(h)[r] - want) <= HALF_BF16 * np.abs(want) * (1 + 2 * HALF_BF16) + 4 * rel * np.abs(want) + 1e-37).all()
+    dg, du, dw = orc.swiglu_backward(G, U, DH, limit, W)
+    da = np.abs(DH * W[:, None] * U * sig)
+    assert (np.abs(f64(dgate)[r] - dg) <= HALF_BF16 * np.abs(dg) * (1 + 2 * HALF_BF16) + 4 * rel * da * (1 + np.abs(G)) + 1e-37).all()
+    assert (np.abs(f64(dup)[r] - du) <= HALF_BF16 * np.abs(du) * (1 + 2 * HALF_BF16) + 4 * rel * np.abs(du) + 1e-37).all()
+    terms = np.abs(DH * s)
+    assert (np.abs(f64(drow)[ok] - dw) <= (4 * rel * terms).sum(1) + cols * U32 * terms.sum(1) + 1e-37).all()
+    assert (f64(drow)[~ok] == 0).all()
+    rest = np.setdiff1d(np.arange(rows), r)
+    for t, b in zip((h, dgate, dup), keep):
+        assert np.array_equal(f64(t)[rest], b[rest])
+
+
+def test_swiglu_plain_rows_and_packed_buffers():
+    """No positions, no weights, gate and up side by side in one buffer; gradients likewise."""
+    g = gen(8)
+    R, C = 19, 40
+    buf, dbuf = randn(g, R, 2 * C), torch.zeros(R, 2 * C, dtype=BF, device="cuda")
+    dh, h = randn(g, R, C), torch.empty(R, C, dtype=BF, device="cuda")
+    gate, up = buf[:, :C], buf[:, C:]
+    moe.moe_swiglu(gate, up, h)
+    moe.moe_swiglu_backward(gate, up, dh, dbuf[:, :C], dbuf[:, C:])
+    _, _, _, s = orc.swiglu(f64(gate), f64(up), 0)
+    dg, du, _ = orc.swiglu_backward(f64(gate), f64(up), f64(dh), 0, np.ones(R))
+    assert np.allclose(f64(h), s, rtol=2.1 * HALF_BF16 / 2, atol=1e-6)
+    assert np.allclose(f64(dbuf[:, :C]), dg, rtol=2.1 * HALF_BF16 / 2, atol=1e-5)
+    assert np.allclose(f64(dbuf[:, C:]), du, rtol=2.1 * HALF_BF16 / 2, atol=1e-5)
+
+
+def test_swiglu_extreme_values():
+    """Saturated gates, infinities and NaN behave as the formula does; the clamp keeps NaN."""
+    vals = torch.tensor([-100.0, -30.0, -0.0, 0.0, 30.0, 100.0, float("nan"), float("inf")], dtype=BF).cuda()
+    gate, up = vals.repeat(8, 1), vals[:, None].expand(8, 8).contiguous()
+    h = torch.empty(8, 8, dtype=BF, device="cuda")
+    moe.moe_swiglu(gate, up, h, limit=5.0)
+    a = torch.nn.functional.silu(gate.double()) * up.double()
+    want = a.clamp(-5, 5).to(BF)
+    assert torch.equal(torch.isnan(h), torch.isnan(want))
+    fin = ~torch.isnan(want)
+    assert torch.allclose(h[fin].double(), want[fin].double(), atol=1e-6, rtol=HALF_BF16)
+
+
+def test_swiglu_backward_against_differences():
+    """Gradients against central differences of the float64 forward, away from the clamp's border."""
+    g = gen(9)
+    R, C, L = 6, 24, 3.0
+    gate, up, dh, pos, w = swiglu_inputs(g, R, C, R, False)
+    dgate, dup = torch.empty_like(gate), torch.empty_like(gate)
+    drow = torch.empty(R, device="cuda")
+    moe.moe_swiglu_backward(gate, up, dh, dgate, dup, limit=L, row_w=w, pos=pos, drow_w=drow)
+    p = pos.cpu().numpy()
+    W = np.empty(R)
+    W[p] = f64(w)
+    G, U, DH = f64(gate), f64(up), f64(dh)
+    f = lambda G, U, W: (DH * W[:, None] * orc.swiglu(G, U, L)[3])  # noqa: E731
+    e = 1e-5
+    a = np.abs(orc.swiglu(G, U, L)[1])
+    far = np.abs(a - L) > 1e-3
+    # a difference quotient is off by e^2 times the third derivative (below 10 |dh w u|) and by 1e-16 / e
+    slack = 1e-6 * (1 + np.abs(DH * W[:, None]) * (1 + np.abs(U)) * (1 + np.abs(G)))
+    ng = (f(G + e, U, W) - f(G - e, U, W)) / (2 * e)
+    nu = (f(G, U + e, W) - f(G, U - e, W)) / (2 * e)
+    nw = (f(G, U, W + e) - f(G, U, W - e)).sum(1) / (2 * e)
+    assert (np.abs(f64(dgate) - ng) <= HALF_BF16 * 1.01 * np.abs(ng) + slack)[far].all()
+    assert (np.abs(f64(dup) - nu) <= HALF_BF16 * 1.01 * np.abs(nu) + slack)[far].all()
+    assert (np.abs(f64(drow) - nw[p]) <= 1e-4 * (1 + np.abs(nw[p]))).all()
+
+
+# ---- AdamW ---------------------------------------------------------------------------------------
+
+SIZES = [1, 7, 128, 129, 1000, 8192, 8193, 20000, 0]
+
+
+def adamw_inputs(seed, pdt, gdt, eight, master, sizes=SIZES):
+    g = gen(seed)
+    params = [randn(g, n, dtype=pdt, scale=0.05) for n in sizes]
+    grads = [randn(g, n, dtype=gdt, scale=1e-2) for n in sizes]
+    ms = [p.float() + 1e-4 for p in params] if master else None
+    if eight:
+        m = [torch.zeros(n, dtype=torch.uint8, device="cuda") for n in sizes]
+        v = [torch.zeros(n, dtype=torch.uint8, device="cuda") for n in sizes]
+        sc = [torch.zeros(-(-n // 128), device="cuda") for n in sizes]
+        sv = [torch.zeros(-(-n // 128), device="cuda") for n in sizes]
+    else:
+        m, v = [randn(g, n, dtype=F32, scale=1e-2) for n in sizes], [randn(g, n, dtype=F32, scale=1e-2).square() for n in sizes]
+        sc = sv = None
+    return params, grads, ms, m, v, sc, sv
+
+
+@pytest.mark.parametrize("pdt", [BF, F32], ids=["pbf16", "pfp32"])
+@pytest.mark.parametrize("gdt", [BF, F32], ids=["gbf16", "gfp32"])
+@pytest.mark.parametrize("eight", [False, True], ids=["s32", "s8"])
+@pytest.mark.parametrize("master", [False, True], ids=["plain", "master"])
+def test_adamw(pdt, gdt, eight, master):
+    if master and pdt == F32:
+        pytest.skip("master weights belong to bf16 parameters")
+    params, grads, ms, m, v, sc, sv = adamw_inputs(10, pdt, gdt, eight, master)
+    wd = [0.1 * (i % 2) for i in range(len(SIZES))]
+    plan = moe.MoEAdamWPlan(params, grads, m, v, master=ms, exp_avg_scale=sc, exp_avg_sq_scale=sv, weight_decay=wd)
+    lr, betas, eps, seed = 1e-2, (0.9, 0.999), 1e-8, 77
+    for step in (1, 2, 3):
+        before = [f64(t) for t in (ms if master else params)]
+        if eight:
+            old = [(orc.state_decode(a.cpu().numpy(), s.cpu().numpy(), True), orc.state_decode(b.cpu().numpy(), q.cpu().numpy(), False))
+                   for a, s, b, q in zip(m, sc, v, sv)]
+        else:
+            old = [(a.cpu().numpy(), b.cpu().numpy()) for a, b in zip(m, v)]
+        moe.moe_adamw_step(plan, lr=lr, step=step, betas=betas, eps=eps, seed=seed)
+        for i, n in enumerate(SIZES):
+            wm, wv = orc.adamw_moments(old[i][0], old[i][1], grads[i].float().cpu().numpy(), betas)
+            if eight:
+                for codes, scales, x, signed in ((m[i], sc[i], wm, True), (v[i], sv[i], wv, False)):
+                    wc, ws = orc.state_encode(x, signed, i, seed, step)
+                    assert np.array_equal(scales.cpu().numpy(), ws)
+                    assert np.array_equal(codes.cpu().numpy(), wc)
+                    out = torch.empty(n, device="cuda")
+                    moe.moe_adamw_dequantise(codes, scales, out, signed)
+                    assert np.array_equal(out.cpu().numpy(), orc.state_decode(wc, ws, signed))
+            else:  # the same fp32 operations: the same bits
+                assert np.array_equal(m[i].cpu().numpy(), wm) and np.array_equal(v[i].cpu().numpy(), wv)
+            want = orc.adamw_param(before[i], wm, wv, lr, step, betas, eps, wd[i])
+            # about ten fp32 operations on the update and three on the parameter
+            tol = 16 * U32 * (np.abs(want - before[i]) + lr) + 4 * U32 * np.abs(before[i])
+            if master:
+                assert (np.abs(f64(ms[i]) - want) <= tol).all()
+                assert torch.equal(params[i], ms[i].to(BF))
+            else:
+                assert (np.abs(f64(params[i]) - want) <= tol + (HALF_BF16 * np.abs(want) if pdt == BF else 0)).all()
+
+
+def test_adamw_device_scalars_match_host():
+    """lr, step and the gradient scale from device memory: the same states bit for bit."""
+    a, b = (adamw_inputs(11, BF, BF, True, True) for _ in range(2))
+    mk = lambda t: moe.MoEAdamWPlan(t[0], t[1], t[3], t[4], master=t[2], exp_avg_scale=t[5], exp_avg_sq_scale=t[6])  # noqa: E731
+    pa, pb = mk(a), mk(b)
+    for g in b[1]:
+        g.mul_(0.5)                       # exact
+    moe.moe_adamw_step(pa, lr=torch.tensor([1e-3], device="cuda"), step=torch.tensor([5], device="cuda"), seed=3,
+                       grad_scale=torch.tensor([0.5], device="cuda"))
+    moe.moe_adamw_step(pb, lr=float(np.float32(1e-3)), step=5, seed=3)
+    for i in (3, 4, 5, 6):
+        for x, y in zip(a[i], b[i]):
+            assert torch.equal(x, y)
+    for x, y in zip(a[2], b[2]):
+        assert torch.allclose(x, y, rtol=1e-6, atol=1e-9)
+
+
+def test_adamw_nonfinite_gradient_shows():
+    """An infinite or NaN gradient is not lost in the 8-bit states; other blocks keep their values."""
+    for bad in (float("nan"), float("inf")):
+        params, grads, _, m, v, sc, sv = adamw_inputs(12, BF, F32, True, False, [512])
+        grads[0][130] = bad
+        plan = moe.MoEAdamWPlan(params, grads, m, v, exp_avg_scale=sc, exp_avg_sq_scale=sv)
+        moe.moe_adamw_step(plan, lr=1e-3, step=1)
+        out = torch.empty(512, device="cuda")
+        moe.moe_adamw_dequantise(m[0], sc[0], out, True)
+        assert not torch.isfinite(out[128:256]).any() or not torch.isfinite(out[130])
+        assert torch.isfinite(out[:128]).all() and torch.isfinite(out[256:]).all()
+
+
+def test_adamw_rounding_is_unbiased():
+    """A constant gradient: with rounding to nearest the second moment would stand still; the mean
+    over many values follows the fp32 recurrence.  One rounding errs by at most an eighth of the
+    value, independently from value to value and step to step, so the mean of n values after s
+    steps is off by less than 5 (0.125 / sqrt(3)) sqrt(s (1-b2)^2 ...) / sqrt(n); 2 % leaves that far behind."""
+    n, steps, betas = 128 * 512, 40, (0.9, 0.99)
+    p, gr = [torch.zeros(n, device="cuda")], [torch.full((n,), 0.25, device="cuda")]
+    gr[0][::2] = 1.0                      # half the values sit below the block's maximum
+    m, v = ([torch.zeros(n, dtype=torch.uint8, device="cuda")] for _ in range(2))
+    sc, sv = ([torch.zeros(n // 128, device="cuda")] for _ in range(2))
+    plan = moe.MoEAdamWPlan(p, gr, m, v, exp_avg_scale=sc, exp_avg_sq_scale=sv)
+    for s in range(1, steps + 1):
+        moe.moe_adamw_step(plan, lr=0.0, step=s, betas=betas, seed=5)
+    out = torch.empty(n, device="cuda")
+    moe.moe_adamw_dequantise(v[0], sv[0], out, False)
+    for start, g in ((0, 1.0), (1, 0.25)):
+        want = g * g * (1 - betas[1] ** steps)
+        assert abs(out[start::2].double().mean().item() / want - 1) < 0.02
+    moe.moe_adamw_dequantise(m[0], sc[0], out, True)
+    for start, g in ((0, 1.0), (1, 0.25)):
+        want = g * (1 - betas[0] ** steps)
+        assert abs(out[start::2].double().mean().item() / want - 1) < 0.02
