@@ -87,59 +87,71 @@ __device__ __forceinline__ int swz_tr(int row) {
   return (((row >> 3) & 1)) << 1;                                            // 64-byte rows
 }
 
+// Loads through the scalar data cache (uniform addresses of data the kernel never writes): they are
+// counted by lgkmcnt, so finding the next tile's rows never waits on the loads of the tiles' data.
+typedef const __attribute__((address_space(4))) int32_t* sptr;
+
 template <int OP, int BR, int BC, int WR, int WC, int NST, bool F32>
-__global__ __launch_bounds__(WR* WC * 64, 2) void grouped_kernel(GroupedArgs a) {
+__global__ __launch_bounds__(WR* WC * 64, (WR * WC == 4 && NST * (BR + BC) * G_KS * 2 > 72 * 1024) ? 1 : 2) void grouped_kernel(GroupedArgs a) {
   constexpr bool XT = OP == OP_WGRAD, YT = OP != OP_FWD;  // operands read through the transposing load
   constexpr int NW = WR * WC;
   constexpr int X_BYTES = BR * G_KS * 2, Y_BYTES = BC * G_KS * 2, ST_BYTES = X_BYTES + Y_BYTES;
   constexpr int XN = X_BYTES / (NW * 1024), YN = Y_BYTES / (NW * 1024);  // loads per wave and step
   static_assert(XN * NW * 1024 == X_BYTES && YN * NW * 1024 == Y_BYTES, "a stage must split evenly over the waves");
   static_assert(OP != OP_WGRAD || BR == BC, "both operands of wgrad share their row indices");
-  constexpr int NLOAD = XN + YN;  // (wgrad's row index loads, in between, only make the waits stricter)
   constexpr int D = NST - 1;  // steps in flight
+  static_assert(XN == 1 || OP == OP_WGRAD || D <= 2, "the load counts of at most one later step are told apart");
   constexpr int RJ = BR / WR / 16, CJ = BC / WC / 16;
   static_assert(RJ * WR * 16 == BR && CJ * WC * 16 == BC, "wave tiles of 16");
   // lanes per LDS row and rows per load of a transposed operand
   constexpr int XL = BR / 8, YL = BC / 8, XR = 64 / XL, YR = 64 / YL;
 
   __shared__ __align__(16) uint8_t lds[NST * ST_BYTES];
-  __shared__ int32_t prefix[OP == OP_WGRAD ? 1 : G_MAX_GROUPS + 1];
+  __shared__ int32_t prefix[OP == OP_WGRAD ? 1 : G_MAX_GROUPS + 65];  // row tiles before each group
+  __shared__ int32_t wave_total[NW];
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, q = lane >> 4;
   const int wr = wave / WC, wc = wave % WC;
   const int G = a.groups;
-  const int Rdim = OP == OP_WGRAD ? a.N : 0;               // wgrad's row extent
-  const int Cdim = OP == OP_FWD ? a.N : a.K;               // contiguous output extent
-  const int Red = OP == OP_FWD ? a.K : a.N;                // reduction extent (forward, dgrad)
+  const int Cdim = OP == OP_FWD ? a.N : a.K;  // contiguous output extent
+  const int Red = OP == OP_FWD ? a.K : a.N;   // reduction extent (forward, dgrad)
   const int nct = (Cdim + BC - 1) / BC;
-  const int nrt = OP == OP_WGRAD ? (Rdim + BR - 1) / BR : 0;
+  const int nrt = OP == OP_WGRAD ? (a.N + BR - 1) / BR : 0;
 
-  // positions of group g, clamped so that no offset leads outside the caller's rows
-  auto begin_of = [&](int g) { return min(max(a.offsets[g], 0), a.rows); };
-  auto count_of = [&](int g) { const int b = begin_of(g); return max(min(a.offsets[g + 1], a.rows) - b, 0); };
-
-  // ---- the prefix of row tiles (forward, dgrad): wave 0 scans 64 groups at a time
+  // ---- the prefix of row tiles over the groups (forward, dgrad), a group per thread and round
   if constexpr (OP != OP_WGRAD) {
-    if (wave == 0) {
-      int run = 0;
-      for (int g0 = 0; g0 < G; g0 += 64) {
-        const int g = g0 + lane;
-        int v = g < G ? (count_of(g) + BR - 1) / BR : 0;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-          const int t = __shfl_up(v, d, 64);
-          if (lane >= d) v += t;
-        }
-        if (g < G) prefix[g + 1] = run + v;
-        run += __shfl(v, 63, 64);
+    int run = 0;
+    for (int g0 = 0; g0 < G; g0 += NW * 64) {
+      const int g = g0 + threadIdx.x;
+      int v = 0;
+      if (g < G) {
+        const int b = min(max(a.offsets[g], 0), a.rows);
+        v = (max(min(a.offsets[g + 1], a.rows) - b, 0) + BR - 1) / BR;
       }
-      if (lane == 0) prefix[0] = 0;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int t = __shfl_up(v, d, 64);
+        if (lane >= d) v += t;
+      }
+      if (lane == 63) wave_total[wave] = v;
+      __syncthreads();
+      int before = run;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        if (w < wave) before += wave_total[w];
+        run += wave_total[w];
+      }
+      if (g < G) prefix[g + 1] = before + v;
+      __syncthreads();
     }
+    // 64 entries past the last group end the lanes' search
+    if (threadIdx.x < 64) prefix[G + 1 + threadIdx.x] = 0x7FFFFFFF;
+    if (threadIdx.x == 0) prefix[0] = 0;
     __syncthreads();
   }
-  const int ntile = OP == OP_WGRAD ? G * nrt : prefix[G];
+  const int ntile = OP == OP_WGRAD ? G * nrt : __builtin_amdgcn_readfirstlane(prefix[G]);
 
   // ---- LDS read addresses, constant per lane
   // row-major operand: row j*16 + r16, chunk (4u + q); transposed: block cb of 16 columns
@@ -163,221 +175,246 @@ __global__ __launch_bounds__(WR* WC * 64, 2) void grouped_kernel(GroupedArgs a) 
     for (int u = 0; u < 2; ++u) ya[u] = X_BYTES + (wc * CJ * 16 + r16) * 128 + (((4 * u + q) ^ swz_k(r16)) << 4);
   }
 
-  const int64_t total = (int64_t)ntile * nct;
-  const int64_t per = (total + 7) >> 3;
-  const int64_t first = (int64_t)(blockIdx.x & 7) * per;
-  const int64_t last = min(first + per, total);
+  // ---- this workgroup's tiles.  The loads run D steps ahead of the products, across tiles, so
+  // the two sides walk the tiles separately.
   const int slots = gridDim.x >> 3;
-  int e = 0;  // group of the current tile (tiles of a workgroup only grow)
-
-  for (int64_t item = first + (blockIdx.x >> 3); item < last; item += slots) {
-    const int tile = (int)(item / nct), ct = (int)(item - (int64_t)tile * nct);
-    int r0;  // first row of the tile: position (forward, dgrad) or weight row (wgrad)
+  const int dtile = slots / nct, dct = slots - dtile * nct;
+  struct Walk {
+    int64_t left;  // tiles after this one's position in the XCD's range
+    int tile, ct;
+    int e, p0, cnt, r0, c0, nsteps, steps1;
+  };
+  const sptr offsets = (sptr)a.offsets;
+  auto locate = [&](Walk& w) {
     if constexpr (OP == OP_WGRAD) {
-      e = tile / nrt;
-      r0 = (tile - e * nrt) * BR;
+      w.e = w.tile / nrt;
+      w.r0 = (w.tile - w.e * nrt) * BR;
     } else {
-      while (prefix[e + 1] <= tile) ++e;
-      r0 = (tile - prefix[e]) * BR;
+      // the lanes look at 64 groups at a time
+      for (;;) {
+        const int n = __popcll(__ballot(prefix[w.e + 1 + lane] <= w.tile));
+        w.e += n;
+        if (n < 64) break;
+      }
+      w.e = __builtin_amdgcn_readfirstlane(w.e);
+      w.r0 = (w.tile - __builtin_amdgcn_readfirstlane(prefix[w.e])) * BR;
     }
-    const int p0 = begin_of(e), cnt = count_of(e);
-    const int c0 = ct * BC;
-    const int nred = OP == OP_WGRAD ? cnt : Red;
-    const int steps1 = (nred + G_KS - 1) / G_KS;
-    const int nsteps = (OP == OP_DGRAD && a.w1) ? 2 * steps1 : steps1;
+    w.p0 = min(max(offsets[w.e], 0), a.rows);
+    w.cnt = max(min(offsets[w.e + 1], a.rows) - w.p0, 0);
+    w.c0 = w.ct * BC;
+    // an empty group's gradient is one step of zeros
+    w.steps1 = OP == OP_WGRAD ? max((w.cnt + G_KS - 1) / G_KS, 1) : (Red + G_KS - 1) / G_KS;
+    w.nsteps = (OP == OP_DGRAD && a.w1) ? 2 * w.steps1 : w.steps1;
+  };
+  auto advance = [&](Walk& w) -> bool {
+    w.left -= slots;
+    if (w.left <= 0) return false;
+    w.tile += dtile;
+    w.ct += dct;
+    if (w.ct >= nct) {
+      w.ct -= nct;
+      ++w.tile;
+    }
+    locate(w);
+    return true;
+  };
+  Walk ld;
+  {
+    const int64_t total = (int64_t)ntile * nct, per = (total + 7) >> 3;
+    const int64_t first = (int64_t)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
+    ld.left = min((int64_t)(blockIdx.x & 7) * per + per, total) - first;
+    if (ld.left <= 0) return;
+    ld.tile = (int)(first / nct);
+    ld.ct = (int)(first - (int64_t)ld.tile * nct);
+    ld.e = 0;
+    locate(ld);
+  }
+  Walk cw = ld;  // the products' side
+  int ls = 0;    // next step to load of tile `ld`
+  bool more = true;
 
-    // ---- load sources
-    const char* xs[XN];
-    const char* ys[YN];
-    int xinc[XN];
-    int64_t yinc[YN];
-    const char* const zero = (const char*)grouped_zeros;
-    auto set_x = [&](const RowsArg& m) {  // row-major operand of the rows
-      if constexpr (!XT) {
+  // ---- load sources
+  const char* xs[XN];
+  const char* ys[YN];
+  int xinc[XN];
+  int64_t yinc[YN];
+  int xn = XN;  // row loads that hold a row of the tile
+  const char* const zero = (const char*)grouped_zeros;
+  // eight consecutive rows of a load: lane's row (lane / 8) of positions p.., through the map
+  auto mapped = [&](const RowsArg& m, int p, int last, int sub, int n) {
+    int src = 0;
+    const sptr map = (sptr)m.map;
 #pragma unroll
-        for (int i = 0; i < XN; ++i) {
-          const int row = (wave * XN + i) * 8 + (lane >> 3);
-          int src = -1;
-          if (r0 + row < cnt) src = m.map ? m.map[p0 + r0 + row] : p0 + r0 + row;
-          const bool ok = (unsigned)src < (unsigned)m.rows;
-          const int ch = (lane & 7) ^ swz_k(row);
-          xs[i] = ok ? (const char*)m.data + ((int64_t)src * m.ld + ch * 8) * 2 : zero;
-          xinc[i] = ok ? G_KS * 2 : 0;
-        }
-      }
-    };
-    auto set_y = [&](const uint16_t* w) {  // the group's weights
-      const char* wb = (const char*)(w + (int64_t)e * a.N * a.K);
-      if constexpr (OP == OP_FWD) {
+    for (int k = 0; k < 8; ++k) {
+      if (k >= n) break;
+      const int t = map[min(p + k, last)];
+      src = sub == k ? t : src;
+    }
+    return src;
+  };
+  auto set_x = [&](const RowsArg& m) {  // row-major operand of the rows; load i holds rows i*NW*8 + wave*8 ..
+    if constexpr (!XT) {
+      const int n = ld.cnt - ld.r0;
+      xn = min((n + NW * 8 - 1) / (NW * 8), XN);
 #pragma unroll
-        for (int i = 0; i < YN; ++i) {
-          const int row = (wave * YN + i) * 8 + (lane >> 3);
-          const bool ok = c0 + row < a.N;
-          ys[i] = ok ? wb + ((int64_t)(c0 + row) * a.K + ((lane & 7) ^ swz_k(row)) * 8) * 2 : zero;
-          yinc[i] = ok ? G_KS * 2 : 0;
-        }
-      } else if constexpr (OP == OP_DGRAD) {
+      for (int i = 0; i < XN; ++i) {
+        const int row0 = (i * NW + wave) * 8, row = row0 + (lane >> 3);
+        const int p = ld.p0 + ld.r0 + row0;
+        int src = p + (lane >> 3);
+        if (m.map && row0 < n) src = mapped(m, p, ld.p0 + ld.cnt - 1, lane >> 3, 8);
+        const bool ok = row < n && (unsigned)src < (unsigned)m.rows;
+        const int ch = (lane & 7) ^ swz_k(row);
+        xs[i] = ok ? (const char*)m.data + ((int64_t)src * m.ld + ch * 8) * 2 : zero;
+        xinc[i] = ok ? G_KS * 2 : 0;
+      }
+    }
+  };
+  auto set_y = [&](const uint16_t* w) {  // the group's weights
+    const char* wb = (const char*)(w + (int64_t)ld.e * a.N * a.K);
+    if constexpr (OP == OP_FWD) {
 #pragma unroll
-        for (int i = 0; i < YN; ++i) {
-          const int row = (wave * YN + i) * YR + lane / YL;
-          const int col = c0 + ((lane % YL) ^ swz_tr<BC>(row)) * 8;
-          const bool ok = col < a.K;
-          ys[i] = ok ? wb + ((int64_t)row * a.K + col) * 2 : zero;
-          yinc[i] = ok ? (int64_t)G_KS * a.K * 2 : 0;
-        }
+      for (int i = 0; i < YN; ++i) {
+        const int row = (wave * YN + i) * 8 + (lane >> 3);
+        const bool ok = ld.c0 + row < a.N;
+        ys[i] = ok ? wb + ((int64_t)(ld.c0 + row) * a.K + ((lane & 7) ^ swz_k(row)) * 8) * 2 : zero;
+        yinc[i] = ok ? G_KS * 2 : 0;
       }
-    };
-    // wgrad: the step's row indices, one per lane (lane l: row wave*XN*XR + l mod (XN*XR)), loaded
-    // one step ahead; a row counts only if it exists in both matrices
-    int idx_d = -1, idx_x = -1, cur_d = -1, cur_x = -1;
-    auto load_idx = [&](int s) {
-      if constexpr (OP == OP_WGRAD) {
-        const int row = s * G_KS + wave * (XN * XR) + (lane & (XN * XR - 1));
-        const int p = p0 + min(row, cnt - 1);
-        const int md = (a.x0.map ? a.x0.map : a.offsets)[a.x0.map ? p : 0];
-        const int mx = (a.x1.map ? a.x1.map : a.offsets)[a.x1.map ? p : 0];
-        idx_d = a.x0.map ? md : p;
-        idx_x = a.x1.map ? mx : p;
-        if (row >= cnt) idx_d = -1;
+    } else if constexpr (OP == OP_DGRAD) {
+#pragma unroll
+      for (int i = 0; i < YN; ++i) {
+        const int row = (wave * YN + i) * YR + lane / YL;
+        const int col = ld.c0 + ((lane % YL) ^ swz_tr<BC>(row)) * 8;
+        const bool ok = col < a.K;
+        ys[i] = ok ? wb + ((int64_t)row * a.K + col) * 2 : zero;
+        yinc[i] = ok ? (int64_t)G_KS * a.K * 2 : 0;
       }
-    };
-    auto take_idx = [&]() {
-      const bool ok = (unsigned)idx_d < (unsigned)a.x0.rows && (unsigned)idx_x < (unsigned)a.x1.rows;
-      cur_d = ok ? idx_d : -1;
-      cur_x = ok ? idx_x : -1;
-    };
+    }
+  };
+  auto set_sources = [&]() {
+    set_x(a.x0);
+    set_y(a.w0);
+  };
 
-    // loads of step s into its stage (s counts through the item; a second operand pair follows the first)
-    auto issue = [&](int s) {
-      const uint32_t st = __builtin_amdgcn_readfirstlane(lds_offset(lds) + (s % NST) * ST_BYTES);
-      if constexpr (OP == OP_WGRAD) {
+  // loads of step `ls` of tile `ld` into the stage of global step g
+  auto issue = [&](int g) {
+    const uint32_t st = __builtin_amdgcn_readfirstlane(lds_offset(lds) + (g % NST) * ST_BYTES);
+    if constexpr (OP == OP_WGRAD) {
+      const int last = ld.p0 + ld.cnt - 1;
 #pragma unroll
-        for (int i = 0; i < XN; ++i) {
-          const int row = (wave * XN + i) * XR + lane / XL;
-          const int ch = (lane % XL) ^ swz_tr<BR>(row);
-          const int d = __shfl(cur_d, i * XR + lane / XL, 64), x = __shfl(cur_x, i * XR + lane / XL, 64);
-          const int cn = r0 + ch * 8, ck = c0 + ch * 8;
-          const char* pd = d >= 0 && cn < a.N ? (const char*)a.x0.data + ((int64_t)d * a.x0.ld + cn) * 2 : zero;
-          const char* px = x >= 0 && ck < a.K ? (const char*)a.x1.data + ((int64_t)x * a.x1.ld + ck) * 2 : zero;
-          dma16(pd, st + (wave * XN + i) * 1024);
-          dma16(px, st + X_BYTES + (wave * XN + i) * 1024);
-        }
-      } else {
-        if (OP == OP_DGRAD && s == steps1) {
-          set_x(a.x1);
-          set_y(a.w1);
-        }
-        const int k0 = (s >= steps1 ? s - steps1 : s) * G_KS;
-        const bool tail = k0 + G_KS > nred;
+      for (int i = 0; i < XN; ++i) {
+        const int row0 = (wave * XN + i) * XR, sub = lane / XL, row = row0 + sub;
+        const int p = ld.p0 + ls * G_KS + row0;
+        int d = p + sub, x = p + sub;
+        if (a.x0.map && ld.cnt > 0) d = mapped(a.x0, p, last, sub, XR);
+        if (a.x1.map && ld.cnt > 0) x = mapped(a.x1, p, last, sub, XR);
+        // a row counts only if it exists in both matrices
+        const bool ok = p + sub <= last && (unsigned)d < (unsigned)a.x0.rows && (unsigned)x < (unsigned)a.x1.rows;
+        const int ch = (lane % XL) ^ swz_tr<BR>(row);
+        const int cn = ld.r0 + ch * 8, ck = ld.c0 + ch * 8;
+        dma16(ok && cn < a.N ? (const char*)a.x0.data + ((int64_t)d * a.x0.ld + cn) * 2 : zero, st + (wave * XN + i) * 1024);
+        dma16(ok && ck < a.K ? (const char*)a.x1.data + ((int64_t)x * a.x1.ld + ck) * 2 : zero,
+              st + X_BYTES + (wave * XN + i) * 1024);
+      }
+    } else {
+      if (OP == OP_DGRAD && ls == ld.steps1) {  // the second operand pair
+        set_x(a.x1);
+        set_y(a.w1);
+      }
+      const int k0 = (ls >= ld.steps1 ? ls - ld.steps1 : ls) * G_KS;
+      const bool tail = k0 + G_KS > Red;
 #pragma unroll
-        for (int i = 0; i < XN; ++i) {
-          const char* p = xs[i];
-          if (tail) {
-            const int row = (wave * XN + i) * 8 + (lane >> 3);
-            if (k0 + ((lane & 7) ^ swz_k(row)) * 8 >= nred) p = zero;
+      for (int i = 0; i < XN; ++i) {
+        if (XN > 1 && i >= xn) break;
+        const char* p = xs[i];
+        if (tail) {
+          const int row = (i * NW + wave) * 8 + (lane >> 3);
+          if (k0 + ((lane & 7) ^ swz_k(row)) * 8 >= Red) p = zero;
+        }
+        dma16(p, st + (i * NW + wave) * 1024);
+        xs[i] += xinc[i];
+      }
+#pragma unroll
+      for (int i = 0; i < YN; ++i) {
+        const char* p = ys[i];
+        if (tail) {
+          if constexpr (OP == OP_FWD) {
+            const int row = (wave * YN + i) * 8 + (lane >> 3);
+            if (k0 + ((lane & 7) ^ swz_k(row)) * 8 >= Red) p = zero;
+          } else {
+            const int row = (wave * YN + i) * YR + lane / YL;
+            if (k0 + row >= Red) p = zero;
           }
-          dma16(p, st + (wave * XN + i) * 1024);
-          xs[i] += xinc[i];
         }
-#pragma unroll
-        for (int i = 0; i < YN; ++i) {
-          const char* p = ys[i];
-          if (tail) {
-            if constexpr (OP == OP_FWD) {
-              const int row = (wave * YN + i) * 8 + (lane >> 3);
-              if (k0 + ((lane & 7) ^ swz_k(row)) * 8 >= nred) p = zero;
-            } else {
-              const int row = (wave * YN + i) * YR + lane / YL;
-              if (k0 + row >= nred) p = zero;
-            }
-          }
-          dma16(p, st + X_BYTES + (wave * YN + i) * 1024);
-          ys[i] += yinc[i];
-        }
+        dma16(p, st + X_BYTES + (wave * YN + i) * 1024);
+        ys[i] += yinc[i];
       }
-    };
+    }
+  };
+  int issued = 0;        // steps whose loads have been issued
+  int xn_last = XN;      // row loads of the last of them
+  auto issue_next = [&]() {
+    if (!more) return;
+    if (ls == ld.nsteps) {
+      more = advance(ld);
+      if (!more) return;
+      ls = 0;
+      if constexpr (OP != OP_WGRAD) set_sources();
+    }
+    issue(issued);
+    xn_last = xn;
+    ++ls;
+    ++issued;
+  };
 
-    floatx4 acc[CJ][RJ];
+  floatx4 acc[CJ][RJ];
+  auto clear = [&]() {
 #pragma unroll
     for (int c = 0; c < CJ; ++c)
 #pragma unroll
       for (int r = 0; r < RJ; ++r) acc[c][r] = floatx4{0.f, 0.f, 0.f, 0.f};
+  };
+  clear();
 
-    auto compute = [&](int s) {
-      const uint8_t* st = lds + (s % NST) * ST_BYTES;
+  auto compute = [&](int g) {
+    const uint8_t* st = lds + (g % NST) * ST_BYTES;
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        u32x4 xf[RJ], yf[CJ];
+    for (int u = 0; u < 2; ++u) {
+      u32x4 xf[RJ], yf[CJ];
 #pragma unroll
-        for (int j = 0; j < RJ; ++j) {
-          if constexpr (XT) {
-            const u32x2 lo = lds_read_tr(st + xa[j] + u * 32 * BR * 2), hi = lds_read_tr(st + xa[j] + (u * 32 + 4) * BR * 2);
-            xf[j] = u32x4{lo[0], lo[1], hi[0], hi[1]};
-          } else {
-            xf[j] = *(const u32x4*)(st + xa[u] + j * 16 * 128);
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < CJ; ++j) {
-          if constexpr (YT) {
-            const u32x2 lo = lds_read_tr(st + ya[j] + u * 32 * BC * 2), hi = lds_read_tr(st + ya[j] + (u * 32 + 4) * BC * 2);
-            yf[j] = u32x4{lo[0], lo[1], hi[0], hi[1]};
-          } else {
-            yf[j] = *(const u32x4*)(st + ya[u] + j * 16 * 128);
-          }
-        }
-#pragma unroll
-        for (int c = 0; c < CJ; ++c)
-#pragma unroll
-          for (int r = 0; r < RJ; ++r) acc[c][r] = mfma16(yf[c], xf[r], acc[c][r]);
-      }
-    };
-
-    // ---- prologue: every wave has left the previous item's stages
-    lds_barrier();
-    if constexpr (OP != OP_WGRAD) {
-      set_x(a.x0);
-      set_y(a.w0);
-    }
-    if (nsteps > 0) {
-      load_idx(0);
-#pragma unroll
-      for (int s = 0; s < D; ++s) {
-        if (s < nsteps) {
-          take_idx();
-          load_idx(s + 1);
-          issue(s);
+      for (int j = 0; j < RJ; ++j) {
+        if constexpr (XT) {
+          const u32x2 lo = lds_read_tr(st + xa[j] + u * 32 * BR * 2), hi = lds_read_tr(st + xa[j] + (u * 32 + 4) * BR * 2);
+          xf[j] = u32x4{lo[0], lo[1], hi[0], hi[1]};
+        } else {
+          xf[j] = *(const u32x4*)(st + xa[u] + j * 16 * 128);
         }
       }
-    }
-    // ---- steps: wait until only the loads of the later steps are outstanding, meet the other
-    // waves (their loads of this stage are in, their reads of the stage to be refilled are done),
-    // refill, multiply
-    const bool live = OP == OP_WGRAD ? r0 + wr * RJ * 16 < a.N : r0 + wr * RJ * 16 < cnt;
-    for (int s = 0; s < nsteps; ++s) {
-      const int ahead = min(nsteps - 1 - s, D - 1);
-      if (ahead >= 2) wait_vmcnt<2 * NLOAD>();
-      else if (ahead == 1) wait_vmcnt<NLOAD>();
-      else wait_vmcnt<0>();
-      lds_barrier();
-      if (s + D < nsteps) {
-        take_idx();
-        load_idx(s + D + 1);
-        issue(s + D);
+#pragma unroll
+      for (int j = 0; j < CJ; ++j) {
+        if constexpr (YT) {
+          const u32x2 lo = lds_read_tr(st + ya[j] + u * 32 * BC * 2), hi = lds_read_tr(st + ya[j] + (u * 32 + 4) * BC * 2);
+          yf[j] = u32x4{lo[0], lo[1], hi[0], hi[1]};
+        } else {
+          yf[j] = *(const u32x4*)(st + ya[u] + j * 16 * 128);
+        }
       }
-      if (live) compute(s);
+#pragma unroll
+      for (int c = 0; c < CJ; ++c)
+#pragma unroll
+        for (int r = 0; r < RJ; ++r) acc[c][r] = mfma16(yf[c], xf[r], acc[c][r]);
     }
+  };
 
-    // ---- epilogue: lane holds columns c..c+3 of one output row
+  // lane holds columns c..c+3 of one output row
+  auto epilogue = [&]() {
 #pragma unroll
     for (int r = 0; r < RJ; ++r) {
-      const int row = r0 + (wr * RJ + r) * 16 + r16;
-      const bool rok = OP == OP_WGRAD ? row < a.N : row < cnt;
-      if (!rok) continue;
-      const int64_t ob = OP == OP_WGRAD ? ((int64_t)e * a.N + row) * a.K : (int64_t)(p0 + row) * a.ldo;
+      const int row = cw.r0 + (wr * RJ + r) * 16 + r16;
+      if (row >= (OP == OP_WGRAD ? a.N : cw.cnt)) continue;
+      const int64_t ob = OP == OP_WGRAD ? ((int64_t)cw.e * a.N + row) * a.K : (int64_t)(cw.p0 + row) * a.ldo;
 #pragma unroll
       for (int c = 0; c < CJ; ++c) {
-        const int col = c0 + (wc * CJ + c) * 16 + 4 * q;
+        const int col = cw.c0 + (wc * CJ + c) * 16 + 4 * q;
         if (col >= Cdim) continue;
         if constexpr (F32) {
           floatx4* o = (floatx4*)((float*)a.out + ob + col);
@@ -387,6 +424,38 @@ __global__ __launch_bounds__(WR* WC * 64, 2) void grouped_kernel(GroupedArgs a) 
               u32x2{f32x2_to_bf16x2(acc[c][r][0], acc[c][r][1]), f32x2_to_bf16x2(acc[c][r][2], acc[c][r][3])};
         }
       }
+    }
+  };
+
+  if constexpr (OP != OP_WGRAD) set_sources();
+#pragma unroll
+  for (int j = 0; j < D; ++j) issue_next();
+
+  // ---- steps: wait until only the loads of the later steps are outstanding (stores of an earlier
+  // tile, which may end out of order, only make the wait stricter), meet the other waves (their
+  // loads of this stage are in, their reads of the stage to be refilled are done), refill, multiply
+  int cs = 0;
+  for (int g = 0;; ++g) {
+    const int ahead = issued - g - 1;
+    if constexpr (OP == OP_WGRAD || XN == 1) {
+      if (ahead == D - 1) wait_vmcnt<(D - 1) * (XN + YN)>();
+      else wait_vmcnt<0>();
+    } else {
+      if (ahead == 0) wait_vmcnt<0>();
+      else if (xn_last == 1) wait_vmcnt<1 + YN>();
+      else if (xn_last == 2) wait_vmcnt<(XN < 2 ? XN : 2) + YN>();
+      else if (xn_last == 3) wait_vmcnt<(XN < 3 ? XN : 3) + YN>();
+      else wait_vmcnt<XN + YN>();
+    }
+    lds_barrier();
+    issue_next();
+    const bool live = OP == OP_WGRAD ? cw.r0 + wr * RJ * 16 < a.N : cw.r0 + wr * RJ * 16 < cw.cnt;
+    if (live) compute(g);
+    if (++cs == cw.nsteps) {
+      if (live) epilogue();
+      clear();
+      cs = 0;
+      if (!advance(cw)) break;
     }
   }
   wait_vmcnt<0>();  // no direct-to-LDS load may outlive the workgroup
@@ -420,14 +489,16 @@ int device_cu_count() {
 
 // Tiles: no group count is known on the host, only the number of positions and groups.
 hipError_t launch_grouped_rows(const GroupedArgs& a, bool dgrad, hipStream_t s) {
-  const int64_t nct = ((dgrad ? a.K : a.N) + 127) / 128;
+  const int cols = dgrad ? a.K : a.N;
   // at most one partial tile per group that holds a position
-  auto items = [&](int br) { return (a.rows / br + std::min<int64_t>(a.groups, a.rows)) * nct; };
-  if (a.rows <= (int64_t)24 * a.groups)
-    return dgrad ? run_grouped<OP_DGRAD, 32, 128, 1, 4, 3>(a, items(32), 2, s)
-                 : run_grouped<OP_FWD, 32, 128, 1, 4, 3>(a, items(32), 2, s);
-  return dgrad ? run_grouped<OP_DGRAD, 128, 128, 2, 2, 2>(a, items(128), 2, s)
-               : run_grouped<OP_FWD, 128, 128, 2, 2, 2>(a, items(128), 2, s);
+  auto items = [&](int br, int bc) { return (a.rows / br + std::min<int64_t>(a.groups, a.rows)) * ((cols + bc - 1) / bc); };
+#define MOE_GROUPED(BR, BC, WR, WC, NST, WGS)                                              \
+  return dgrad ? run_grouped<OP_DGRAD, BR, BC, WR, WC, NST>(a, items(BR, BC), WGS, s)      \
+               : run_grouped<OP_FWD, BR, BC, WR, WC, NST>(a, items(BR, BC), WGS, s)
+  if (items(32, 128) < device_cu_count()) MOE_GROUPED(32, 64, 1, 4, 8, 1);
+  if (a.rows <= (int64_t)24 * a.groups) MOE_GROUPED(32, 128, 1, 4, 3, 2);
+  MOE_GROUPED(256, 128, 4, 2, 3, 1);
+#undef MOE_GROUPED
 }
 
 hipError_t launch_grouped_wgrad(const GroupedArgs& a, hipStream_t s) {
