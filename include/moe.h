@@ -342,7 +342,7 @@ typedef enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_FP32 = 1 } moe_dtype_t;
 typedef struct {
   int32_t groups;         /* 1..1025 */
   int32_t out_features;   /* N: multiple of 8, at most 65536 */
-  int32_t in_features;    /* K: multiple of 8, at most 65536 */
+  int32_t in_features;    /* K: multiple of 8, at most 65536; N * K below 2^31 - 128 */
   int64_t rows;           /* positions; below 2^31 - 4096 */
   const int32_t* offsets; /* device [groups + 1], 4-byte aligned, not decreasing */
 } moe_groups_t;
@@ -353,7 +353,7 @@ typedef struct {
 typedef struct {
   const void* data;       /* device bf16, row stride ld; NULL only with rows 0 */
   int64_t rows;           /* rows of the matrix; with row_map NULL at least the positions */
-  int64_t ld;             /* values between rows: at least the columns, multiple of 8 */
+  int64_t ld;             /* values between rows: at least the columns, multiple of 8, at most 2^22 */
   const int32_t* row_map;
 } moe_rows_t;
 
@@ -367,7 +367,7 @@ moe_status_t moe_grouped_gemm(const moe_groups_t* groups, const moe_rows_t* x, c
                               int32_t y_dtype, int32_t accumulate, void* stream);
 
 /* Input gradient: dx[p] = dy[p] w_g (+ dy2[p] w2_g, both or neither), summed in fp32 and rounded
- * once.  dy, dy2 [.., out_features]; w, w2 as above; dx bf16 or fp32 [rows, in_features]. */
+ * once.  dy, dy2 [.., out_features], with the same rows, row stride and row map; w, w2 as above; dx bf16 or fp32 [rows, in_features]. */
 moe_status_t moe_grouped_gemm_dgrad(const moe_groups_t* groups, const moe_rows_t* dy, const void* w,
                                     const moe_rows_t* dy2, const void* w2, void* dx, int64_t lddx, int32_t dx_dtype,
                                     int32_t accumulate, void* stream);

@@ -18,15 +18,19 @@
 // lane order, so each lane picks the 16 bytes that belong in its slot), which spreads the rows of
 // one fragment read over all LDS banks.
 //
-// Masking is done by address: a lane whose row or column does not exist (ragged ends, rows outside
-// the matrix, sizes that fill no tile) loads 16 zero bytes from a constant, so no masked value is
-// ever read and an infinity or NaN outside the group cannot reach a sum.
+// Masking is done by address: the direct loads go through buffer descriptors, and a lane whose row
+// or column does not exist (ragged ends, rows outside the matrix, sizes that fill no tile) takes
+// an offset past the descriptor's end, for which the load writes zeros to LDS.  No masked value is
+// ever read, and an infinity or NaN outside the group cannot reach a sum.  Descriptors also keep
+// the address arithmetic off the vector units: a lane's offset in the tile stays, and the
+// descriptor's base moves from step to step.
 //
 // The workgroups are persistent and need no list from another kernel: each builds the prefix of
 // row tiles over the groups in LDS from `offsets`, and XCD x's workgroups walk the contiguous x-th
 // eighth of the tiles together, so tiles that share operand rows or weights run side by side in
 // one L2.
 #include <atomic>
+#include <utility>
 
 #include "moe_common.h"
 #include "moe_internal.h"
@@ -36,7 +40,6 @@ namespace moe {
 namespace {
 
 constexpr int OP_FWD = 0, OP_DGRAD = 1, OP_WGRAD = 2;
-constexpr int G_KS = 64;                 // reduction values per step
 constexpr int G_MAX_GROUPS = 1025;       // 1024 routed experts and a shared one
 
 __device__ __align__(16) const uint32_t grouped_zeros[4] = {0, 0, 0, 0};
@@ -51,6 +54,18 @@ __device__ __forceinline__ void dma16(const void* g, uint32_t lds_off) {
 }
 __device__ __forceinline__ uint32_t lds_offset(const void* p) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
+}
+
+// The same through a buffer descriptor of BUF_MAX bytes: an offset past its end gives zeros.
+constexpr uint32_t BUF_OUT = 0xFFFFFFF0u;
+constexpr int64_t BUF_MAX = 0xFFFFFF00ll;
+__device__ __forceinline__ u32x4 buffer_at(uint64_t base) {
+  return u32x4{(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)base),
+               (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(base >> 32)), (uint32_t)BUF_MAX, 0x00020000u};
+}
+__device__ __forceinline__ void dma16(uint32_t off, const u32x4& rsrc, uint32_t lds_off) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds_off), "v"(off), "s"(rsrc)
+               : "memory");
 }
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -79,7 +94,8 @@ __device__ __forceinline__ void wait_vmcnt() {
 // 16-byte chunk swizzles of an LDS row: rows of 64 reduction values (8 chunks), and rows of W
 // output values whose 32-byte blocks are read by the transposing load: one read touches rows
 // 8q..8q+3 (or 8q+4..8q+7) of lane groups q, told apart by bits 0, 1 and 3 of the row.
-__device__ __forceinline__ int swz_k(int row) { return (row >> 1) & 7; }
+template <int KS>
+__device__ __forceinline__ int swz_k(int row) { return KS == 64 ? (row >> 1) & 7 : (row >> 2) & 3; }
 template <int W>
 __device__ __forceinline__ int swz_tr(int row) {
   if constexpr (W >= 128) return ((row & 3) | ((row >> 1) & 4)) << 1;
@@ -87,20 +103,32 @@ __device__ __forceinline__ int swz_tr(int row) {
   return (((row >> 3) & 1)) << 1;                                            // 64-byte rows
 }
 
+// f(0) .. f(N-1), written out by the front end (a loop over registers that the optimiser unrolls
+// too late leaves them in memory)
+template <typename F, int... I>
+__device__ __forceinline__ void each_impl(F& f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void each(F f) {
+  each_impl(f, std::make_integer_sequence<int, N>{});
+}
+
 // Loads through the scalar data cache (uniform addresses of data the kernel never writes): they are
 // counted by lgkmcnt, so finding the next tile's rows never waits on the loads of the tiles' data.
 typedef const __attribute__((address_space(4))) int32_t* sptr;
 
-template <int OP, int BR, int BC, int WR, int WC, int NST, bool F32>
-__global__ __launch_bounds__(WR* WC * 64, (WR * WC == 4 && NST * (BR + BC) * G_KS * 2 > 72 * 1024) ? 1 : 2) void grouped_kernel(GroupedArgs a) {
+template <int OP, int KS, int BR, int BC, int WR, int WC, int NST, bool F32>
+__global__ __launch_bounds__(WR* WC * 64, (WR * WC == 4 && NST * (BR + BC) * KS * 2 > 72 * 1024) ? 1 : 2) void grouped_kernel(GroupedArgs a) {
   constexpr bool XT = OP == OP_WGRAD, YT = OP != OP_FWD;  // operands read through the transposing load
   constexpr int NW = WR * WC;
-  constexpr int X_BYTES = BR * G_KS * 2, Y_BYTES = BC * G_KS * 2, ST_BYTES = X_BYTES + Y_BYTES;
+  constexpr int X_BYTES = BR * KS * 2, Y_BYTES = BC * KS * 2, ST_BYTES = X_BYTES + Y_BYTES;
   constexpr int XN = X_BYTES / (NW * 1024), YN = Y_BYTES / (NW * 1024);  // loads per wave and step
   static_assert(XN * NW * 1024 == X_BYTES && YN * NW * 1024 == Y_BYTES, "a stage must split evenly over the waves");
   static_assert(OP != OP_WGRAD || BR == BC, "both operands of wgrad share their row indices");
   constexpr int D = NST - 1;  // steps in flight
-  static_assert(XN == 1 || OP == OP_WGRAD || D <= 2, "the load counts of at most one later step are told apart");
+  constexpr int KB = KS * 2, KC = KS / 8;  // bytes and 16-byte chunks of a row of reduction values
+  constexpr int KR = 64 / KC;              // such rows per load
   constexpr int RJ = BR / WR / 16, CJ = BC / WC / 16;
   static_assert(RJ * WR * 16 == BR && CJ * WC * 16 == BC, "wave tiles of 16");
   // lanes per LDS row and rows per load of a transposed operand
@@ -155,7 +183,7 @@ __global__ __launch_bounds__(WR* WC * 64, (WR * WC == 4 && NST * (BR + BC) * G_K
 
   // ---- LDS read addresses, constant per lane
   // row-major operand: row j*16 + r16, chunk (4u + q); transposed: block cb of 16 columns
-  int xa[XT ? RJ : 2], ya[YT ? CJ : 2];
+  int xa[XT ? RJ : KS / 32], ya[YT ? CJ : KS / 32];
   if constexpr (XT) {
     const int row = 8 * q + (r16 >> 2);
 #pragma unroll
@@ -163,7 +191,7 @@ __global__ __launch_bounds__(WR* WC * 64, (WR * WC == 4 && NST * (BR + BC) * G_K
       xa[j] = row * BR * 2 + ((((wr * RJ + j) * 2) ^ swz_tr<BR>(row)) << 4) + (r16 & 3) * 8;
   } else {
 #pragma unroll
-    for (int u = 0; u < 2; ++u) xa[u] = (wr * RJ * 16 + r16) * 128 + (((4 * u + q) ^ swz_k(r16)) << 4);
+    for (int u = 0; u < KS / 32; ++u) xa[u] = (wr * RJ * 16 + r16) * KB + (((4 * u + q) ^ swz_k<KS>(r16)) << 4);
   }
   if constexpr (YT) {
     const int row = 8 * q + (r16 >> 2);
@@ -172,7 +200,7 @@ __global__ __launch_bounds__(WR* WC * 64, (WR * WC == 4 && NST * (BR + BC) * G_K
       ya[j] = X_BYTES + row * BC * 2 + ((((wc * CJ + j) * 2) ^ swz_tr<BC>(row)) << 4) + (r16 & 3) * 8;
   } else {
 #pragma unroll
-    for (int u = 0; u < 2; ++u) ya[u] = X_BYTES + (wc * CJ * 16 + r16) * 128 + (((4 * u + q) ^ swz_k(r16)) << 4);
+    for (int u = 0; u < KS / 32; ++u) ya[u] = X_BYTES + (wc * CJ * 16 + r16) * KB + (((4 * u + q) ^ swz_k<KS>(r16)) << 4);
   }
 
   // ---- this workgroup's tiles.  The loads run D steps ahead of the products, across tiles, so
@@ -203,7 +231,7 @@ __global__ __launch_bounds__(WR* WC * 64, (WR * WC == 4 && NST * (BR + BC) * G_K
     w.cnt = max(min(offsets[w.e + 1], a.rows) - w.p0, 0);
     w.c0 = w.ct * BC;
     // an empty group's gradient is one step of zeros
-    w.steps1 = OP == OP_WGRAD ? max((w.cnt + G_KS - 1) / G_KS, 1) : (Red + G_KS - 1) / G_KS;
+    w.steps1 = OP == OP_WGRAD ? max((w.cnt + KS - 1) / KS, 1) : (Red + KS - 1) / KS;
     w.nsteps = (OP == OP_DGRAD && a.w1) ? 2 * w.steps1 : w.steps1;
   };
   auto advance = [&](Walk& w) -> bool {
@@ -233,137 +261,179 @@ __global__ __launch_bounds__(WR* WC * 64, (WR * WC == 4 && NST * (BR + BC) * G_K
   int ls = 0;    // next step to load of tile `ld`
   bool more = true;
 
-  // ---- load sources
-  const char* xs[XN];
-  const char* ys[YN];
-  int xinc[XN];
-  int64_t yinc[YN];
-  int xn = XN;  // row loads that hold a row of the tile
+  // ---- load sources: descriptor bases that move with the steps, offsets that stay for the tile
+  uint64_t xb = 0, yb = 0;
+  int64_t xstep = 0, ystep = 0;
+  uint32_t xo[XN], yo[YN];
+  const char* xs[XN];  // a mapped matrix of more than BUF_MAX bytes: 64-bit addresses per lane
+  int xn = XN;         // row loads that hold a row of the tile
+  int left = 0;        // reduction values from step `ls` on
   const char* const zero = (const char*)grouped_zeros;
-  // eight consecutive rows of a load: lane's row (lane / 8) of positions p.., through the map
-  auto mapped = [&](const RowsArg& m, int p, int last, int sub, int n) {
+  auto wide = [&](const RowsArg& m) { return m.map && (int64_t)m.rows * m.ld * 2 > BUF_MAX; };
+  const bool wide0 = wide(a.x0), wide1 = OP == OP_WGRAD && wide(a.x1);
+  // the n consecutive rows of a load: row `sub` of positions p.., through the map
+  auto mapped = [&](const RowsArg& m, int p, int last, int sub, auto n) {
     int src = 0;
     const sptr map = (sptr)m.map;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      if (k >= n) break;
+    each<decltype(n)::value>([&](auto k) {
       const int t = map[min(p + k, last)];
       src = sub == k ? t : src;
-    }
+    });
     return src;
   };
-  auto set_x = [&](const RowsArg& m) {  // row-major operand of the rows; load i holds rows i*NW*8 + wave*8 ..
+  auto set_x = [&](const RowsArg& m) {  // row-major operand of the rows; load i holds rows (i*NW + wave)*KR ..
     if constexpr (!XT) {
       const int n = ld.cnt - ld.r0;
-      xn = min((n + NW * 8 - 1) / (NW * 8), XN);
-#pragma unroll
-      for (int i = 0; i < XN; ++i) {
-        const int row0 = (i * NW + wave) * 8, row = row0 + (lane >> 3);
-        const int p = ld.p0 + ld.r0 + row0;
-        int src = p + (lane >> 3);
-        if (m.map && row0 < n) src = mapped(m, p, ld.p0 + ld.cnt - 1, lane >> 3, 8);
-        const bool ok = row < n && (unsigned)src < (unsigned)m.rows;
-        const int ch = (lane & 7) ^ swz_k(row);
-        xs[i] = ok ? (const char*)m.data + ((int64_t)src * m.ld + ch * 8) * 2 : zero;
-        xinc[i] = ok ? G_KS * 2 : 0;
-      }
+      xn = min((n + NW * KR - 1) / (NW * KR), XN);
+      xb = (uint64_t)m.data + (m.map ? 0 : (int64_t)(ld.p0 + ld.r0) * m.ld * 2);
+      xstep = KB;
+      each<XN>([&](auto i) {
+        const int row0 = (i * NW + wave) * KR, row = row0 + lane / KC;
+        const int ch = (lane % KC) ^ swz_k<KS>(row);
+        // (one store to each array: stores that branches share would keep the arrays in memory)
+        uint32_t o = (uint32_t)row * (uint32_t)(m.ld * 2) + ch * 16;
+        bool ok = row < n;
+        const char* ptr = zero;
+        if (m.map) {
+          int src = -1;
+          if (row0 < n) src = mapped(m, ld.p0 + ld.r0 + row0, ld.p0 + ld.cnt - 1, lane / KC, std::integral_constant<int, KR>{});
+          ok = ok && (unsigned)src < (unsigned)m.rows;
+          o = (uint32_t)src * (uint32_t)(m.ld * 2) + ch * 16;
+          if (wide0 && ok) ptr = (const char*)m.data + ((int64_t)src * m.ld + ch * 8) * 2;
+        }
+        xo[i] = ok ? o : BUF_OUT;
+        xs[i] = ptr;
+      });
     }
   };
   auto set_y = [&](const uint16_t* w) {  // the group's weights
-    const char* wb = (const char*)(w + (int64_t)ld.e * a.N * a.K);
+    yb = (uint64_t)(w + (int64_t)ld.e * a.N * a.K);
     if constexpr (OP == OP_FWD) {
-#pragma unroll
-      for (int i = 0; i < YN; ++i) {
-        const int row = (wave * YN + i) * 8 + (lane >> 3);
-        const bool ok = ld.c0 + row < a.N;
-        ys[i] = ok ? wb + ((int64_t)(ld.c0 + row) * a.K + ((lane & 7) ^ swz_k(row)) * 8) * 2 : zero;
-        yinc[i] = ok ? G_KS * 2 : 0;
-      }
+      yb += (int64_t)ld.c0 * a.K * 2;
+      ystep = KB;
+      each<YN>([&](auto i) {
+        const int row = (wave * YN + i) * KR + lane / KC;
+        yo[i] = ld.c0 + row < a.N ? (uint32_t)row * (uint32_t)(a.K * 2) + ((lane % KC) ^ swz_k<KS>(row)) * 16 : BUF_OUT;
+      });
     } else if constexpr (OP == OP_DGRAD) {
-#pragma unroll
-      for (int i = 0; i < YN; ++i) {
+      yb += (int64_t)ld.c0 * 2;
+      ystep = (int64_t)KS * a.K * 2;
+      each<YN>([&](auto i) {
         const int row = (wave * YN + i) * YR + lane / YL;
-        const int col = ld.c0 + ((lane % YL) ^ swz_tr<BC>(row)) * 8;
-        const bool ok = col < a.K;
-        ys[i] = ok ? wb + ((int64_t)row * a.K + col) * 2 : zero;
-        yinc[i] = ok ? (int64_t)G_KS * a.K * 2 : 0;
-      }
+        const int col = ((lane % YL) ^ swz_tr<BC>(row)) * 8;
+        yo[i] = ld.c0 + col < a.K ? (uint32_t)row * (uint32_t)(a.K * 2) + col * 2 : BUF_OUT;
+      });
     }
   };
   auto set_sources = [&]() {
-    set_x(a.x0);
-    set_y(a.w0);
+    if constexpr (OP == OP_WGRAD) {
+      left = ld.cnt;
+      xb = (uint64_t)a.x0.data + ld.r0 * 2 + (a.x0.map ? 0 : (int64_t)ld.p0 * a.x0.ld * 2);
+      xstep = a.x0.map ? 0 : KS * a.x0.ld * 2;
+      yb = (uint64_t)a.x1.data + ld.c0 * 2 + (a.x1.map ? 0 : (int64_t)ld.p0 * a.x1.ld * 2);
+      ystep = a.x1.map ? 0 : KS * a.x1.ld * 2;
+      each<XN>([&](auto i) {
+        const int row = (wave * XN + i) * XR + lane / XL, ch = (lane % XL) ^ swz_tr<BR>(row);
+        xo[i] = ld.r0 + ch * 8 < a.N ? (uint32_t)row * (uint32_t)(a.x0.ld * 2) + ch * 16 : BUF_OUT;
+        yo[i] = ld.c0 + ch * 8 < a.K ? (uint32_t)row * (uint32_t)(a.x1.ld * 2) + ch * 16 : BUF_OUT;
+      });
+    } else {
+      left = Red;
+      set_x(a.x0);
+      set_y(a.w0);
+    }
   };
 
-  // loads of step `ls` of tile `ld` into the stage of global step g
-  auto issue = [&](int g) {
-    const uint32_t st = __builtin_amdgcn_readfirstlane(lds_offset(lds) + (g % NST) * ST_BYTES);
+  // loads of step `ls` of tile `ld` into the stage at LDS offset st
+  auto issue = [&](uint32_t st) {
     if constexpr (OP == OP_WGRAD) {
-      const int last = ld.p0 + ld.cnt - 1;
-#pragma unroll
-      for (int i = 0; i < XN; ++i) {
-        const int row0 = (wave * XN + i) * XR, sub = lane / XL, row = row0 + sub;
-        const int p = ld.p0 + ls * G_KS + row0;
-        int d = p + sub, x = p + sub;
-        if (a.x0.map && ld.cnt > 0) d = mapped(a.x0, p, last, sub, XR);
-        if (a.x1.map && ld.cnt > 0) x = mapped(a.x1, p, last, sub, XR);
+      const u32x4 xr = buffer_at(xb), yr = buffer_at(yb);
+      const uint32_t xt = st + wave * XN * 1024;
+      if (!a.x0.map && !a.x1.map) {
+        if (left >= KS) {
+          each<XN>([&](auto i) {
+            dma16(xo[i], xr, xt + i * 1024);
+            dma16(yo[i], yr, xt + X_BYTES + i * 1024);
+          });
+        } else {
+          each<XN>([&](auto i) {
+            const bool ok = (wave * XN + i) * XR + lane / XL < left;
+            dma16(ok ? xo[i] : BUF_OUT, xr, xt + i * 1024);
+            dma16(ok ? yo[i] : BUF_OUT, yr, xt + X_BYTES + i * 1024);
+          });
+        }
+      } else {
         // a row counts only if it exists in both matrices
-        const bool ok = p + sub <= last && (unsigned)d < (unsigned)a.x0.rows && (unsigned)x < (unsigned)a.x1.rows;
-        const int ch = (lane % XL) ^ swz_tr<BR>(row);
-        const int cn = ld.r0 + ch * 8, ck = ld.c0 + ch * 8;
-        dma16(ok && cn < a.N ? (const char*)a.x0.data + ((int64_t)d * a.x0.ld + cn) * 2 : zero, st + (wave * XN + i) * 1024);
-        dma16(ok && ck < a.K ? (const char*)a.x1.data + ((int64_t)x * a.x1.ld + ck) * 2 : zero,
-              st + X_BYTES + (wave * XN + i) * 1024);
+        const int last = ld.p0 + ld.cnt - 1;
+        each<XN>([&](auto i) {
+          const int row0 = (wave * XN + i) * XR, sub = lane / XL, row = row0 + sub;
+          const int p = ld.p0 + ls * KS + row0;
+          int d = 0, x = 0;
+          if (a.x0.map && ld.cnt > 0) d = mapped(a.x0, p, last, sub, std::integral_constant<int, XR>{});
+          if (a.x1.map && ld.cnt > 0) x = mapped(a.x1, p, last, sub, std::integral_constant<int, XR>{});
+          const bool ok = p + sub <= last && (unsigned)d < (unsigned)a.x0.rows && (unsigned)x < (unsigned)a.x1.rows;
+          const int ch = (lane % XL) ^ swz_tr<BR>(row);
+          const bool okd = ok && xo[i] != BUF_OUT, okx = ok && yo[i] != BUF_OUT;
+          const uint32_t od = a.x0.map ? (uint32_t)d * (uint32_t)(a.x0.ld * 2) + ch * 16 : xo[i];
+          const uint32_t ox = a.x1.map ? (uint32_t)x * (uint32_t)(a.x1.ld * 2) + ch * 16 : yo[i];
+          if (wide0) dma16(okd ? (const char*)a.x0.data + ((int64_t)d * a.x0.ld + ld.r0 + ch * 8) * 2 : zero, xt + i * 1024);
+          else dma16(okd ? od : BUF_OUT, xr, xt + i * 1024);
+          if (wide1) dma16(okx ? (const char*)a.x1.data + ((int64_t)x * a.x1.ld + ld.c0 + ch * 8) * 2 : zero, xt + X_BYTES + i * 1024);
+          else dma16(okx ? ox : BUF_OUT, yr, xt + X_BYTES + i * 1024);
+        });
       }
     } else {
       if (OP == OP_DGRAD && ls == ld.steps1) {  // the second operand pair
+        left = Red;
         set_x(a.x1);
         set_y(a.w1);
       }
-      const int k0 = (ls >= ld.steps1 ? ls - ld.steps1 : ls) * G_KS;
-      const bool tail = k0 + G_KS > Red;
-#pragma unroll
-      for (int i = 0; i < XN; ++i) {
-        if (XN > 1 && i >= xn) break;
-        const char* p = xs[i];
-        if (tail) {
-          const int row = (i * NW + wave) * 8 + (lane >> 3);
-          if (k0 + ((lane & 7) ^ swz_k(row)) * 8 >= Red) p = zero;
-        }
-        dma16(p, st + (i * NW + wave) * 1024);
-        xs[i] += xinc[i];
-      }
-#pragma unroll
-      for (int i = 0; i < YN; ++i) {
-        const char* p = ys[i];
-        if (tail) {
-          if constexpr (OP == OP_FWD) {
-            const int row = (wave * YN + i) * 8 + (lane >> 3);
-            if (k0 + ((lane & 7) ^ swz_k(row)) * 8 >= Red) p = zero;
-          } else {
-            const int row = (wave * YN + i) * YR + lane / YL;
-            if (k0 + row >= Red) p = zero;
+      const u32x4 xr = buffer_at(xb), yr = buffer_at(yb);
+      const uint32_t xt = st + wave * 1024, yt = st + X_BYTES + wave * YN * 1024;
+      if (!wide0 && left >= KS) {
+        each<XN>([&](auto i) {
+          if (XN == 1 || i < xn) dma16(xo[i], xr, xt + i * NW * 1024);
+        });
+        each<YN>([&](auto i) { dma16(yo[i], yr, yt + i * 1024); });
+      } else {
+        // the last step of a reduction that is no multiple of KS: what follows in memory is the next
+        // row, or the next group
+        each<XN>([&](auto i) {
+          if (XN == 1 || i < xn) {
+            const int row = (i * NW + wave) * KR + lane / KC;
+            const bool past = ((lane % KC) ^ swz_k<KS>(row)) * 8 >= left;
+            if (wide0) dma16(past || xs[i] == zero ? zero : xs[i] + (Red - left) * 2, xt + i * NW * 1024);
+            else dma16(past ? BUF_OUT : xo[i], xr, xt + i * NW * 1024);
           }
-        }
-        dma16(p, st + X_BYTES + (wave * YN + i) * 1024);
-        ys[i] += yinc[i];
+        });
+        each<YN>([&](auto i) {
+          const int row = OP == OP_FWD ? (wave * YN + i) * KR + lane / KC : (wave * YN + i) * YR + lane / YL;
+          const bool past = (OP == OP_FWD ? ((lane % KC) ^ swz_k<KS>(row)) * 8 : row) >= left;
+          dma16(past ? BUF_OUT : yo[i], yr, yt + i * 1024);
+        });
       }
     }
+    left -= KS;
+    xb += xstep;
+    yb += ystep;
   };
-  int issued = 0;        // steps whose loads have been issued
-  int xn_last = XN;      // row loads of the last of them
+  const uint32_t lds0 = lds_offset(lds);
+  uint32_t lst = lds0;  // stage of the next step to load
+  int flying = 0;       // steps loaded or in flight and not yet computed
+  int n_last = 0;       // loads of the last of them
   auto issue_next = [&]() {
     if (!more) return;
     if (ls == ld.nsteps) {
       more = advance(ld);
       if (!more) return;
       ls = 0;
-      if constexpr (OP != OP_WGRAD) set_sources();
+      set_sources();
     }
-    issue(issued);
-    xn_last = xn;
+    issue(__builtin_amdgcn_readfirstlane(lst));
+    lst = lst == lds0 + (NST - 1) * ST_BYTES ? lds0 : lst + ST_BYTES;
+    n_last = xn;
     ++ls;
-    ++issued;
+    ++flying;
   };
 
   floatx4 acc[CJ][RJ];
@@ -375,10 +445,9 @@ __global__ __launch_bounds__(WR* WC * 64, (WR * WC == 4 && NST * (BR + BC) * G_K
   };
   clear();
 
-  auto compute = [&](int g) {
-    const uint8_t* st = lds + (g % NST) * ST_BYTES;
+  auto compute = [&](const uint8_t* st) {
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int u = 0; u < KS / 32; ++u) {
       u32x4 xf[RJ], yf[CJ];
 #pragma unroll
       for (int j = 0; j < RJ; ++j) {
@@ -386,7 +455,7 @@ __global__ __launch_bounds__(WR* WC * 64, (WR * WC == 4 && NST * (BR + BC) * G_K
           const u32x2 lo = lds_read_tr(st + xa[j] + u * 32 * BR * 2), hi = lds_read_tr(st + xa[j] + (u * 32 + 4) * BR * 2);
           xf[j] = u32x4{lo[0], lo[1], hi[0], hi[1]};
         } else {
-          xf[j] = *(const u32x4*)(st + xa[u] + j * 16 * 128);
+          xf[j] = *(const u32x4*)(st + xa[u] + j * 16 * KB);
         }
       }
 #pragma unroll
@@ -395,7 +464,7 @@ __global__ __launch_bounds__(WR* WC * 64, (WR * WC == 4 && NST * (BR + BC) * G_K
           const u32x2 lo = lds_read_tr(st + ya[j] + u * 32 * BC * 2), hi = lds_read_tr(st + ya[j] + (u * 32 + 4) * BC * 2);
           yf[j] = u32x4{lo[0], lo[1], hi[0], hi[1]};
         } else {
-          yf[j] = *(const u32x4*)(st + ya[u] + j * 16 * 128);
+          yf[j] = *(const u32x4*)(st + ya[u] + j * 16 * KB);
         }
       }
 #pragma unroll
@@ -427,30 +496,33 @@ __global__ __launch_bounds__(WR* WC * 64, (WR * WC == 4 && NST * (BR + BC) * G_K
     }
   };
 
-  if constexpr (OP != OP_WGRAD) set_sources();
+  set_sources();
 #pragma unroll
   for (int j = 0; j < D; ++j) issue_next();
 
   // ---- steps: wait until only the loads of the later steps are outstanding (stores of an earlier
   // tile, which may end out of order, only make the wait stricter), meet the other waves (their
   // loads of this stage are in, their reads of the stage to be refilled are done), refill, multiply
-  int cs = 0;
-  for (int g = 0;; ++g) {
-    const int ahead = issued - g - 1;
-    if constexpr (OP == OP_WGRAD || XN == 1) {
-      if (ahead == D - 1) wait_vmcnt<(D - 1) * (XN + YN)>();
-      else wait_vmcnt<0>();
+  int cs = 0, stage = 0;
+  for (;;) {
+    --flying;
+    if (flying < D - 1) {  // the end: at most D - 1 of these waits in a launch
+      wait_vmcnt<0>();
+    } else if constexpr (OP == OP_WGRAD || XN == 1) {
+      wait_vmcnt<(D - 1) * (XN + YN)>();
     } else {
-      if (ahead == 0) wait_vmcnt<0>();
-      else if (xn_last == 1) wait_vmcnt<1 + YN>();
-      else if (xn_last == 2) wait_vmcnt<(XN < 2 ? XN : 2) + YN>();
-      else if (xn_last == 3) wait_vmcnt<(XN < 3 ? XN : 3) + YN>();
-      else wait_vmcnt<XN + YN>();
+      static_assert(OP == OP_WGRAD || XN == 1 || (D <= 2 && XN <= 4), "counts of one later step");
+      if (D == 1) wait_vmcnt<0>();
+      else if (n_last >= 4) wait_vmcnt<(XN < 4 ? XN : 4) + YN>();
+      else if (n_last == 3) wait_vmcnt<(XN < 3 ? XN : 3) + YN>();
+      else if (n_last == 2) wait_vmcnt<(XN < 2 ? XN : 2) + YN>();
+      else wait_vmcnt<1 + YN>();
     }
     lds_barrier();
     issue_next();
     const bool live = OP == OP_WGRAD ? cw.r0 + wr * RJ * 16 < a.N : cw.r0 + wr * RJ * 16 < cw.cnt;
-    if (live) compute(g);
+    if (live) compute(lds + stage);
+    stage = stage == (NST - 1) * ST_BYTES ? 0 : stage + ST_BYTES;
     if (++cs == cw.nsteps) {
       if (live) epilogue();
       clear();
@@ -461,16 +533,16 @@ __global__ __launch_bounds__(WR* WC * 64, (WR * WC == 4 && NST * (BR + BC) * G_K
   wait_vmcnt<0>();  // no direct-to-LDS load may outlive the workgroup
 }
 
-template <int OP, int BR, int BC, int WR, int WC, int NST>
+template <int OP, int KS, int BR, int BC, int WR, int WC, int NST>
 hipError_t run_grouped(const GroupedArgs& a, int64_t max_items, int wg_per_cu, hipStream_t s) {
   const int cus = device_cu_count();
   if (cus <= 0) return hipErrorInvalidDevice;
   const int64_t grid = std::min<int64_t>((int64_t)(cus / 8 * 8) * wg_per_cu, (max_items + 7) / 8 * 8);
   if (grid <= 0) return hipSuccess;
   if (a.out_f32)
-    hipLaunchKernelGGL((grouped_kernel<OP, BR, BC, WR, WC, NST, true>), dim3((unsigned)grid), dim3(WR * WC * 64), 0, s, a);
+    hipLaunchKernelGGL((grouped_kernel<OP, KS, BR, BC, WR, WC, NST, true>), dim3((unsigned)grid), dim3(WR * WC * 64), 0, s, a);
   else
-    hipLaunchKernelGGL((grouped_kernel<OP, BR, BC, WR, WC, NST, false>), dim3((unsigned)grid), dim3(WR * WC * 64), 0, s, a);
+    hipLaunchKernelGGL((grouped_kernel<OP, KS, BR, BC, WR, WC, NST, false>), dim3((unsigned)grid), dim3(WR * WC * 64), 0, s, a);
   return hipGetLastError();
 }
 
@@ -492,18 +564,21 @@ hipError_t launch_grouped_rows(const GroupedArgs& a, bool dgrad, hipStream_t s) 
   const int cols = dgrad ? a.K : a.N;
   // at most one partial tile per group that holds a position
   auto items = [&](int br, int bc) { return (a.rows / br + std::min<int64_t>(a.groups, a.rows)) * ((cols + bc - 1) / bc); };
-#define MOE_GROUPED(BR, BC, WR, WC, NST, WGS)                                              \
-  return dgrad ? run_grouped<OP_DGRAD, BR, BC, WR, WC, NST>(a, items(BR, BC), WGS, s)      \
-               : run_grouped<OP_FWD, BR, BC, WR, WC, NST>(a, items(BR, BC), WGS, s)
-  if (items(32, 128) < device_cu_count()) MOE_GROUPED(32, 64, 1, 4, 8, 1);
-  if (a.rows <= (int64_t)24 * a.groups) MOE_GROUPED(32, 128, 1, 4, 3, 2);
-  MOE_GROUPED(256, 128, 4, 2, 3, 1);
+#define MOE_GROUPED(KS, BR, BC, WR, WC, NST, WGS)                                              \
+  return dgrad ? run_grouped<OP_DGRAD, KS, BR, BC, WR, WC, NST>(a, items(BR, BC), WGS, s)      \
+               : run_grouped<OP_FWD, KS, BR, BC, WR, WC, NST>(a, items(BR, BC), WGS, s)
+  const char* v = getenv("GV");
+  if (v && *v == '3') MOE_GROUPED(64, 128, 128, 2, 2, 2, 2);
+  if (v && *v == '5') MOE_GROUPED(64, 128, 256, 2, 4, 3, 1);
+  if (items(32, 128) < device_cu_count()) MOE_GROUPED(64, 32, 64, 1, 4, 8, 1);
+  if (a.rows <= (int64_t)24 * a.groups) MOE_GROUPED(64, 32, 128, 1, 4, 3, 2);
+  MOE_GROUPED(64, 256, 128, 4, 2, 3, 1);
 #undef MOE_GROUPED
 }
 
 hipError_t launch_grouped_wgrad(const GroupedArgs& a, hipStream_t s) {
   const int64_t items = (int64_t)a.groups * ((a.N + 127) / 128) * ((a.K + 127) / 128);
-  return run_grouped<OP_WGRAD, 128, 128, 2, 2, 2>(a, items, 2, s);
+  return run_grouped<OP_WGRAD, 64, 128, 128, 2, 2, 2>(a, items, 2, s);
 }
 
 }  // namespace moe

@@ -48,6 +48,7 @@ moe_status_t need_opt(const void* p, const char* name, uintptr_t align) {
 }
 
 constexpr int64_t MAX_ROWS = ((int64_t)1 << 31) - 1;
+constexpr int64_t MAX_LD = (int64_t)1 << 22;  // a tile's rows stay within a 32-bit offset
 constexpr int32_t MAX_FEATURES = 65536, MAX_GROUPS = 1025;
 
 // address range of a row-major matrix
@@ -67,7 +68,7 @@ moe_status_t apart(const Span& out, const Span& in) {
 moe_status_t check_ld(int64_t ld, int64_t cols, const char* name) {
   if (ld < cols) return fail(MOE_ERR_INVALID_ARG, "%s: row stride %lld is below the %lld columns", name, (long long)ld, (long long)cols);
   if (ld % 8) return fail(MOE_ERR_UNSUPPORTED, "%s: row stride %lld is not a multiple of 8", name, (long long)ld);
-  if (ld > ((int64_t)1 << 31)) return fail(MOE_ERR_UNSUPPORTED, "%s: row stride %lld is too large", name, (long long)ld);
+  if (ld > MAX_LD) return fail(MOE_ERR_UNSUPPORTED, "%s: row stride %lld is too large", name, (long long)ld);
   return MOE_OK;
 }
 
@@ -81,6 +82,8 @@ moe_status_t check_groups(const moe_groups_t* g) {
     return fail(MOE_ERR_UNSUPPORTED, "out_features %d and in_features %d must be multiples of 8", g->out_features, g->in_features);
   if (g->out_features > MAX_FEATURES || g->in_features > MAX_FEATURES)
     return fail(MOE_ERR_UNSUPPORTED, "out_features %d or in_features %d is above %d", g->out_features, g->in_features, MAX_FEATURES);
+  if ((int64_t)g->out_features * g->in_features >= (int64_t)0x7FFFFF80)
+    return fail(MOE_ERR_UNSUPPORTED, "weights of %d x %d values are above 4 GiB a group", g->out_features, g->in_features);
   if (g->rows < 0) return fail(MOE_ERR_INVALID_ARG, "rows = %lld must be >= 0", (long long)g->rows);
   // the tiles of a partial last row may step past the last position
   if (g->rows > MAX_ROWS - 4096) return fail(MOE_ERR_UNSUPPORTED, "rows = %lld is too large for 32-bit positions", (long long)g->rows);
@@ -123,6 +126,8 @@ moe_status_t grouped_rows(bool dgrad, const moe_groups_t* g, const moe_rows_t* x
   MOE_TRY(need(w, "w"));
   if (x2) {
     MOE_TRY(check_rows(g, x2, red, "dy2"));
+    if (x2->row_map != x->row_map || x2->rows != x->rows || x2->ld != x->ld)
+      return fail(MOE_ERR_INVALID_ARG, "dy and dy2 must have the same rows, row stride and row map");
     MOE_TRY(need(w2, "w2"));
   }
   MOE_TRY(check_out(dtype, accumulate, out, on));

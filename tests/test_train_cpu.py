@@ -75,6 +75,9 @@ def wgrad(g=None, dy=None, x=None, dw=at(3), dtype=0, acc=0):
     (lambda: dgrad(dy2=rows(5, 64)), INVALID, b"together"),
     (lambda: dgrad(w2=at(6)), INVALID, b"together"),
     (lambda: dgrad(dy2=rows(5, 64, ld=8), w2=at(6)), INVALID, b"dy2"),
+    (lambda: dgrad(dy2=rows(5, 64, ld=72), w2=at(6)), INVALID, b"same rows, row stride and row map"),
+    (lambda: forward(groups(out_features=65536, in_features=32768)), UNSUPPORTED, b"4 GiB"),
+    (lambda: forward(x=rows(1, 128, ld=(1 << 22) + 8)), UNSUPPORTED, b"row stride"),
     (lambda: dgrad(dy2=rows(5, 64), w2=at(6), dx=at(6)), INVALID, b"dx overlaps w2"),
     (lambda: wgrad(x=rows(2, 128, rows=50)), INVALID, b"x: 50 rows"),
     (lambda: wgrad(dw=at(2)), INVALID, b"dw overlaps x"),

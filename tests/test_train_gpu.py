@@ -399,3 +399,30 @@ def test_adamw_rounding_is_unbiased():
     for start, g in ((0, 1.0), (1, 0.25)):
         want = g * (1 - betas[0] ** steps)
         assert abs(out[start::2].double().mean().item() / want - 1) < 0.02
+
+
+# ---- offsets past 32 bits ------------------------------------------------------------------------
+
+def test_grouped_operands_past_four_gibibytes():
+    """Rows far apart in a buffer of more than 4 GiB, by position and through maps, in every product."""
+    g = gen(20)
+    R, LD, N, K = 1100, 1 << 21, 40, 72
+    buf = torch.empty(R, LD, dtype=BF, device="cuda")        # 4.6 GB
+    x, dy = buf[:, 8:8 + K], buf[:, 1024:1024 + N]
+    x.copy_(randn(g, R, K))
+    dy.copy_(randn(g, R, N))
+    counts = [500, 0, 350, 250]
+    off, o = offsets_of(counts), offsets_of(counts).cpu().numpy()
+    w = randn(g, 4, N, K)
+    for mapped in (False, True):
+        m = torch.randint(-1, R + 1, (R,), generator=g, dtype=torch.int32).cuda() if mapped else None
+        mn = None if m is None else m.cpu().numpy()
+        y, dx = torch.zeros(R, N, device="cuda"), torch.zeros(R, K, device="cuda")
+        dw = torch.zeros(4, N, K, device="cuda")
+        moe.moe_grouped_gemm(x, w, off, y, row_map=m)
+        moe.moe_grouped_gemm_dgrad(dy, w, off, dx, row_map=m)
+        moe.moe_grouped_gemm_wgrad(dy, x, off, dw, dy_map=m, x_map=m)
+        X, DY, W = f64(x), f64(dy), f64(w)
+        check(y, *orc.grouped_forward(X, W, o, np.zeros((R, N)), mn), K, False)
+        check(dx, *orc.grouped_dgrad(DY, W, o, np.zeros((R, K)), mn), N, False)
+        check(dw, *orc.grouped_wgrad(DY, X, o, np.zeros((4, N, K)), mn, mn), 500, False)
