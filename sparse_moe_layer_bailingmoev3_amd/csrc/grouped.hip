@@ -103,6 +103,26 @@ __device__ __forceinline__ int swz_tr(int row) {
   return (((row >> 3) & 1)) << 1;                                            // 64-byte rows
 }
 
+// v[j] of lane b of every quad <-> v[b] of lane j
+__device__ __forceinline__ void quad_transpose(floatx4 (&v)[4]) {
+  const bool b0 = threadIdx.x & 1, b1 = threadIdx.x & 2;
+  auto swap = [](float& x, float& y, bool up, auto ctrl) {  // lower lane keeps x, upper keeps y
+    const float t = __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(up ? x : y), decltype(ctrl)::value, 0xF, 0xF, true));
+    x = up ? t : x;
+    y = up ? y : t;
+  };
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float w[4] = {v[0][i], v[1][i], v[2][i], v[3][i]};
+    swap(w[0], w[1], b0, std::integral_constant<int, 0xB1>{});  // quad_perm 1 0 3 2
+    swap(w[2], w[3], b0, std::integral_constant<int, 0xB1>{});
+    swap(w[0], w[2], b1, std::integral_constant<int, 0x4E>{});  // quad_perm 2 3 0 1
+    swap(w[1], w[3], b1, std::integral_constant<int, 0x4E>{});
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j][i] = w[j];
+  }
+}
+
 // f(0) .. f(N-1), written out by the front end (a loop over registers that the optimiser unrolls
 // too late leaves them in memory)
 template <typename F, int... I>
@@ -474,26 +494,60 @@ __global__ __launch_bounds__(WR* WC * 64, (WR * WC == 4 && NST * (BR + BC) * KS 
     }
   };
 
-  // lane holds columns c..c+3 of one output row
+  // Lane (r16, q) holds columns 16c + 4q .. +3 of output row r16 for the fragments c.  Four
+  // fragments are first turned within each quad of lanes, after which lane (4a + b, q) holds
+  // columns 16b + 4q .. of rows 4a .. 4a+3: 16 lanes then write (and, adding, read) one row's 64
+  // columns side by side, whole cache lines instead of 64-byte pieces of them.
   auto epilogue = [&]() {
+    const int rows = OP == OP_WGRAD ? a.N : cw.cnt;
+    const int64_t ob = OP == OP_WGRAD ? (int64_t)cw.e * a.N * a.K : (int64_t)cw.p0 * a.ldo;
+    const int64_t ldo = OP == OP_WGRAD ? a.K : a.ldo;
+    // row and first column of piece j of fragment row r
+    constexpr bool TURN = CJ == 4;
+    const int row0 = cw.r0 + wr * RJ * 16 + (TURN ? r16 & 12 : r16);
+    const int col0 = cw.c0 + wc * CJ * 16 + 4 * q + (TURN ? (r16 & 3) * 16 : 0);
+    auto at = [&](int r, int j, bool& ok) -> int64_t {
+      const int row = row0 + r * 16 + (TURN ? j : 0), col = col0 + (TURN ? 0 : j * 16);
+      ok = row < rows && col < Cdim;
+      return ob + (int64_t)row * ldo + col;
+    };
+    if constexpr (TURN) {
 #pragma unroll
-    for (int r = 0; r < RJ; ++r) {
-      const int row = cw.r0 + (wr * RJ + r) * 16 + r16;
-      if (row >= (OP == OP_WGRAD ? a.N : cw.cnt)) continue;
-      const int64_t ob = OP == OP_WGRAD ? ((int64_t)cw.e * a.N + row) * a.K : (int64_t)(cw.p0 + row) * a.ldo;
+      for (int r = 0; r < RJ; ++r) {
+        floatx4 v[4] = {acc[0][r], acc[1][r], acc[2][r], acc[3][r]};
+        quad_transpose(v);
 #pragma unroll
-      for (int c = 0; c < CJ; ++c) {
-        const int col = cw.c0 + (wc * CJ + c) * 16 + 4 * q;
-        if (col >= Cdim) continue;
-        if constexpr (F32) {
-          floatx4* o = (floatx4*)((float*)a.out + ob + col);
-          *o = a.accumulate ? *o + acc[c][r] : acc[c][r];
-        } else {
-          *(u32x2*)((uint16_t*)a.out + ob + col) =
-              u32x2{f32x2_to_bf16x2(acc[c][r][0], acc[c][r][1]), f32x2_to_bf16x2(acc[c][r][2], acc[c][r][3])};
-        }
+        for (int j = 0; j < 4; ++j) acc[j][r] = v[j];
       }
     }
+    if constexpr (F32) {
+      if (a.accumulate) {
+        // all of the old values at once: added one by one, each would wait for its own load
+        floatx4 old[CJ][RJ];
+#pragma unroll
+        for (int r = 0; r < RJ; ++r)
+#pragma unroll
+          for (int j = 0; j < CJ; ++j) {
+            bool ok;
+            const int64_t i = at(r, j, ok);
+            old[j][r] = *(const floatx4*)((const float*)a.out + (ok ? i : ob));
+          }
+#pragma unroll
+        for (int r = 0; r < RJ; ++r)
+#pragma unroll
+          for (int j = 0; j < CJ; ++j) acc[j][r] += old[j][r];
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < RJ; ++r)
+#pragma unroll
+      for (int j = 0; j < CJ; ++j) {
+        bool ok;
+        const int64_t i = at(r, j, ok);
+        if (!ok) continue;
+        if constexpr (F32) *(floatx4*)((float*)a.out + i) = acc[j][r];
+        else *(u32x2*)((uint16_t*)a.out + i) = u32x2{f32x2_to_bf16x2(acc[j][r][0], acc[j][r][1]), f32x2_to_bf16x2(acc[j][r][2], acc[j][r][3])};
+      }
   };
 
   set_sources();
