@@ -312,84 +312,102 @@ def moe_quantise_mxfp8(x, rows, cols, codes, scales, stream=None):
 _ERR_INVALID, _ERR_UNSUPPORTED = -1, -2
 
 
-def _require(ok, message, status=_ERR_INVALID):
-    if not ok:
-        raise MoEError(status, message)
+def _refuse(message, status=_ERR_INVALID):
+    raise MoEError(status, message)
 
 
-class _on_device:
-    """The device that all tensors lie on, made current for the call; its current stream unless one
-    is given (which must belong to it)."""
+_torch_module = None
 
-    def __init__(self, tensors, stream):
+
+def _torch():
+    global _torch_module
+    if _torch_module is None:
         import torch
-        devices = {t.device for t in tensors if t is not None}
-        _require(len(devices) == 1, f"tensors lie on several devices: {sorted(map(str, devices))}")
-        self._dev = devices.pop()
-        _require(self._dev.type == "cuda", f"tensors must lie on a GPU, not on {self._dev}")
-        given = getattr(stream, "device", None)
-        _require(given is None or given == self._dev, f"stream belongs to {given}, tensors lie on {self._dev}")
-        self._guard = torch.cuda.device(self._dev)
-        self._stream = stream
+        _torch_module = torch
+    return _torch_module
 
-    def __enter__(self):
-        self._guard.__enter__()
-        return _stream(self._stream)
 
-    def __exit__(self, *exc):
-        return self._guard.__exit__(*exc)
+def _enqueue(fn, tensors, stream, *args):
+    """fn(*args, stream) with the tensors' device current; its current stream unless one is given
+    (which must belong to it)."""
+    torch = _torch()
+    dev = -2
+    for t in tensors:
+        if t is not None:
+            d = t.get_device()
+            if dev == -2:
+                dev = d
+            if d != dev or d < 0:
+                devices = sorted({str(x.device) for x in tensors if x is not None})
+                _refuse(f"tensors lie on several devices: {devices}" if len(devices) > 1 else
+                        f"tensors must lie on a GPU, not on {devices[0]}")
+    given = getattr(stream, "device", None)
+    if given is not None and given.index != dev:
+        _refuse(f"stream belongs to {given}, tensors lie on cuda:{dev}")
+    if torch.cuda.current_device() == dev:
+        _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream if stream is None else _stream(stream)))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, _stream(stream)))
 
 
 def _dtype_code(t, name):
-    import torch
-    codes = {torch.bfloat16: MOE_DTYPE_BF16, torch.float32: MOE_DTYPE_FP32}
-    _require(t.dtype in codes, f"{name} must be bfloat16 or float32, not {t.dtype}", _ERR_UNSUPPORTED)
-    return codes[t.dtype]
+    torch = _torch()
+    if t.dtype is torch.bfloat16:
+        return MOE_DTYPE_BF16
+    if t.dtype is not torch.float32:
+        _refuse(f"{name} must be bfloat16 or float32, not {t.dtype}", _ERR_UNSUPPORTED)
+    return MOE_DTYPE_FP32
 
 
 def _typed(t, name, dtype, dim):
-    import torch
-    _require(isinstance(t, torch.Tensor), f"{name} must be a tensor")
-    _require(dtype is None or t.dtype == dtype, f"{name} must be {dtype}, not {t.dtype}")
-    _require(t.dim() == dim, f"{name} must have {dim} dimension(s), not {t.dim()}")
-    return t
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        _refuse(f"{name} must be a tensor")
+    if dtype is not None and t.dtype is not dtype:
+        _refuse(f"{name} must be {dtype}, not {t.dtype}")
+    if t.dim() != dim:
+        _refuse(f"{name} must have {dim} dimension(s), not {t.dim()}")
 
 
 def _matrix(t, name, dtype=None):
-    """A [rows, columns] tensor whose columns lie side by side; returns it and its row stride."""
+    """Row stride of a [rows, columns] tensor whose columns lie side by side."""
     _typed(t, name, dtype, 2)
-    _require(t.shape[1] <= 1 or t.stride(1) == 1, f"{name}: the values of a row must lie side by side")
-    return t, t.stride(0) if t.shape[0] > 1 else max(t.stride(0), (t.shape[1] + 7) // 8 * 8)
+    rows, cols = t.shape
+    ld, unit = t.stride()
+    if cols > 1 and unit != 1:
+        _refuse(f"{name}: the values of a row must lie side by side")
+    return ld if rows > 1 else max(ld, (cols + 7) // 8 * 8)
 
 
 def _vector(t, name, dtype, n=None):
-    if t is None:
-        return None
     _typed(t, name, dtype, 1)
-    _require(t.numel() <= 1 or t.stride(0) == 1, f"{name} must be contiguous")
-    _require(n is None or t.numel() == n, f"{name} has {t.numel()} entries, {n} needed")
-    return t
+    if t.shape[0] > 1 and t.stride(0) != 1:
+        _refuse(f"{name} must be contiguous")
+    if n is not None and t.shape[0] != n:
+        _refuse(f"{name} has {t.shape[0]} entries, {n} needed")
 
 
 def _weights3(t, name):
-    import torch
-    _typed(t, name, torch.bfloat16, 3)
-    _require(t.is_contiguous(), f"{name} must be contiguous")
-    return t
+    _typed(t, name, _torch().bfloat16, 3)
+    if not t.is_contiguous():
+        _refuse(f"{name} must be contiguous")
 
 
 def _groups(offsets, groups, n, k, rows):
-    import torch
-    _vector(offsets, "offsets", torch.int32, groups + 1)
-    return _Groups(groups, n, k, rows, _ptr(offsets))
+    _vector(offsets, "offsets", _torch().int32, groups + 1)
+    return _Groups(groups, n, k, rows, offsets.data_ptr())
 
 
 def _operand(t, name, cols, row_map, positions):
-    import torch
-    t, ld = _matrix(t, name, torch.bfloat16)
-    _require(t.shape[1] == cols, f"{name} has {t.shape[1]} columns, {cols} needed")
-    _vector(row_map, f"the row map of {name}", torch.int32, positions)
-    return _Rows(_ptr(t) if t.shape[0] else None, t.shape[0], ld, _ptr(row_map))
+    torch = _torch()
+    ld = _matrix(t, name, torch.bfloat16)
+    rows, c = t.shape
+    if c != cols:
+        _refuse(f"{name} has {c} columns, {cols} needed")
+    if row_map is not None:
+        _vector(row_map, f"the row map of {name}", torch.int32, positions)
+    return _Rows(t.data_ptr() if rows else None, rows, ld, None if row_map is None else row_map.data_ptr())
 
 
 def moe_grouped_gemm(x, w, offsets, y, row_map=None, accumulate=False, stream=None):
@@ -397,69 +415,71 @@ def moe_grouped_gemm(x, w, offsets, y, row_map=None, accumulate=False, stream=No
     x bf16 [.., in], w bf16 [G, out, in], offsets int32 [G+1], y bf16 or fp32 [P, out] (added to
     with accumulate, fp32 only), row_map int32 [P] (None: position p is row p)."""
     _weights3(w, "w")
-    y, ldy = _matrix(y, "y")
+    ldy = _matrix(y, "y")
     G, N, K = w.shape
-    _require(y.shape[1] == N, f"y has {y.shape[1]} columns, w makes {N}")
-    P = y.shape[0]
+    P, cols = y.shape
+    if cols != N:
+        _refuse(f"y has {cols} columns, w makes {N}")
     g, a = _groups(offsets, G, N, K, P), _operand(x, "x", K, row_map, P)
-    with _on_device((x, w, offsets, y, row_map), stream) as s:
-        _check(load_library().moe_grouped_gemm(ctypes.byref(g), ctypes.byref(a), _ptr(w), _ptr(y), ldy, _dtype_code(y, "y"),
-                                               int(bool(accumulate)), s))
+    _enqueue(load_library().moe_grouped_gemm, (x, w, offsets, y, row_map), stream, ctypes.byref(g), ctypes.byref(a),
+             w.data_ptr(), y.data_ptr(), ldy, _dtype_code(y, "y"), 1 if accumulate else 0)
 
 
 def moe_grouped_gemm_dgrad(dy, w, offsets, dx, row_map=None, dy2=None, w2=None, accumulate=False, stream=None):
     """dx[p] = dy[row_map[p]] w[g] (+ dy2[row_map[p]] w2[g]): dy bf16 [.., out], w bf16 [G, out, in],
-    dx bf16 or fp32 [P, in]."""
+    dx bf16 or fp32 [P, in]; dy2 has dy's rows and row stride."""
     _weights3(w, "w")
-    dx, lddx = _matrix(dx, "dx")
+    lddx = _matrix(dx, "dx")
     G, N, K = w.shape
-    _require(dx.shape[1] == K, f"dx has {dx.shape[1]} columns, w makes {K}")
-    _require((dy2 is None) == (w2 is None), "dy2 and w2 must be given together")
-    P = dx.shape[0]
-    g, a, b = _groups(offsets, G, N, K, P), _operand(dy, "dy", N, row_map, P), None
+    P, cols = dx.shape
+    if cols != K:
+        _refuse(f"dx has {cols} columns, w makes {K}")
+    if (dy2 is None) != (w2 is None):
+        _refuse("dy2 and w2 must be given together")
+    g, a, b, pw2 = _groups(offsets, G, N, K, P), _operand(dy, "dy", N, row_map, P), None, None
     if w2 is not None:
         _weights3(w2, "w2")
-        _require(w2.shape == w.shape, f"w2 is {tuple(w2.shape)}, w is {tuple(w.shape)}")
-        b = ctypes.byref(_operand(dy2, "dy2", N, row_map, P))
-    with _on_device((dy, w, offsets, dx, row_map, dy2, w2), stream) as s:
-        _check(load_library().moe_grouped_gemm_dgrad(ctypes.byref(g), ctypes.byref(a), _ptr(w), b, _ptr(w2), _ptr(dx), lddx,
-                                                     _dtype_code(dx, "dx"), int(bool(accumulate)), s))
+        if w2.shape != w.shape:
+            _refuse(f"w2 is {tuple(w2.shape)}, w is {tuple(w.shape)}")
+        b, pw2 = ctypes.byref(_operand(dy2, "dy2", N, row_map, P)), w2.data_ptr()
+    _enqueue(load_library().moe_grouped_gemm_dgrad, (dy, w, offsets, dx, row_map, dy2, w2), stream, ctypes.byref(g),
+             ctypes.byref(a), w.data_ptr(), b, pw2, dx.data_ptr(), lddx, _dtype_code(dx, "dx"), 1 if accumulate else 0)
 
 
 def moe_grouped_gemm_wgrad(dy, x, offsets, dw, dy_map=None, x_map=None, accumulate=False, stream=None):
     """dw[g] = sum over group g's positions of dy[dy_map[p]]^T x[x_map[p]]: dy bf16 [.., out], x bf16
     [.., in], dw bf16 or fp32 [G, out, in] (added to with accumulate, fp32 only)."""
     _typed(dw, "dw", None, 3)
-    _require(dw.is_contiguous(), "dw must be contiguous")
+    if not dw.is_contiguous():
+        _refuse("dw must be contiguous")
     G, N, K = dw.shape
-    sizes = {m.shape[0] if m is not None else t.shape[0] for t, m in ((dy, dy_map), (x, x_map))}
-    _require(len(sizes) == 1, f"dy and x cover different numbers of positions: {sorted(sizes)}")
-    P = sizes.pop()
+    P, px = (t.shape[0] if m is None else m.shape[0] for t, m in ((dy, dy_map), (x, x_map)))
+    if P != px:
+        _refuse(f"dy and x cover different numbers of positions: {P} and {px}")
     g = _groups(offsets, G, N, K, P)
     a, b = _operand(dy, "dy", N, dy_map, P), _operand(x, "x", K, x_map, P)
-    with _on_device((dy, x, offsets, dw, dy_map, x_map), stream) as s:
-        _check(load_library().moe_grouped_gemm_wgrad(ctypes.byref(g), ctypes.byref(a), ctypes.byref(b), _ptr(dw),
-                                                     _dtype_code(dw, "dw"), int(bool(accumulate)), s))
+    _enqueue(load_library().moe_grouped_gemm_wgrad, (dy, x, offsets, dw, dy_map, x_map), stream, ctypes.byref(g),
+             ctypes.byref(a), ctypes.byref(b), dw.data_ptr(), _dtype_code(dw, "dw"), 1 if accumulate else 0)
 
 
-def _like(first, /, **named):
-    """Row stride that the named matrices of the first one's shape share."""
-    import torch
-    strides = set()
-    for name, t in named.items():
-        t, ld = _matrix(t, name, torch.bfloat16)
-        _require(t.shape == first.shape, f"{name} is {tuple(t.shape)}, gate is {tuple(first.shape)}")
-        strides.add(ld)
-    _require(len(strides) == 1, f"{' and '.join(named)} must have the same row stride")
-    return strides.pop()
+def _like(shape, t, name):
+    """Row stride of a bf16 matrix of that shape."""
+    ld = _matrix(t, name, _torch().bfloat16)
+    if t.shape != shape:
+        _refuse(f"{name} is {tuple(t.shape)}, gate is {tuple(shape)}")
+    return ld
 
 
 def _pairs(row_w, pos, rows):
     """Number of rows handled: that of the positions or weights given, else all."""
-    import torch
-    n = pos.numel() if pos is not None else row_w.numel() if row_w is not None else rows
-    _vector(pos, "pos", torch.int32, n)
-    _vector(row_w, "row_w", torch.float32, n)
+    torch = _torch()
+    n = rows
+    if pos is not None:
+        _vector(pos, "pos", torch.int32)
+        n = pos.shape[0]
+    if row_w is not None:
+        _vector(row_w, "row_w", torch.float32, None if pos is None else n)
+        n = row_w.shape[0]
     return n
 
 
@@ -467,23 +487,28 @@ def moe_swiglu(gate, up, h, limit=0.0, row_w=None, pos=None, stream=None):
     """h[pos[i]] = row_w[i] * clamp(silu(gate[pos[i]]) * up[pos[i]], -limit, limit): gate, up, h bf16
     [R, C]; row_w fp32 [n] (None: 1), pos int32 [n], distinct (None: row i), entries outside [0, R)
     skipped; limit <= 0: no clamp."""
-    ld, ldh = _like(gate, gate=gate, up=up), _like(gate, h=h)
-    R, C = gate.shape
-    n = _pairs(row_w, pos, R)
-    with _on_device((gate, up, h, row_w, pos), stream) as s:
-        _check(load_library().moe_swiglu(n, R, C, float(limit), _ptr(gate), _ptr(up), ld, _ptr(row_w), _ptr(pos), _ptr(h), ldh, s))
+    ld, shape = _matrix(gate, "gate", _torch().bfloat16), gate.shape
+    if _like(shape, up, "up") != ld:
+        _refuse("gate and up must have the same row stride")
+    ldh, (R, C), n = _like(shape, h, "h"), shape, _pairs(row_w, pos, shape[0])
+    _enqueue(load_library().moe_swiglu, (gate, up, h, row_w, pos), stream, n, R, C, float(limit), gate.data_ptr(),
+             up.data_ptr(), ld, _ptr(row_w), _ptr(pos), h.data_ptr(), ldh)
 
 
 def moe_swiglu_backward(gate, up, dh, dgate, dup, limit=0.0, row_w=None, pos=None, drow_w=None, stream=None):
     """Gradients of moe_swiglu from dh: dgate, dup bf16 [R, C], drow_w fp32 [n] (None: not wanted)."""
-    import torch
-    ld, lddh, ldd = _like(gate, gate=gate, up=up), _like(gate, dh=dh), _like(gate, dgate=dgate, dup=dup)
-    R, C = gate.shape
-    n = _pairs(row_w, pos, R)
-    _vector(drow_w, "drow_w", torch.float32, n)
-    with _on_device((gate, up, dh, dgate, dup, row_w, pos, drow_w), stream) as s:
-        _check(load_library().moe_swiglu_backward(n, R, C, float(limit), _ptr(gate), _ptr(up), ld, _ptr(dh), lddh, _ptr(row_w),
-                                                  _ptr(pos), _ptr(dgate), _ptr(dup), ldd, _ptr(drow_w), s))
+    ld, shape = _matrix(gate, "gate", _torch().bfloat16), gate.shape
+    if _like(shape, up, "up") != ld:
+        _refuse("gate and up must have the same row stride")
+    lddh, ldd = _like(shape, dh, "dh"), _like(shape, dgate, "dgate")
+    if _like(shape, dup, "dup") != ldd:
+        _refuse("dgate and dup must have the same row stride")
+    (R, C), n = shape, _pairs(row_w, pos, shape[0])
+    if drow_w is not None:
+        _vector(drow_w, "drow_w", _torch().float32, n)
+    _enqueue(load_library().moe_swiglu_backward, (gate, up, dh, dgate, dup, row_w, pos, drow_w), stream, n, R, C,
+             float(limit), gate.data_ptr(), up.data_ptr(), ld, dh.data_ptr(), lddh, _ptr(row_w), _ptr(pos),
+             dgate.data_ptr(), dup.data_ptr(), ldd, _ptr(drow_w))
 
 
 class MoEAdamWPlan:
@@ -495,13 +520,14 @@ class MoEAdamWPlan:
 
     def __init__(self, params, grads, exp_avg, exp_avg_sq, master=None, exp_avg_scale=None, exp_avg_sq_scale=None,
                  weight_decay=0.0):
-        import torch
+        torch = _torch()
         cols = {"params": list(params), "grads": list(grads), "exp_avg": list(exp_avg), "exp_avg_sq": list(exp_avg_sq)}
         n = len(cols["params"])
-        _require(n > 0, "params must not be empty")
+        if n == 0:
+            _refuse("params must not be empty")
         eight = len(cols["exp_avg"]) > 0 and cols["exp_avg"][0].dtype == torch.uint8
-        _require((exp_avg_scale is not None) == eight and (exp_avg_sq_scale is not None) == eight,
-                 "scales belong to uint8 states, and both must be given")
+        if (exp_avg_scale is not None) != eight or (exp_avg_sq_scale is not None) != eight:
+            _refuse("scales belong to uint8 states, and both must be given")
         for name, t in (("master", master), ("exp_avg_scale", exp_avg_scale), ("exp_avg_sq_scale", exp_avg_sq_scale)):
             if t is not None:
                 cols[name] = list(t)
@@ -509,63 +535,69 @@ class MoEAdamWPlan:
         types = {"params": cols["params"][0].dtype, "grads": cols["grads"][0].dtype if cols["grads"] else None,
                  "exp_avg": state, "exp_avg_sq": state, "master": torch.float32, "exp_avg_scale": torch.float32,
                  "exp_avg_sq_scale": torch.float32}
+        device = cols["params"][0].device
         for name, ts in cols.items():
-            _require(len(ts) == n, f"{name} has {len(ts)} tensors, params {n}")
+            if len(ts) != n:
+                _refuse(f"{name} has {len(ts)} tensors, params {n}")
             for i, t in enumerate(ts):
-                _require(t.dtype == types[name], f"{name}[{i}] must be {types[name]}, not {t.dtype}")
-                _require(t.is_contiguous(), f"{name}[{i}] must be contiguous")
+                if t.dtype != types[name]:
+                    _refuse(f"{name}[{i}] must be {types[name]}, not {t.dtype}")
+                if not t.is_contiguous():
+                    _refuse(f"{name}[{i}] must be contiguous")
                 want = cols["params"][i].numel()
                 want = -(-want // 128) if name.endswith("scale") else want
-                _require(t.numel() == want, f"{name}[{i}] has {t.numel()} values, {want} needed")
+                if t.numel() != want:
+                    _refuse(f"{name}[{i}] has {t.numel()} values, {want} needed")
+                if t.device != device or not t.is_cuda:
+                    _refuse(f"{name}[{i}] lies on {t.device}, params[0] on {device}; one GPU must hold them all")
         decay = list(weight_decay) if hasattr(weight_decay, "__len__") else [weight_decay] * n
-        _require(len(decay) == n, f"weight_decay has {len(decay)} entries, params {n}")
-        self._keep = cols
-        with _on_device([t for ts in cols.values() for t in ts], None):
-            self.device = cols["params"][0].device
-            table = (_AdamWTensor * n)()
-            field = {"params": "param", "grads": "grad"}
-            for name, ts in cols.items():
-                for i, t in enumerate(ts):
-                    setattr(table[i], field.get(name, name), _ptr(t) or None)
-            for i, t in enumerate(cols["params"]):
-                table[i].numel, table[i].weight_decay = t.numel(), float(decay[i])
-            self.struct = _AdamWPlan()
-            args = (n, ctypes.byref(table), _dtype_code(cols["params"][0], "params"), _dtype_code(cols["grads"][0], "grads"),
-                    MOE_STATE_8BIT if eight else MOE_STATE_FP32, ctypes.byref(self.struct))
-            lib = load_library()
-            _check(lib.moe_adamw_plan(*args, None, 0))
-            host = torch.empty(self.struct.image_bytes, dtype=torch.uint8)
-            _check(lib.moe_adamw_plan(*args, _ptr(host), host.numel()))
-            self.image = host.to(self.device)
+        if len(decay) != n:
+            _refuse(f"weight_decay has {len(decay)} entries, params {n}")
+        self._keep, self.device = cols, device
+        table = (_AdamWTensor * n)()
+        field = {"params": "param", "grads": "grad"}
+        for name, ts in cols.items():
+            for i, t in enumerate(ts):
+                setattr(table[i], field.get(name, name), t.data_ptr() or None)
+        for i, t in enumerate(cols["params"]):
+            table[i].numel, table[i].weight_decay = t.numel(), float(decay[i])
+        self.struct = _AdamWPlan()
+        args = (n, ctypes.byref(table), _dtype_code(cols["params"][0], "params"), _dtype_code(cols["grads"][0], "grads"),
+                MOE_STATE_8BIT if eight else MOE_STATE_FP32, ctypes.byref(self.struct))
+        lib = load_library()
+        _check(lib.moe_adamw_plan(*args, None, 0))
+        host = torch.empty(self.struct.image_bytes, dtype=torch.uint8)
+        _check(lib.moe_adamw_plan(*args, host.data_ptr(), host.numel()))
+        self.image = host.to(device)
 
 
 def moe_adamw_step(plan: MoEAdamWPlan, lr, step, betas=(0.9, 0.999), eps=1e-8, seed=0, grad_scale=None, stream=None):
     """One AdamW step over the plan's tensors, in place.  lr and step (1 for the first) are numbers,
     or device tensors (fp32, int64) read when the step runs; grad_scale an fp32 device tensor that
     multiplies every gradient; seed that of the 8-bit states' stochastic rounding."""
-    import torch
+    torch = _torch()
     cfg = _AdamWConfig(beta1=betas[0], beta2=betas[1], eps=eps, seed=seed & 0xFFFFFFFF)
     given = [plan.image]
     for name, v, dtype in (("lr", lr, torch.float32), ("step", step, torch.int64), ("grad_scale", grad_scale, torch.float32)):
         if isinstance(v, torch.Tensor):
-            _require(v.dtype == dtype and v.numel() == 1, f"{name} must hold one {dtype} value")
+            if v.dtype != dtype or v.numel() != 1:
+                _refuse(f"{name} must hold one {dtype} value")
             given.append(v)
-            setattr(cfg, name if name == "grad_scale" else name + "_ptr", _ptr(v))
+            setattr(cfg, name if name == "grad_scale" else name + "_ptr", v.data_ptr())
         elif name != "grad_scale":
             setattr(cfg, name, v)
-        else:
-            _require(v is None, "grad_scale must be a device tensor")
-    with _on_device(given, stream) as s:
-        _check(load_library().moe_adamw_step(ctypes.byref(cfg), ctypes.byref(plan.struct), _ptr(plan.image), s))
+        elif v is not None:
+            _refuse("grad_scale must be a device tensor")
+    _enqueue(load_library().moe_adamw_step, given, stream, ctypes.byref(cfg), ctypes.byref(plan.struct), plan.image.data_ptr())
 
 
 def moe_adamw_dequantise(codes, scales, out, signed, stream=None):
     """Values of an 8-bit state array: codes uint8 [n], scales fp32 [ceil(n / 128)] -> out fp32 [n];
     signed: exp_avg's codes, else exp_avg_sq's."""
-    import torch
+    torch = _torch()
     _vector(codes, "codes", torch.uint8)
-    n = codes.numel()
+    n = codes.shape[0]
     _vector(scales, "scales", torch.float32, -(-n // 128))
     _vector(out, "out", torch.float32, n)
-    with _on_device((codes, scales, out), stream) as s:
-        _check(load_library().moe_adamw_dequantise(_ptr(codes), _ptr(scales), n, int(bool(signed)), _ptr(out), s))
+    _enqueue(load_library().moe_adamw_dequantise, (codes, scales, out), stream, codes.data_ptr(), scales.data_ptr(), n,
+             1 if signed else 0, out.data_ptr())
