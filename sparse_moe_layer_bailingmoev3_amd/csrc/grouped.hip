@@ -30,6 +30,7 @@
 // eighth of the tiles together, so tiles that share operand rows or weights run side by side in
 // one L2.
 #include <atomic>
+#include <cmath>
 #include <utility>
 
 #include "moe_common.h"
@@ -95,7 +96,7 @@ __device__ __forceinline__ void wait_vmcnt() {
 // output values whose 32-byte blocks are read by the transposing load: one read touches rows
 // 8q..8q+3 (or 8q+4..8q+7) of lane groups q, told apart by bits 0, 1 and 3 of the row.
 template <int KS>
-__device__ __forceinline__ int swz_k(int row) { return KS == 64 ? (row >> 1) & 7 : (row >> 2) & 3; }
+__device__ __forceinline__ int swz_k(int row) { return KS == 64 ? (row >> 1) & 7 : row & 15; }
 template <int W>
 __device__ __forceinline__ int swz_tr(int row) {
   if constexpr (W >= 128) return ((row & 3) | ((row >> 1) & 4)) << 1;
@@ -284,8 +285,7 @@ __global__ __launch_bounds__(WR* WC * 64, (WR * WC == 4 && NST * (BR + BC) * KS 
   // ---- load sources: descriptor bases that move with the steps, offsets that stay for the tile
   uint64_t xb = 0, yb = 0;
   int64_t xstep = 0, ystep = 0;
-  uint32_t xo[XN], yo[YN];
-  const char* xs[XN];  // a mapped matrix of more than BUF_MAX bytes: 64-bit addresses per lane
+  uint32_t xo[XN], yo[YN];  // (the rows of a mapped matrix of more than BUF_MAX bytes: row numbers)
   int xn = XN;         // row loads that hold a row of the tile
   int left = 0;        // reduction values from step `ls` on
   const char* const zero = (const char*)grouped_zeros;
@@ -310,19 +310,15 @@ __global__ __launch_bounds__(WR* WC * 64, (WR * WC == 4 && NST * (BR + BC) * KS 
       each<XN>([&](auto i) {
         const int row0 = (i * NW + wave) * KR, row = row0 + lane / KC;
         const int ch = (lane % KC) ^ swz_k<KS>(row);
-        // (one store to each array: stores that branches share would keep the arrays in memory)
         uint32_t o = (uint32_t)row * (uint32_t)(m.ld * 2) + ch * 16;
         bool ok = row < n;
-        const char* ptr = zero;
         if (m.map) {
           int src = -1;
           if (row0 < n) src = mapped(m, ld.p0 + ld.r0 + row0, ld.p0 + ld.cnt - 1, lane / KC, std::integral_constant<int, KR>{});
           ok = ok && (unsigned)src < (unsigned)m.rows;
-          o = (uint32_t)src * (uint32_t)(m.ld * 2) + ch * 16;
-          if (wide0 && ok) ptr = (const char*)m.data + ((int64_t)src * m.ld + ch * 8) * 2;
+          o = wide0 ? (uint32_t)src : (uint32_t)src * (uint32_t)(m.ld * 2) + ch * 16;
         }
         xo[i] = ok ? o : BUF_OUT;
-        xs[i] = ptr;
       });
     }
   };
@@ -364,6 +360,27 @@ __global__ __launch_bounds__(WR* WC * 64, (WR * WC == 4 && NST * (BR + BC) * KS 
     }
   };
 
+  // wgrad through maps: the rows of the next step's loads, read one step ahead (a step waits for
+  // all loads of the one before, these among them)
+  int di[XT ? XN : 1], xi[XT ? XN : 1];
+  auto load_rows = [&]() {
+    if constexpr (OP == OP_WGRAD) {
+      static_assert(D == 1, "row indices are one step ahead");
+      if (a.x0.map || a.x1.map) {
+        each<XN>([&](auto i) {
+          const int p = ld.p0 + max(min(ls * KS + (wave * XN + i) * XR + lane / XL, ld.cnt - 1), 0);
+          int d = 0, x = 0;
+          if (ld.cnt > 0) {
+            if (a.x0.map) d = a.x0.map[p];
+            if (a.x1.map) x = a.x1.map[p];
+          }
+          di[i] = d;
+          xi[i] = x;
+        });
+      }
+    }
+  };
+
   // loads of step `ls` of tile `ld` into the stage at LDS offset st
   auto issue = [&](uint32_t st) {
     if constexpr (OP == OP_WGRAD) {
@@ -384,15 +401,10 @@ __global__ __launch_bounds__(WR* WC * 64, (WR * WC == 4 && NST * (BR + BC) * KS 
         }
       } else {
         // a row counts only if it exists in both matrices
-        const int last = ld.p0 + ld.cnt - 1;
         each<XN>([&](auto i) {
-          const int row0 = (wave * XN + i) * XR, sub = lane / XL, row = row0 + sub;
-          const int p = ld.p0 + ls * KS + row0;
-          int d = 0, x = 0;
-          if (a.x0.map && ld.cnt > 0) d = mapped(a.x0, p, last, sub, std::integral_constant<int, XR>{});
-          if (a.x1.map && ld.cnt > 0) x = mapped(a.x1, p, last, sub, std::integral_constant<int, XR>{});
-          const bool ok = p + sub <= last && (unsigned)d < (unsigned)a.x0.rows && (unsigned)x < (unsigned)a.x1.rows;
-          const int ch = (lane % XL) ^ swz_tr<BR>(row);
+          const int row = (wave * XN + i) * XR + lane / XL, ch = (lane % XL) ^ swz_tr<BR>(row);
+          const int d = di[i], x = xi[i];
+          const bool ok = row < left && (unsigned)d < (unsigned)a.x0.rows && (unsigned)x < (unsigned)a.x1.rows;
           const bool okd = ok && xo[i] != BUF_OUT, okx = ok && yo[i] != BUF_OUT;
           const uint32_t od = a.x0.map ? (uint32_t)d * (uint32_t)(a.x0.ld * 2) + ch * 16 : xo[i];
           const uint32_t ox = a.x1.map ? (uint32_t)x * (uint32_t)(a.x1.ld * 2) + ch * 16 : yo[i];
@@ -421,9 +433,13 @@ __global__ __launch_bounds__(WR* WC * 64, (WR * WC == 4 && NST * (BR + BC) * KS 
         each<XN>([&](auto i) {
           if (XN == 1 || i < xn) {
             const int row = (i * NW + wave) * KR + lane / KC;
-            const bool past = ((lane % KC) ^ swz_k<KS>(row)) * 8 >= left;
-            if (wide0) dma16(past || xs[i] == zero ? zero : xs[i] + (Red - left) * 2, xt + i * NW * 1024);
-            else dma16(past ? BUF_OUT : xo[i], xr, xt + i * NW * 1024);
+            const int k = ((lane % KC) ^ swz_k<KS>(row)) * 8;
+            const bool past = k >= left;
+            if (wide0) {  // a mapped matrix: row number to 64-bit address
+              const RowsArg& m = OP == OP_DGRAD && ls >= ld.steps1 ? a.x1 : a.x0;
+              const char* p = (const char*)m.data + ((int64_t)xo[i] * m.ld + (Red - left) + k) * 2;
+              dma16(past || xo[i] == BUF_OUT ? zero : p, xt + i * NW * 1024);
+            } else dma16(past ? BUF_OUT : xo[i], xr, xt + i * NW * 1024);
           }
         });
         each<YN>([&](auto i) {
@@ -441,19 +457,18 @@ __global__ __launch_bounds__(WR* WC * 64, (WR * WC == 4 && NST * (BR + BC) * KS 
   uint32_t lst = lds0;  // stage of the next step to load
   int flying = 0;       // steps loaded or in flight and not yet computed
   int n_last = 0;       // loads of the last of them
-  auto issue_next = [&]() {
+  auto issue_next = [&]() {  // `ld`, `ls` and the sources stand at the step to load
     if (!more) return;
-    if (ls == ld.nsteps) {
-      more = advance(ld);
-      if (!more) return;
-      ls = 0;
-      set_sources();
-    }
     issue(__builtin_amdgcn_readfirstlane(lst));
     lst = lst == lds0 + (NST - 1) * ST_BYTES ? lds0 : lst + ST_BYTES;
     n_last = xn;
-    ++ls;
     ++flying;
+    if (++ls == ld.nsteps) {
+      more = advance(ld);
+      ls = 0;
+      if (more) set_sources();
+    }
+    if (more) load_rows();
   };
 
   floatx4 acc[CJ][RJ];
@@ -522,20 +537,24 @@ __global__ __launch_bounds__(WR* WC * 64, (WR * WC == 4 && NST * (BR + BC) * KS 
     }
     if constexpr (F32) {
       if (a.accumulate) {
-        // all of the old values at once: added one by one, each would wait for its own load
-        floatx4 old[CJ][RJ];
+        // the old values of many pieces at once: added one by one, each would wait for its own load
+        constexpr int RP = RJ > 4 ? 1 : RJ;
 #pragma unroll
-        for (int r = 0; r < RJ; ++r)
+        for (int r0 = 0; r0 < RJ; r0 += RP) {
+          floatx4 old[CJ][RP];
 #pragma unroll
-          for (int j = 0; j < CJ; ++j) {
-            bool ok;
-            const int64_t i = at(r, j, ok);
-            old[j][r] = *(const floatx4*)((const float*)a.out + (ok ? i : ob));
-          }
+          for (int r = 0; r < RP; ++r)
 #pragma unroll
-        for (int r = 0; r < RJ; ++r)
+            for (int j = 0; j < CJ; ++j) {
+              bool ok;
+              const int64_t i = at(r0 + r, j, ok);
+              old[j][r] = *(const floatx4*)((const float*)a.out + (ok ? i : ob));
+            }
 #pragma unroll
-          for (int j = 0; j < CJ; ++j) acc[j][r] += old[j][r];
+          for (int r = 0; r < RP; ++r)
+#pragma unroll
+            for (int j = 0; j < CJ; ++j) acc[j][r0 + r] += old[j][r];
+        }
       }
     }
 #pragma unroll
@@ -551,6 +570,7 @@ __global__ __launch_bounds__(WR* WC * 64, (WR * WC == 4 && NST * (BR + BC) * KS 
   };
 
   set_sources();
+  load_rows();
 #pragma unroll
   for (int j = 0; j < D; ++j) issue_next();
 
@@ -613,26 +633,84 @@ int device_cu_count() {
   return n;
 }
 
-// Tiles: no group count is known on the host, only the number of positions and groups.
-hipError_t launch_grouped_rows(const GroupedArgs& a, bool dgrad, hipStream_t s) {
-  const int cols = dgrad ? a.K : a.N;
-  // at most one partial tile per group that holds a position
-  auto items = [&](int br, int bc) { return (a.rows / br + std::min<int64_t>(a.groups, a.rows)) * ((cols + bc - 1) / bc); };
-#define MOE_GROUPED(KS, BR, BC, WR, WC, NST, WGS)                                              \
-  return dgrad ? run_grouped<OP_DGRAD, KS, BR, BC, WR, WC, NST>(a, items(BR, BC), WGS, s)      \
-               : run_grouped<OP_FWD, KS, BR, BC, WR, WC, NST>(a, items(BR, BC), WGS, s)
-  const char* v = getenv("GV");
-  if (v && *v == '3') MOE_GROUPED(64, 128, 128, 2, 2, 2, 2);
-  if (v && *v == '5') MOE_GROUPED(64, 128, 256, 2, 4, 3, 1);
-  if (items(32, 128) < device_cu_count()) MOE_GROUPED(64, 32, 64, 1, 4, 8, 1);
-  if (a.rows <= (int64_t)24 * a.groups) MOE_GROUPED(64, 32, 128, 1, 4, 3, 2);
-  MOE_GROUPED(64, 256, 128, 4, 2, 3, 1);
-#undef MOE_GROUPED
+// ---- which tile --------------------------------------------------------------------------------
+// The group sizes are on the device; the host knows the positions and groups.  Each tile shape is
+// priced for groups of equal size and the cheapest is taken:
+//   rounds of the tiles over the workgroups that fit the card x (steps x step + tile), or what the
+//   weights and results take at the memory's rate if that is more (then the first shape in order).
+// `step` and `tile` (us, the end of a tile included) were fitted to sweeps over 1 to 8192 tokens,
+// 1 to 512 groups and weights of 136 x 520 to 2560 x 768; `alone` is a step with one workgroup on
+// its compute unit.  Sides measured (us, forward, 768 x 2560 weights, 8 of 512 groups a token):
+//   1 token: 16x64 12, 32x128 19, 64x256 23, 128x256 31, 256x256 38
+//   2048:    16x64 556, 32x128 422, 64x256 351, 128x256 351, 256x256 395
+//   8192:    16x64 1740, 32x128 918, 64x256 579, 128x256 532, 256x256 489
+struct Shape {
+  int br, bc, ks, wgs;  // tile, reduction values per step, workgroups per compute unit
+  float alone, step, tile;
+};
+constexpr double MEMORY_BYTES_PER_US = 5.8e6;
+
+static double price(const Shape& v, double items, double steps64, int cus) {
+  const double n = std::min<double>(v.wgs, std::max(1.0, items / cus));
+  const double step = std::max<double>(v.alone, v.step * n / v.wgs);
+  return std::ceil(items / ((double)cus * v.wgs)) * (std::ceil(steps64 * 64 / v.ks) * step + v.tile);
 }
 
+hipError_t launch_grouped_rows(const GroupedArgs& a, bool dgrad, hipStream_t s) {
+  const int cols = dgrad ? a.K : a.N, red = dgrad ? a.N : a.K, cus = device_cu_count();
+  if (cus <= 0) return hipErrorInvalidDevice;
+  const int pair = a.w1 ? 2 : 1;
+  static const Shape shapes[2][6] = {
+      // the reduction along the weights' rows (forward): order of preference where memory bounds all
+      {{16, 64, 128, 1, .30f, .48f, 1.f}, {128, 256, 64, 1, .6f, 1.13f, 3.f}, {64, 256, 64, 1, .42f, .86f, 2.5f},
+       {32, 128, 64, 2, .32f, .55f, 1.5f}, {64, 64, 64, 3, .33f, .77f, .7f}, {256, 256, 64, 1, .8f, 1.6f, 4.f}},
+      // across them (dgrad)
+      {{128, 256, 64, 1, .6f, 1.25f, 3.f}, {64, 256, 64, 1, .42f, .82f, 2.5f}, {32, 128, 64, 2, .32f, .67f, 1.5f},
+       {16, 64, 128, 1, .30f, .42f, 1.f}, {64, 64, 64, 3, .33f, 1.1f, .7f}, {256, 256, 64, 1, .8f, 2.2f, 4.f}}};
+  const double avg = (double)a.rows / a.groups, filled = a.groups * -std::expm1(-avg);
+  const double floor = (filled * a.N * (double)a.K * 2 * pair + (double)a.rows * cols * (a.out_f32 ? 4 : 2)) / MEMORY_BYTES_PER_US;
+  const Shape* best = nullptr;
+  double cost = 0;
+  for (const Shape& v : shapes[dgrad]) {
+    const double in_group = std::max(avg, a.rows / std::max(filled, 1e-9));
+    const double tiles = filled * std::max(1.0, in_group / v.br + (a.groups > 1 ? 0.5 : 0.0));
+    const double c = std::max(floor, price(v, tiles * ((cols + v.bc - 1) / v.bc), pair * ((red + 63) / 64), cus));
+    if (!best || c < cost) best = &v, cost = c;
+  }
+  // at most one partial tile per group that holds a position
+  auto items = [&](int br, int bc) { return (a.rows / br + std::min<int64_t>(a.groups, a.rows)) * ((cols + bc - 1) / bc); };
+#define MOE_GROUPED(KS, BR, BC, WR, WC, NST, WGS)                                                   \
+  if (best->br == BR && best->bc == BC)                                                             \
+    return dgrad ? run_grouped<OP_DGRAD, KS, BR, BC, WR, WC, NST>(a, items(BR, BC), WGS, s)         \
+                 : run_grouped<OP_FWD, KS, BR, BC, WR, WC, NST>(a, items(BR, BC), WGS, s)
+  MOE_GROUPED(128, 16, 64, 1, 4, 7, 1);
+  MOE_GROUPED(64, 32, 128, 1, 4, 3, 2);
+  MOE_GROUPED(64, 64, 64, 2, 2, 3, 3);
+  MOE_GROUPED(64, 64, 256, 2, 4, 3, 1);
+  MOE_GROUPED(64, 128, 256, 2, 4, 3, 1);
+  MOE_GROUPED(64, 256, 256, 2, 4, 2, 1);
+#undef MOE_GROUPED
+  return hipErrorInvalidValue;
+}
+
+// Weight gradient: square tiles (both operands share their rows), the same pricing.  Sides measured
+// (us, fp32 results): 512 groups of 768 x 2560, 8192 tokens: 64 2004, 128 1164, 256 871; one group,
+// 8192 rows: 64 74, 128 97, 256 192; 64 groups of 136 x 520, 1024 tokens: 64 9.5, 128 12, 256 14.
 hipError_t launch_grouped_wgrad(const GroupedArgs& a, hipStream_t s) {
-  const int64_t items = (int64_t)a.groups * ((a.N + 127) / 128) * ((a.K + 127) / 128);
-  return run_grouped<OP_WGRAD, 64, 128, 128, 2, 2, 2>(a, items, 2, s);
+  const int cus = device_cu_count();
+  if (cus <= 0) return hipErrorInvalidDevice;
+  static const Shape shapes[3] = {{256, 256, 64, 1, 1.5f, 2.3f, 9.4f}, {128, 128, 64, 2, .75f, 1.4f, 4.9f}, {64, 64, 64, 4, .55f, 1.4f, 2.f}};
+  auto items = [&](int64_t b) { return a.groups * ((a.N + b - 1) / b) * ((a.K + b - 1) / b); };
+  const double steps = std::max(1.0, (double)a.rows / a.groups / 64 + 0.5);
+  const Shape* best = nullptr;
+  double cost = 0;
+  for (const Shape& v : shapes) {
+    const double c = price(v, (double)items(v.br), steps, cus);
+    if (!best || c < cost) best = &v, cost = c;
+  }
+  if (best->br == 256) return run_grouped<OP_WGRAD, 64, 256, 256, 2, 4, 2>(a, items(256), 1, s);
+  if (best->br == 128) return run_grouped<OP_WGRAD, 64, 128, 128, 2, 2, 2>(a, items(128), 2, s);
+  return run_grouped<OP_WGRAD, 64, 64, 64, 2, 2, 2>(a, items(64), 4, s);
 }
 
 }  // namespace moe
