@@ -377,7 +377,7 @@ def _matrix(t, name, dtype=None):
     ld, unit = t.stride()
     if cols > 1 and unit != 1:
         _refuse(f"{name}: the values of a row must lie side by side")
-    return ld if rows > 1 else max(ld, (cols + 7) // 8 * 8)
+    return ld if rows > 1 else (cols + 7) // 8 * 8
 
 
 def _vector(t, name, dtype, n=None):

@@ -306,13 +306,10 @@ def adamw_inputs(seed, pdt, gdt, eight, master, sizes=SIZES):
     return params, grads, ms, m, v, sc, sv
 
 
-@pytest.mark.parametrize("pdt", [BF, F32], ids=["pbf16", "pfp32"])
+@pytest.mark.parametrize("pdt,master", [(BF, False), (BF, True), (F32, False)], ids=["bf16", "bf16_master", "fp32"])
 @pytest.mark.parametrize("gdt", [BF, F32], ids=["gbf16", "gfp32"])
 @pytest.mark.parametrize("eight", [False, True], ids=["s32", "s8"])
-@pytest.mark.parametrize("master", [False, True], ids=["plain", "master"])
-def test_adamw(pdt, gdt, eight, master):
-    if master and pdt == F32:
-        pytest.skip("master weights belong to bf16 parameters")
+def test_adamw(pdt, master, gdt, eight):
     params, grads, ms, m, v, sc, sv = adamw_inputs(10, pdt, gdt, eight, master)
     wd = [0.1 * (i % 2) for i in range(len(SIZES))]
     plan = moe.MoEAdamWPlan(params, grads, m, v, master=ms, exp_avg_scale=sc, exp_avg_sq_scale=sv, weight_decay=wd)
@@ -426,3 +423,295 @@ def test_grouped_operands_past_four_gibibytes():
         check(y, *orc.grouped_forward(X, W, o, np.zeros((R, N)), mn), K, False)
         check(dx, *orc.grouped_dgrad(DY, W, o, np.zeros((R, K)), mn), N, False)
         check(dw, *orc.grouped_wgrad(DY, X, o, np.zeros((4, N, K)), mn, mn), 500, False)
+
+
+# ---- how the operators are called ----------------------------------------------------------------
+
+def test_grouped_most_groups():
+    """1025 groups (a full layer's experts and a shared one), most of them empty."""
+    g = gen(21)
+    counts = np.zeros(1025, int)
+    counts[[0, 63, 64, 511, 512, 1023, 1024]] = [3, 1, 2, 17, 1, 1, 40]
+    off, P, N, K = offsets_of(counts), int(counts.sum()), 24, 40
+    x, w, dy = randn(g, P, K), randn(g, 1025, N, K), randn(g, P, N)
+    o = off.cpu().numpy()
+    y, dx = torch.zeros(P, N, device="cuda"), torch.zeros(P, K, device="cuda")
+    dw = torch.full((1025, N, K), 5.0, device="cuda")
+    moe.moe_grouped_gemm(x, w, off, y)
+    moe.moe_grouped_gemm_dgrad(dy, w, off, dx)
+    moe.moe_grouped_gemm_wgrad(dy, x, off, dw)
+    check(y, *orc.grouped_forward(f64(x), f64(w), o, np.zeros((P, N))), K, False)
+    check(dx, *orc.grouped_dgrad(f64(dy), f64(w), o, np.zeros((P, K))), N, False)
+    check(dw, *orc.grouped_wgrad(f64(dy), f64(x), o, np.zeros((1025, N, K))), 40, False)
+
+
+# every tile shape that a size rule can take: (positions a group, groups, weights)
+SHAPES = [(1, 70, (768, 136)), (4, 40, (768, 136)), (16, 64, (264, 520)), (40, 24, (520, 264)), (70, 130, (264, 136)),
+          (200, 12, (264, 136)), (300, 70, (264, 520)), (900, 2, (264, 136)), (64, 1, (2560, 768)), (3000, 1, (136, 72)),
+          (60, 130, (776, 776)), (150, 200, (72, 136)), (40, 60, (136, 776)), (90, 130, (520, 136)), (300, 60, (136, 264)),
+          (20, 300, (520, 520))]
+
+
+@pytest.mark.parametrize("rows,G,dims", SHAPES, ids=str)
+def test_grouped_tile_shapes(rows, G, dims):
+    """Groups around an average size, whichever tile shape that picks; every group checked."""
+    g = gen(22)
+    N, K = dims
+    counts = np.maximum(0, rows + torch.randint(-rows // 2, rows // 2 + 2, (G,), generator=g).numpy())
+    off, P = offsets_of(counts), int(counts.sum())
+    T = P // 2 + 1
+    x, w, dy = randn(g, T, K), randn(g, G, N, K), randn(g, T, N)
+    m = torch.randint(0, T, (P,), generator=g, dtype=torch.int32).cuda()
+    o, mn = off.cpu().numpy(), m.cpu().numpy()
+    y, dx = torch.zeros(P, N, device="cuda"), torch.zeros(P, K, dtype=BF, device="cuda")
+    dw = torch.ones(G, N, K, device="cuda")
+    moe.moe_grouped_gemm(x, w, off, y, row_map=m)
+    moe.moe_grouped_gemm_dgrad(dy, w, off, dx, row_map=m)
+    moe.moe_grouped_gemm_wgrad(dy, x, off, dw, dy_map=m, x_map=m, accumulate=True)
+    X, W, DY = f64(x), f64(w), f64(dy)
+    check(y, *orc.grouped_forward(X, W, o, np.zeros((P, N)), mn), K, False)
+    check(dx, *orc.grouped_dgrad(DY, W, o, np.zeros((P, K)), mn), N, True)
+    check(dw, *orc.grouped_wgrad(DY, X, o, np.ones((G, N, K)), mn, mn, True), int(counts.max()) + 1, False)
+
+
+def test_no_rows():
+    off = offsets_of([0, 0])
+    e = lambda n: torch.empty(0, n, dtype=BF, device="cuda")  # noqa: E731
+    w = torch.ones(2, 16, 24, dtype=BF, device="cuda")
+    moe.moe_grouped_gemm(e(24), w, off, e(16))
+    moe.moe_grouped_gemm_dgrad(e(16), w, off, e(24))
+    dw = torch.ones(2, 16, 24, device="cuda")
+    moe.moe_grouped_gemm_wgrad(e(16), e(24), off, dw, accumulate=True)
+    assert (dw == 1).all()
+    moe.moe_grouped_gemm_wgrad(e(16), e(24), off, dw)
+    assert not dw.any()
+    y = torch.ones(3, 16, dtype=BF, device="cuda")           # positions whose rows do not exist
+    moe.moe_grouped_gemm(e(24), w, offsets_of([1, 2]), y, row_map=torch.zeros(3, dtype=torch.int32, device="cuda"))
+    assert not y.any()
+    moe.moe_swiglu(e(8), e(8), e(8))
+    drow = torch.ones(2, device="cuda")
+    moe.moe_swiglu_backward(e(8), e(8), e(8), e(8), e(8), pos=torch.tensor([0, -1], dtype=torch.int32, device="cuda"), drow_w=drow)
+    assert not drow.any()
+
+
+def test_wrong_adamw_image_writes_nothing():
+    """The device copy of another plan is recognised by the kernel."""
+    mk = lambda n: moe.MoEAdamWPlan(*([torch.ones(n, device="cuda")] for _ in range(4)))  # noqa: E731
+    a, b = mk(100), mk(20000)
+    a.image = b.image
+    moe.moe_adamw_step(a, lr=1.0, step=1)
+    for p in (a, b):
+        assert all((t[0] == 1).all() for t in p._keep.values())
+
+
+class Step:
+    """The operators of one training step of a small layer, on buffers of its own."""
+
+    def __init__(self, seed, T=70, E=8, K=2, H=136, I=72, limit=3.0):
+        g = gen(seed)
+        self.T, self.K, self.E, self.limit = T, K, E, limit
+        idx = torch.stack([torch.randperm(E, generator=g)[:K].sort().values for _ in range(T)])
+        flat = idx.reshape(-1)
+        order = torch.argsort(flat, stable=True)
+        inv = torch.empty(T * K, dtype=torch.int32)
+        inv[order] = torch.arange(T * K, dtype=torch.int32)
+        self.offsets = offsets_of(torch.bincount(flat, minlength=E).numpy())
+        self.token, self.inv = (order // K).to(torch.int32).cuda(), inv.cuda()
+        self.idx = idx
+        self.w = (torch.rand(T * K, generator=g) + 0.2).cuda()
+        self.x, self.dout = randn(g, T, H), randn(g, T, H)
+        self.gate, self.up, self.down = (randn(g, E, *s, scale=s[1] ** -0.5) for s in ((I, H), (I, H), (H, I)))
+        P = T * K
+        bf, f32 = dict(dtype=BF, device="cuda"), dict(dtype=F32, device="cuda")
+        self.g, self.u, self.h, self.dh, self.dg, self.du = (torch.empty(P, I, **bf) for _ in range(6))
+        self.y, self.dx_sorted = torch.empty(P, H, **f32), torch.empty(P, H, **f32)
+        self.d_gate, self.d_up = torch.zeros(E, I, H, **f32), torch.zeros(E, I, H, **f32)
+        self.d_down, self.dw = torch.zeros(E, H, I, **f32), torch.empty(P, **f32)
+        self.out, self.dx = torch.empty(T, H, **bf), torch.empty(T, H, **bf)
+        params = [self.gate, self.up, self.down]
+        z = lambda: [torch.zeros(p.numel(), dtype=torch.uint8, device="cuda") for p in params]  # noqa: E731
+        sc = lambda: [torch.zeros(-(-p.numel() // 128), **f32) for p in params]  # noqa: E731
+        self.m, self.v, self.ms, self.vs = z(), z(), sc(), sc()
+        self.master = [p.float() for p in params]
+        self.step = torch.zeros(1, dtype=torch.int64, device="cuda")
+        self.plan = moe.MoEAdamWPlan(params, [self.d_gate, self.d_up, self.d_down], self.m, self.v, master=self.master,
+                                     exp_avg_scale=self.ms, exp_avg_sq_scale=self.vs, weight_decay=0.01)
+
+    def combine(self, rows, out):
+        # moe_combine takes layer sizes (multiples of 128 and 64); this layer's are odd, so torch sums
+        out.copy_(rows[self.inv.long()].view(self.T, self.K, -1).sum(1))
+
+    def forward(self):
+        moe.moe_grouped_gemm(self.x, self.gate, self.offsets, self.g, row_map=self.token)
+        moe.moe_grouped_gemm(self.x, self.up, self.offsets, self.u, row_map=self.token)
+        moe.moe_swiglu(self.g, self.u, self.h, limit=self.limit, row_w=self.w, pos=self.inv)
+        moe.moe_grouped_gemm(self.h, self.down, self.offsets, self.y)
+
+    def backward(self):
+        moe.moe_grouped_gemm_dgrad(self.dout, self.down, self.offsets, self.dh, row_map=self.token)
+        moe.moe_grouped_gemm_wgrad(self.dout, self.h, self.offsets, self.d_down, dy_map=self.token, accumulate=True)
+        moe.moe_swiglu_backward(self.g, self.u, self.dh, self.dg, self.du, limit=self.limit, row_w=self.w, pos=self.inv, drow_w=self.dw)
+        moe.moe_grouped_gemm_dgrad(self.dg, self.gate, self.offsets, self.dx_sorted, dy2=self.du, w2=self.up)
+        moe.moe_grouped_gemm_wgrad(self.dg, self.x, self.offsets, self.d_gate, x_map=self.token, accumulate=True)
+        moe.moe_grouped_gemm_wgrad(self.du, self.x, self.offsets, self.d_up, x_map=self.token, accumulate=True)
+
+    def update(self):
+        self.step.add_(1)
+        moe.moe_adamw_step(self.plan, lr=1e-3, step=self.step, seed=9)
+
+    def run(self):
+        for t in (self.d_gate, self.d_up, self.d_down):
+            t.zero_()
+        self.forward()
+        self.combine(self.y, self.out)
+        self.backward()
+        self.combine(self.dx_sorted, self.dx)
+        self.update()
+
+    def results(self):
+        return [self.out, self.dx, self.dw, self.d_gate, self.d_up, self.d_down, self.gate, self.up, self.down, *self.m, *self.v,
+                *self.ms, *self.vs, *self.master]
+
+
+def layer64(s, x, gate, up, down, w):
+    """The routed experts in float64, token by token and slot by slot."""
+    out = torch.zeros(s.T, x.shape[1], dtype=torch.float64)
+    for t in range(s.T):
+        for k in range(s.K):
+            e = int(s.idx[t, k])
+            a = torch.nn.functional.silu(gate[e] @ x[t]) * (up[e] @ x[t])
+            out[t] = out[t] + w[t * s.K + k] * (down[e] @ a.clamp(-s.limit, s.limit))
+    return out
+
+
+def test_training_step_of_a_layer():
+    """All operators in turn against float64 autograd and a difference along a random direction.  On
+    the way to any result at most six roundings to bf16 follow each other, each at most 2^-8 of its
+    value; the 2-norm of a result may be off by twice their sum."""
+    s = Step(30)
+    leaves = [t.double().cpu().requires_grad_() for t in (s.x, s.gate, s.up, s.down, s.w)]
+    loss_of = lambda *a: (layer64(s, *a) * s.dout.double().cpu()).sum()  # noqa: E731
+    want = layer64(s, *leaves)
+    (want * s.dout.double().cpu()).sum().backward()
+    s.run()
+    got = [s.dx, s.d_gate, s.d_up, s.d_down, s.dw]
+    bound = 2 * 6 * HALF_BF16
+    assert np.linalg.norm(f64(s.out) - want.detach().numpy()) <= bound * np.linalg.norm(want.detach().numpy())
+    g = gen(31)
+    for t, l in zip(got, leaves):
+        assert np.linalg.norm(f64(t) - l.grad.numpy()) <= bound * np.linalg.norm(l.grad.numpy())
+        d = torch.randn(l.shape, generator=g, dtype=torch.float64)
+        e = 1e-6
+        with torch.no_grad():
+            moved = [[(o + sgn * e * d if o is l else o) for o in leaves] for sgn in (1, -1)]
+            slope = ((loss_of(*moved[0]) - loss_of(*moved[1])) / (2 * e)).item()
+        dot = float((f64(t) * d.numpy()).sum())
+        # the direction's product errs by at most the gradient's error times the direction's length; the
+        # values that the clamp's border crosses within e move the quotient by less than 1e-3 of it
+        assert abs(dot - slope) <= bound * np.linalg.norm(l.grad.numpy()) * np.linalg.norm(d.numpy()) + 1e-3 * abs(slope)
+
+
+def test_training_step_is_deterministic():
+    a, b = Step(32), Step(32)
+    a.run()
+    b.run()
+    for x, y in zip(a.results(), b.results()):
+        assert torch.equal(x, y)
+
+
+def test_training_steps_in_a_graph():
+    """A captured step (its AdamW reading the step count from the device) replayed several times,
+    with eager work between the replays, against the same steps run eagerly."""
+    a, b = Step(33), Step(33)
+    eager = Step(34)
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        eager.run()                        # warm up, on other buffers
+    stream.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        a.run()
+    for _ in range(4):
+        graph.replay()
+        eager.run()
+        b.run()
+        torch.cuda.synchronize()
+        for x, y in zip(a.results(), b.results()):
+            assert torch.equal(x, y)
+
+
+def test_two_steps_on_two_streams():
+    """Two layers' steps enqueued at once on two streams: the results of each alone."""
+    solo = [Step(s, T=300) for s in (35, 36)]
+    for s in solo:
+        s.run()
+    torch.cuda.synchronize()
+    both = [Step(s, T=300) for s in (35, 36)]
+    streams = [torch.cuda.Stream() for _ in both]
+    torch.cuda.synchronize()
+    for s, st in zip(both, streams):
+        with torch.cuda.stream(st):
+            s.run()
+    torch.cuda.synchronize()
+    for s, t in zip(solo, both):
+        for x, y in zip(s.results(), t.results()):
+            assert torch.equal(x, y)
+
+
+def test_given_stream_is_used():
+    """stream= orders a call after that stream's work, not after the current one's."""
+    st = torch.cuda.Stream()
+    s = Step(37)
+    torch.cuda.synchronize()
+    big = torch.randn(4096, 4096, device="cuda")
+    src = torch.zeros_like(s.x)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(st):
+        for _ in range(5):
+            big = big @ big
+        src.copy_(s.x)                     # ready only after the products on `st`
+    y = torch.empty_like(s.g)
+    moe.moe_grouped_gemm(src, s.gate, s.offsets, y, row_map=s.token, stream=st)
+    st.synchronize()
+    s.forward()
+    torch.cuda.synchronize()
+    assert torch.equal(y, s.g)
+
+
+def test_layer_with_shared_expert_matches_moe_forward():
+    """The forward of the training operators, shared expert included, on the layer's own routing,
+    dispatch and combine, against moe_forward.  Both round on the way (here gate, up and h to bf16,
+    there h and y to fp16), so the outputs differ by at most twice four roundings of 2^-8 in the
+    2-norm; the combine is moe_combine with weights of one."""
+    from moe_case import cfg_for
+    from synthetic import CONFIGS
+    sc = CONFIGS["tiny"]
+    cfg, T, H, I, E, K = cfg_for(sc), 50, sc.H, sc.I, sc.E, sc.K
+    g = gen(38)
+    x, rw = randn(g, T, H), randn(g, E, H, dtype=F32, scale=H ** -0.5)
+    gate, up, down = randn(g, E, I, H, scale=H ** -0.5), randn(g, E, I, H, scale=H ** -0.5), randn(g, E, H, I, scale=I ** -0.5)
+    sg, su, sd = randn(g, I, H, scale=H ** -0.5), randn(g, I, H, scale=H ** -0.5), randn(g, H, I, scale=I ** -0.5)
+    ws = torch.empty(moe.moe_workspace_size(cfg, T), dtype=torch.uint8, device="cuda")
+    want = torch.empty(T, H, dtype=BF, device="cuda")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    idx, w = torch.empty(T, K, **i32), torch.empty(T, K, device="cuda")
+    moe.moe_forward(cfg, T, x, rw, None, moe.MoEExpertWeights(gate, up, down, shared_gate=sg, shared_up=su, shared_down=sd),
+                    want, idx, w, None, ws)
+    P = T * K + T
+    counts, off = torch.empty(E + 1, **i32), torch.empty(E + 2, **i32)
+    token, inv = torch.empty(P, **i32), torch.empty(T, K, **i32)
+    moe.moe_dispatch(cfg, T, idx, counts, off, token, inv, ws)
+    gb, ub, hb = (torch.empty(P, I, dtype=BF, device="cuda") for _ in range(3))
+    y = torch.empty(P, H, device="cuda")
+    for o, wg, wu, wd in ((off[:E + 1], gate, up, down), (off[E:], sg[None], su[None], sd[None])):
+        moe.moe_grouped_gemm(x, wg, o, gb, row_map=token)
+        moe.moe_grouped_gemm(x, wu, o, ub, row_map=token)
+    moe.moe_swiglu(gb, ub, hb, row_w=w.view(-1), pos=inv.view(-1))
+    moe.moe_swiglu(gb[T * K:], ub[T * K:], hb[T * K:])
+    for o, wd in ((off[:E + 1], down), (off[E:], sd[None])):
+        moe.moe_grouped_gemm(hb, wd, o, y)
+    out = torch.empty_like(want)
+    moe.moe_combine(cfg, T, y, inv, torch.ones_like(w), out)
+    assert np.linalg.norm(f64(out) - f64(want)) <= 2 * 4 * HALF_BF16 * np.linalg.norm(f64(want))
+    moe.moe_update_expert_bias(cfg, counts, torch.zeros(E, device="cuda"), 1e-3)
+    torch.cuda.synchronize()
