@@ -327,28 +327,82 @@ def _torch():
     return _torch_module
 
 
-def _enqueue(fn, tensors, stream, *args):
-    """fn(*args, stream) with the tensors' device current; its current stream unless one is given
-    (which must belong to it)."""
+def _enqueue(fn, dev, stream, *args):
+    """fn(*args, stream) with device `dev`, which holds the tensors, current; its current stream
+    unless one is given (which must belong to it)."""
+    if dev < 0:
+        _refuse("tensors must lie on a GPU")
     torch = _torch()
-    dev = -2
-    for t in tensors:
-        if t is not None:
-            d = t.get_device()
-            if dev == -2:
-                dev = d
-            if d != dev or d < 0:
-                devices = sorted({str(x.device) for x in tensors if x is not None})
-                _refuse(f"tensors lie on several devices: {devices}" if len(devices) > 1 else
-                        f"tensors must lie on a GPU, not on {devices[0]}")
-    given = getattr(stream, "device", None)
-    if given is not None and given.index != dev:
-        _refuse(f"stream belongs to {given}, tensors lie on cuda:{dev}")
+    if stream is not None:
+        given = getattr(stream, "device", None)
+        if given is not None and given.index != dev:
+            _refuse(f"stream belongs to {given}, tensors lie on cuda:{dev}")
+        stream = _stream(stream)
+    else:
+        stream = _raw_stream(dev)
     if torch.cuda.current_device() == dev:
-        _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream if stream is None else _stream(stream)))
+        status = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
-            _check(fn(*args, _stream(stream)))
+            status = fn(*args, stream)
+    if status:
+        _check(status)
+
+
+def _raw_stream(dev):
+    """Handle of the device's current stream."""
+    torch = _torch()
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return get(dev) if get is not None else torch.cuda.current_stream(dev).cuda_stream
+
+
+def _device_of(t, name):
+    """Index of the GPU that holds t (-1: none; refused once everything else is in order)."""
+    if not isinstance(t, _torch().Tensor):
+        _refuse(f"{name} must be a tensor")
+    return t.get_device()
+
+
+def _explain(t, name, dtype, dim, dev):
+    """Refuses t: why it is not a tensor of that type and dimension on that device."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        _refuse(f"{name} must be a tensor")
+    if dtype is not None and t.dtype is not dtype:
+        _refuse(f"{name} must be {dtype}, not {t.dtype}")
+    if t.dim() != dim:
+        _refuse(f"{name} must have {dim} dimension(s), not {t.dim()}")
+    _refuse(f"{name} lies on {t.device}, the others on {f'cuda:{dev}' if dev >= 0 else 'the CPU'}")
+
+
+def _matrix(t, name, dtype, dev):
+    """(rows, columns, row stride) of a matrix whose columns lie side by side."""
+    if (dtype is not None and t.dtype is not dtype) or t.dim() != 2 or t.get_device() != dev:
+        _explain(t, name, dtype, 2, dev)
+    rows, cols = t.shape
+    ld, unit = t.stride()
+    if unit != 1 and cols > 1:
+        _refuse(f"{name}: the values of a row must lie side by side")
+    return rows, cols, ld if rows > 1 else (cols + 7) // 8 * 8
+
+
+def _vector(t, name, dtype, n, dev):
+    if t.dtype is not dtype or t.dim() != 1 or t.get_device() != dev:
+        _explain(t, name, dtype, 1, dev)
+    size = t.shape[0]
+    if n is not None and size != n:
+        _refuse(f"{name} has {size} entries, {n} needed")
+    if size > 1 and t.stride(0) != 1:
+        _refuse(f"{name} must be contiguous")
+    return size
+
+
+def _weights3(t, name, dtype, dev):
+    if (dtype is not None and t.dtype is not dtype) or t.dim() != 3 or t.get_device() != dev:
+        _explain(t, name, dtype, 3, dev)
+    if not t.is_contiguous():
+        _refuse(f"{name} must be contiguous")
+    return t.shape
 
 
 def _dtype_code(t, name):
@@ -360,155 +414,113 @@ def _dtype_code(t, name):
     return MOE_DTYPE_FP32
 
 
-def _typed(t, name, dtype, dim):
+def _operand(t, name, cols, row_map, positions, dev):
     torch = _torch()
-    if not isinstance(t, torch.Tensor):
-        _refuse(f"{name} must be a tensor")
-    if dtype is not None and t.dtype is not dtype:
-        _refuse(f"{name} must be {dtype}, not {t.dtype}")
-    if t.dim() != dim:
-        _refuse(f"{name} must have {dim} dimension(s), not {t.dim()}")
-
-
-def _matrix(t, name, dtype=None):
-    """Row stride of a [rows, columns] tensor whose columns lie side by side."""
-    _typed(t, name, dtype, 2)
-    rows, cols = t.shape
-    ld, unit = t.stride()
-    if cols > 1 and unit != 1:
-        _refuse(f"{name}: the values of a row must lie side by side")
-    return ld if rows > 1 else (cols + 7) // 8 * 8
-
-
-def _vector(t, name, dtype, n=None):
-    _typed(t, name, dtype, 1)
-    if t.shape[0] > 1 and t.stride(0) != 1:
-        _refuse(f"{name} must be contiguous")
-    if n is not None and t.shape[0] != n:
-        _refuse(f"{name} has {t.shape[0]} entries, {n} needed")
-
-
-def _weights3(t, name):
-    _typed(t, name, _torch().bfloat16, 3)
-    if not t.is_contiguous():
-        _refuse(f"{name} must be contiguous")
-
-
-def _groups(offsets, groups, n, k, rows):
-    _vector(offsets, "offsets", _torch().int32, groups + 1)
-    return _Groups(groups, n, k, rows, offsets.data_ptr())
-
-
-def _operand(t, name, cols, row_map, positions):
-    torch = _torch()
-    ld = _matrix(t, name, torch.bfloat16)
-    rows, c = t.shape
+    rows, c, ld = _matrix(t, name, torch.bfloat16, dev)
     if c != cols:
         _refuse(f"{name} has {c} columns, {cols} needed")
+    at = None
     if row_map is not None:
-        _vector(row_map, f"the row map of {name}", torch.int32, positions)
-    return _Rows(t.data_ptr() if rows else None, rows, ld, None if row_map is None else row_map.data_ptr())
+        _vector(row_map, f"the row map of {name}", torch.int32, positions, dev)
+        at = row_map.data_ptr()
+    return _Rows(t.data_ptr() if rows else None, rows, ld, at)
 
 
 def moe_grouped_gemm(x, w, offsets, y, row_map=None, accumulate=False, stream=None):
     """y[p] = w[g] x[row_map[p]] for the positions offsets[g] <= p < offsets[g+1] of every group g:
     x bf16 [.., in], w bf16 [G, out, in], offsets int32 [G+1], y bf16 or fp32 [P, out] (added to
     with accumulate, fp32 only), row_map int32 [P] (None: position p is row p)."""
-    _weights3(w, "w")
-    ldy = _matrix(y, "y")
-    G, N, K = w.shape
-    P, cols = y.shape
+    torch, dev = _torch(), _device_of(w, "w")
+    G, N, K = _weights3(w, "w", torch.bfloat16, dev)
+    P, cols, ldy = _matrix(y, "y", None, dev)
     if cols != N:
         _refuse(f"y has {cols} columns, w makes {N}")
-    g, a = _groups(offsets, G, N, K, P), _operand(x, "x", K, row_map, P)
-    _enqueue(load_library().moe_grouped_gemm, (x, w, offsets, y, row_map), stream, ctypes.byref(g), ctypes.byref(a),
-             w.data_ptr(), y.data_ptr(), ldy, _dtype_code(y, "y"), 1 if accumulate else 0)
+    _vector(offsets, "offsets", torch.int32, G + 1, dev)
+    _enqueue(load_library().moe_grouped_gemm, dev, stream, _Groups(G, N, K, P, offsets.data_ptr()),
+             _operand(x, "x", K, row_map, P, dev), w.data_ptr(), y.data_ptr(), ldy, _dtype_code(y, "y"), 1 if accumulate else 0)
 
 
 def moe_grouped_gemm_dgrad(dy, w, offsets, dx, row_map=None, dy2=None, w2=None, accumulate=False, stream=None):
     """dx[p] = dy[row_map[p]] w[g] (+ dy2[row_map[p]] w2[g]): dy bf16 [.., out], w bf16 [G, out, in],
     dx bf16 or fp32 [P, in]; dy2 has dy's rows and row stride."""
-    _weights3(w, "w")
-    lddx = _matrix(dx, "dx")
-    G, N, K = w.shape
-    P, cols = dx.shape
+    torch, dev = _torch(), _device_of(w, "w")
+    G, N, K = shape = _weights3(w, "w", torch.bfloat16, dev)
+    P, cols, lddx = _matrix(dx, "dx", None, dev)
     if cols != K:
         _refuse(f"dx has {cols} columns, w makes {K}")
     if (dy2 is None) != (w2 is None):
         _refuse("dy2 and w2 must be given together")
-    g, a, b, pw2 = _groups(offsets, G, N, K, P), _operand(dy, "dy", N, row_map, P), None, None
+    _vector(offsets, "offsets", torch.int32, G + 1, dev)
+    b, pw2 = None, None
     if w2 is not None:
-        _weights3(w2, "w2")
-        if w2.shape != w.shape:
-            _refuse(f"w2 is {tuple(w2.shape)}, w is {tuple(w.shape)}")
-        b, pw2 = ctypes.byref(_operand(dy2, "dy2", N, row_map, P)), w2.data_ptr()
-    _enqueue(load_library().moe_grouped_gemm_dgrad, (dy, w, offsets, dx, row_map, dy2, w2), stream, ctypes.byref(g),
-             ctypes.byref(a), w.data_ptr(), b, pw2, dx.data_ptr(), lddx, _dtype_code(dx, "dx"), 1 if accumulate else 0)
+        if _weights3(w2, "w2", torch.bfloat16, dev) != shape:
+            _refuse(f"w2 is {tuple(w2.shape)}, w is {tuple(shape)}")
+        b, pw2 = _operand(dy2, "dy2", N, row_map, P, dev), w2.data_ptr()
+    _enqueue(load_library().moe_grouped_gemm_dgrad, dev, stream, _Groups(G, N, K, P, offsets.data_ptr()),
+             _operand(dy, "dy", N, row_map, P, dev), w.data_ptr(), b, pw2, dx.data_ptr(), lddx, _dtype_code(dx, "dx"),
+             1 if accumulate else 0)
 
 
 def moe_grouped_gemm_wgrad(dy, x, offsets, dw, dy_map=None, x_map=None, accumulate=False, stream=None):
     """dw[g] = sum over group g's positions of dy[dy_map[p]]^T x[x_map[p]]: dy bf16 [.., out], x bf16
     [.., in], dw bf16 or fp32 [G, out, in] (added to with accumulate, fp32 only)."""
-    _typed(dw, "dw", None, 3)
-    if not dw.is_contiguous():
-        _refuse("dw must be contiguous")
-    G, N, K = dw.shape
+    torch, dev = _torch(), _device_of(dw, "dw")
+    G, N, K = _weights3(dw, "dw", None, dev)
     P, px = (t.shape[0] if m is None else m.shape[0] for t, m in ((dy, dy_map), (x, x_map)))
     if P != px:
         _refuse(f"dy and x cover different numbers of positions: {P} and {px}")
-    g = _groups(offsets, G, N, K, P)
-    a, b = _operand(dy, "dy", N, dy_map, P), _operand(x, "x", K, x_map, P)
-    _enqueue(load_library().moe_grouped_gemm_wgrad, (dy, x, offsets, dw, dy_map, x_map), stream, ctypes.byref(g),
-             ctypes.byref(a), ctypes.byref(b), dw.data_ptr(), _dtype_code(dw, "dw"), 1 if accumulate else 0)
+    _vector(offsets, "offsets", torch.int32, G + 1, dev)
+    _enqueue(load_library().moe_grouped_gemm_wgrad, dev, stream, _Groups(G, N, K, P, offsets.data_ptr()),
+             _operand(dy, "dy", N, dy_map, P, dev), _operand(x, "x", K, x_map, P, dev), dw.data_ptr(), _dtype_code(dw, "dw"),
+             1 if accumulate else 0)
 
 
-def _like(shape, t, name):
-    """Row stride of a bf16 matrix of that shape."""
-    ld = _matrix(t, name, _torch().bfloat16)
-    if t.shape != shape:
-        _refuse(f"{name} is {tuple(t.shape)}, gate is {tuple(shape)}")
+def _like(first, t, name, dev):
+    """Row stride of a bf16 matrix with the rows and columns of gate (`first`)."""
+    rows, cols, ld = _matrix(t, name, _torch().bfloat16, dev)
+    if rows != first[0] or cols != first[1]:
+        _refuse(f"{name} is [{rows}, {cols}], gate is [{first[0]}, {first[1]}]")
     return ld
 
 
-def _pairs(row_w, pos, rows):
-    """Number of rows handled: that of the positions or weights given, else all."""
+def _pairs(row_w, pos, rows, dev):
+    """Rows handled (those of the positions or weights given, else all), the two addresses."""
     torch = _torch()
-    n = rows
+    n, pw, pp = None, None, None
     if pos is not None:
-        _vector(pos, "pos", torch.int32)
-        n = pos.shape[0]
+        n, pp = _vector(pos, "pos", torch.int32, None, dev), pos.data_ptr()
     if row_w is not None:
-        _vector(row_w, "row_w", torch.float32, None if pos is None else n)
-        n = row_w.shape[0]
-    return n
+        n, pw = _vector(row_w, "row_w", torch.float32, n, dev), row_w.data_ptr()
+    return rows if n is None else n, pw, pp
 
 
 def moe_swiglu(gate, up, h, limit=0.0, row_w=None, pos=None, stream=None):
     """h[pos[i]] = row_w[i] * clamp(silu(gate[pos[i]]) * up[pos[i]], -limit, limit): gate, up, h bf16
     [R, C]; row_w fp32 [n] (None: 1), pos int32 [n], distinct (None: row i), entries outside [0, R)
     skipped; limit <= 0: no clamp."""
-    ld, shape = _matrix(gate, "gate", _torch().bfloat16), gate.shape
-    if _like(shape, up, "up") != ld:
+    dev = _device_of(gate, "gate")
+    R, C, ld = first = _matrix(gate, "gate", _torch().bfloat16, dev)
+    if _like(first, up, "up", dev) != ld:
         _refuse("gate and up must have the same row stride")
-    ldh, (R, C), n = _like(shape, h, "h"), shape, _pairs(row_w, pos, shape[0])
-    _enqueue(load_library().moe_swiglu, (gate, up, h, row_w, pos), stream, n, R, C, float(limit), gate.data_ptr(),
-             up.data_ptr(), ld, _ptr(row_w), _ptr(pos), h.data_ptr(), ldh)
+    ldh, (n, pw, pp) = _like(first, h, "h", dev), _pairs(row_w, pos, R, dev)
+    _enqueue(load_library().moe_swiglu, dev, stream, n, R, C, float(limit), gate.data_ptr(), up.data_ptr(), ld, pw, pp, h.data_ptr(), ldh)
 
 
 def moe_swiglu_backward(gate, up, dh, dgate, dup, limit=0.0, row_w=None, pos=None, drow_w=None, stream=None):
     """Gradients of moe_swiglu from dh: dgate, dup bf16 [R, C], drow_w fp32 [n] (None: not wanted)."""
-    ld, shape = _matrix(gate, "gate", _torch().bfloat16), gate.shape
-    if _like(shape, up, "up") != ld:
+    torch, dev = _torch(), _device_of(gate, "gate")
+    R, C, ld = first = _matrix(gate, "gate", torch.bfloat16, dev)
+    if _like(first, up, "up", dev) != ld:
         _refuse("gate and up must have the same row stride")
-    lddh, ldd = _like(shape, dh, "dh"), _like(shape, dgate, "dgate")
-    if _like(shape, dup, "dup") != ldd:
+    lddh, ldd = _like(first, dh, "dh", dev), _like(first, dgate, "dgate", dev)
+    if _like(first, dup, "dup", dev) != ldd:
         _refuse("dgate and dup must have the same row stride")
-    (R, C), n = shape, _pairs(row_w, pos, shape[0])
+    (n, pw, pp), pd = _pairs(row_w, pos, R, dev), None
     if drow_w is not None:
-        _vector(drow_w, "drow_w", _torch().float32, n)
-    _enqueue(load_library().moe_swiglu_backward, (gate, up, dh, dgate, dup, row_w, pos, drow_w), stream, n, R, C,
-             float(limit), gate.data_ptr(), up.data_ptr(), ld, dh.data_ptr(), lddh, _ptr(row_w), _ptr(pos),
-             dgate.data_ptr(), dup.data_ptr(), ldd, _ptr(drow_w))
+        _vector(drow_w, "drow_w", torch.float32, n, dev)
+        pd = drow_w.data_ptr()
+    _enqueue(load_library().moe_swiglu_backward, dev, stream, n, R, C, float(limit), gate.data_ptr(), up.data_ptr(), ld, dh.data_ptr(),
+             lddh, pw, pp, dgate.data_ptr(), dup.data_ptr(), ldd, pd)
 
 
 class MoEAdamWPlan:
@@ -548,11 +560,13 @@ class MoEAdamWPlan:
                 want = -(-want // 128) if name.endswith("scale") else want
                 if t.numel() != want:
                     _refuse(f"{name}[{i}] has {t.numel()} values, {want} needed")
-                if t.device != device or not t.is_cuda:
-                    _refuse(f"{name}[{i}] lies on {t.device}, params[0] on {device}; one GPU must hold them all")
         decay = list(weight_decay) if hasattr(weight_decay, "__len__") else [weight_decay] * n
         if len(decay) != n:
             _refuse(f"weight_decay has {len(decay)} entries, params {n}")
+        for name, ts in cols.items():
+            for i, t in enumerate(ts):
+                if t.device != device or not t.is_cuda:
+                    _refuse(f"{name}[{i}] lies on {t.device}; one GPU must hold them all")
         self._keep, self.device = cols, device
         table = (_AdamWTensor * n)()
         field = {"params": "param", "grads": "grad"}
@@ -575,29 +589,26 @@ def moe_adamw_step(plan: MoEAdamWPlan, lr, step, betas=(0.9, 0.999), eps=1e-8, s
     """One AdamW step over the plan's tensors, in place.  lr and step (1 for the first) are numbers,
     or device tensors (fp32, int64) read when the step runs; grad_scale an fp32 device tensor that
     multiplies every gradient; seed that of the 8-bit states' stochastic rounding."""
-    torch = _torch()
+    torch, dev = _torch(), plan.device.index
     cfg = _AdamWConfig(beta1=betas[0], beta2=betas[1], eps=eps, seed=seed & 0xFFFFFFFF)
-    given = [plan.image]
     for name, v, dtype in (("lr", lr, torch.float32), ("step", step, torch.int64), ("grad_scale", grad_scale, torch.float32)):
         if isinstance(v, torch.Tensor):
-            if v.dtype != dtype or v.numel() != 1:
-                _refuse(f"{name} must hold one {dtype} value")
-            given.append(v)
+            if v.dtype != dtype or v.numel() != 1 or v.get_device() != dev:
+                _refuse(f"{name} must hold one {dtype} value on {plan.device}")
             setattr(cfg, name if name == "grad_scale" else name + "_ptr", v.data_ptr())
         elif name != "grad_scale":
             setattr(cfg, name, v)
         elif v is not None:
             _refuse("grad_scale must be a device tensor")
-    _enqueue(load_library().moe_adamw_step, given, stream, ctypes.byref(cfg), ctypes.byref(plan.struct), plan.image.data_ptr())
+    _enqueue(load_library().moe_adamw_step, dev, stream, cfg, plan.struct, plan.image.data_ptr())
 
 
 def moe_adamw_dequantise(codes, scales, out, signed, stream=None):
     """Values of an 8-bit state array: codes uint8 [n], scales fp32 [ceil(n / 128)] -> out fp32 [n];
     signed: exp_avg's codes, else exp_avg_sq's."""
-    torch = _torch()
-    _vector(codes, "codes", torch.uint8)
-    n = codes.shape[0]
-    _vector(scales, "scales", torch.float32, -(-n // 128))
-    _vector(out, "out", torch.float32, n)
-    _enqueue(load_library().moe_adamw_dequantise, (codes, scales, out), stream, codes.data_ptr(), scales.data_ptr(), n,
-             1 if signed else 0, out.data_ptr())
+    torch, dev = _torch(), _device_of(codes, "codes")
+    n = _vector(codes, "codes", torch.uint8, None, dev)
+    _vector(scales, "scales", torch.float32, -(-n // 128), dev)
+    _vector(out, "out", torch.float32, n, dev)
+    _enqueue(load_library().moe_adamw_dequantise, dev, stream, codes.data_ptr(), scales.data_ptr(), n, 1 if signed else 0,
+             out.data_ptr())

@@ -195,33 +195,50 @@ def i32(*v):
     return torch.tensor(v, dtype=torch.int32)
 
 
+def u8(n):
+    return torch.zeros(n, dtype=torch.uint8)
+
+
+OFF = i32(0, 2, 4)
+
+
 @needs_lib
-@pytest.mark.parametrize("call", [
-    lambda: moe.moe_grouped_gemm(bf(4, 16), bf(2, 8, 16), i32(0, 2, 4), bf(4, 8)),                       # not on a GPU
-    lambda: moe.moe_grouped_gemm(bf(4, 16), bf(2, 8, 24), i32(0, 2, 4), bf(4, 8)),                       # columns
-    lambda: moe.moe_grouped_gemm(bf(4, 16), bf(2, 8, 16), i32(0, 4), bf(4, 8)),                          # offsets
-    lambda: moe.moe_grouped_gemm(bf(4, 16), bf(2, 8, 16), i32(0, 2, 4).long(), bf(4, 8)),
-    lambda: moe.moe_grouped_gemm(bf(4, 16).float(), bf(2, 8, 16), i32(0, 2, 4), bf(4, 8)),
-    lambda: moe.moe_grouped_gemm(bf(4, 16), bf(2, 16, 8).transpose(1, 2), i32(0, 2, 4), bf(4, 8)),
-    lambda: moe.moe_grouped_gemm(bf(16, 4).t(), bf(2, 8, 16), i32(0, 2, 4), bf(4, 8)),
-    lambda: moe.moe_grouped_gemm(bf(4, 16), bf(2, 8, 16), i32(0, 2, 4), bf(4, 8), row_map=i32(0, 1)),
-    lambda: moe.moe_grouped_gemm(bf(4, 16), bf(2, 8, 16), i32(0, 2, 4), bf(4, 16)),
-    lambda: moe.moe_grouped_gemm_dgrad(bf(4, 8), bf(2, 8, 16), i32(0, 2, 4), bf(4, 16), dy2=bf(4, 8)),
-    lambda: moe.moe_grouped_gemm_dgrad(bf(4, 8), bf(2, 8, 16), i32(0, 2, 4), bf(4, 16), dy2=bf(4, 8), w2=bf(2, 16, 16)),
-    lambda: moe.moe_grouped_gemm_wgrad(bf(4, 8), bf(5, 16), i32(0, 2, 4), bf(2, 8, 16)),
-    lambda: moe.moe_swiglu(bf(4, 8), bf(4, 16), bf(4, 8)),
-    lambda: moe.moe_swiglu(bf(4, 8), bf(4, 8), bf(4, 8), row_w=torch.zeros(3), pos=i32(0, 1)),
-    lambda: moe.moe_swiglu_backward(bf(4, 8), bf(4, 8), bf(4, 8), bf(4, 8), bf(4, 16)[:, :8]),
-    lambda: moe.MoEAdamWPlan([bf(8)], [bf(9)], [bf(8).float()], [bf(8).float()]),
-    lambda: moe.MoEAdamWPlan([bf(8)], [bf(8)], [bf(8).float()], [bf(8)]),
-    lambda: moe.MoEAdamWPlan([bf(8)], [bf(8)], [torch.zeros(8, dtype=torch.uint8)], [torch.zeros(8, dtype=torch.uint8)]),
-    lambda: moe.MoEAdamWPlan([], [], [], []),
-    lambda: moe.moe_adamw_dequantise(torch.zeros(129, dtype=torch.uint8), torch.zeros(1), torch.zeros(129), True),
+@pytest.mark.parametrize("call,words", [
+    (lambda: moe.moe_grouped_gemm(bf(4, 16), bf(2, 8, 16), OFF, bf(4, 8)), "must lie on a GPU"),
+    (lambda: moe.moe_grouped_gemm(bf(4, 16), bf(2, 8, 24), OFF, bf(4, 8)), "x has 16 columns, 24 needed"),
+    (lambda: moe.moe_grouped_gemm(bf(4, 16), bf(2, 8, 16), i32(0, 4), bf(4, 8)), "offsets has 2 entries, 3 needed"),
+    (lambda: moe.moe_grouped_gemm(bf(4, 16), bf(2, 8, 16), OFF.long(), bf(4, 8)), "offsets must be torch.int32"),
+    (lambda: moe.moe_grouped_gemm(bf(4, 16).float(), bf(2, 8, 16), OFF, bf(4, 8)), "x must be torch.bfloat16"),
+    (lambda: moe.moe_grouped_gemm(bf(4, 16), bf(2, 16, 8).transpose(1, 2), OFF, bf(4, 8)), "w must be contiguous"),
+    (lambda: moe.moe_grouped_gemm(bf(16, 4).t(), bf(2, 8, 16), OFF, bf(4, 8)), "side by side"),
+    (lambda: moe.moe_grouped_gemm(bf(4, 16), bf(2, 8, 16), OFF, bf(4, 8), row_map=i32(0, 1)), "row map of x has 2 entries"),
+    (lambda: moe.moe_grouped_gemm(bf(4, 16), bf(2, 8, 16), OFF, bf(4, 16)), "y has 16 columns, w makes 8"),
+    (lambda: moe.moe_grouped_gemm(bf(4, 16), bf(2, 8, 16), OFF, bf(4, 8).half()), "y must be bfloat16 or float32"),
+    (lambda: moe.moe_grouped_gemm(bf(4, 16), bf(8, 16), OFF, bf(4, 8)), "w must have 3 dimension"),
+    (lambda: moe.moe_grouped_gemm(bf(4, 16), None, OFF, bf(4, 8)), "w must be a tensor"),
+    (lambda: moe.moe_grouped_gemm(bf(4, 16), bf(2, 8, 16), OFF, bf(4, 8), stream=torch.device("cpu")), "must lie on a GPU"),
+    (lambda: moe.moe_grouped_gemm_dgrad(bf(4, 8), bf(2, 8, 16), OFF, bf(4, 16), dy2=bf(4, 8)), "given together"),
+    (lambda: moe.moe_grouped_gemm_dgrad(bf(4, 8), bf(2, 8, 16), OFF, bf(4, 16), dy2=bf(4, 8), w2=bf(2, 16, 16)), "w2 is"),
+    (lambda: moe.moe_grouped_gemm_dgrad(bf(4, 8), bf(2, 8, 16), OFF, bf(4, 8)), "dx has 8 columns"),
+    (lambda: moe.moe_grouped_gemm_wgrad(bf(4, 8), bf(5, 16), OFF, bf(2, 8, 16)), "different numbers of positions"),
+    (lambda: moe.moe_grouped_gemm_wgrad(bf(4, 8), bf(4, 24), OFF, bf(2, 8, 16)), "x has 24 columns"),
+    (lambda: moe.moe_swiglu(bf(4, 8), bf(4, 16), bf(4, 8)), "up is [4, 16], gate is [4, 8]"),
+    (lambda: moe.moe_swiglu(bf(4, 8), bf(4, 16)[:, :8], bf(4, 8)), "same row stride"),
+    (lambda: moe.moe_swiglu(bf(4, 8), bf(4, 8), bf(4, 8), row_w=torch.zeros(3), pos=i32(0, 1)), "row_w has 3 entries, 2 needed"),
+    (lambda: moe.moe_swiglu_backward(bf(4, 8), bf(4, 8), bf(4, 8), bf(4, 8), bf(4, 16)[:, :8]), "dgate and dup"),
+    (lambda: moe.moe_swiglu_backward(bf(4, 8), bf(4, 8), bf(4, 8), bf(4, 8), bf(4, 8), drow_w=torch.zeros(3)), "drow_w has 3"),
+    (lambda: moe.MoEAdamWPlan([bf(8)], [bf(9)], [bf(8).float()], [bf(8).float()]), "grads[0] has 9 values, 8 needed"),
+    (lambda: moe.MoEAdamWPlan([bf(8)], [bf(8)], [bf(8).float()], [bf(8)]), "exp_avg_sq[0] must be torch.float32"),
+    (lambda: moe.MoEAdamWPlan([bf(8)], [bf(8)], [u8(8)], [u8(8)]), "scales belong to uint8 states"),
+    (lambda: moe.MoEAdamWPlan([bf(8)], [bf(8)], [bf(8).float()], [bf(8).float()]), "one GPU must hold them all"),
+    (lambda: moe.MoEAdamWPlan([], [], [], []), "params must not be empty"),
+    (lambda: moe.moe_adamw_dequantise(u8(129), torch.zeros(1), torch.zeros(129), True), "scales has 1 entries, 2 needed"),
 ])
-def test_binding_refusals(call):
+def test_binding_refusals(call, words):
     with pytest.raises(moe.MoEError) as e:
         call()
     assert e.value.status in (INVALID, UNSUPPORTED)
+    assert words in str(e.value)
 
 
 # ---- the definitions -----------------------------------------------------------------------------
