@@ -39,8 +39,9 @@ __device__ __forceinline__ uint32_t dpp_max16(uint32_t v) {
 }
 
 // 32 random bits of a pair of values: an index hash of multiplications by odd constants and shifts
-__device__ __forceinline__ uint32_t pair_bits(uint32_t pair, uint32_t key) {
-  uint32_t x = pair * 0x8DA6B343u + key;
+// (`x`: pair * HASH_STEP + key, which the pairs of a lane reach by additions)
+constexpr uint32_t HASH_STEP = 0x8DA6B343u;
+__device__ __forceinline__ uint32_t pair_bits(uint32_t x) {
   x ^= x >> 15;
   x *= 0xD8163841u;
   x ^= x >> 13;
@@ -60,11 +61,16 @@ __device__ __forceinline__ float decode(uint32_t c, float scale) {
   }
 }
 
+// A code still among the bits above it (bits 8 and up are not cleared): |x| / scale with 16 random
+// bits added below the kept ones.  The bias of the exponent field is no more than set bits above
+// the code (and its bit 7, which the sign replaces), so nothing is subtracted.
 template <bool SIGNED>
 __device__ __forceinline__ uint32_t encode(float x, float inv, uint32_t r16) {
-  const int bits = __float_as_int(fabsf(x) * inv) + (int)(r16 << 4);
-  const int c = min(max((bits >> 20) - (SIGNED ? M_BIAS : V_BIAS), 0), SIGNED ? 127 : 255);
-  return SIGNED ? (uint32_t)c | ((__float_as_uint(x) >> 24) & 128u) : (uint32_t)c;
+  static_assert(V_BIAS == 0x300 && M_BIAS == 0x380, "the biases lie above the codes");
+  constexpr int LO = SIGNED ? M_BIAS : V_BIAS, HI = LO + (SIGNED ? 127 : 255);
+  const int bits = (__float_as_int(fabsf(x) * inv) + (int)(r16 << 4)) >> 20;
+  const uint32_t c = (uint32_t)min(max(bits, LO), HI);
+  return SIGNED ? (c & 0x7Fu) | (__float_as_uint(x) >> 24 & ~0x7Fu) : c;
 }
 
 // eight values -> their block's scale, the codes in two words
@@ -78,13 +84,15 @@ __device__ __forceinline__ float encode8(const float (&x)[8], const uint32_t (&r
   const float inv = scale > 0.f ? 1.0f / scale : 0.f;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    uint32_t w = 0;
+    uint32_t c[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const uint32_t r = rnd[h * 2 + j / 2];
-      w |= encode<SIGNED>(x[h * 4 + j], inv, j & 1 ? r >> 16 : r & 0xFFFFu) << (8 * j);
+      c[j] = encode<SIGNED>(x[h * 4 + j], inv, j & 1 ? r >> 16 : r & 0xFFFFu);
     }
-    codes[h] = w;
+    // the low bytes of four words
+    const uint32_t lo = __builtin_amdgcn_perm(c[1], c[0], 0x0C0C0400u), hi = __builtin_amdgcn_perm(c[3], c[2], 0x0C0C0400u);
+    codes[h] = lo | hi << 16;
   }
   return scale;
 }
@@ -189,6 +197,10 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamWArgs a) {
     if (i / ADAMW_BLOCK * ADAMW_BLOCK >= n) break;
     float g[8], m[8], v[8], p[8];
     load8<GF32>(t.grad, i, n, g);
+    if (a.grad_scale) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) g[j] = g[j] * gscale;
+    }
     if constexpr (MASTER) load8<true>(t.master, i, n, p);
     else load8<PF32>(t.param, i, n, p);
     if constexpr (EIGHT) {
@@ -205,19 +217,23 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamWArgs a) {
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      if (a.grad_scale) g[j] = g[j] * gscale;
       m[j] = m[j] * a.b1 + g[j] * a.omb1;
       v[j] = v[j] * a.b2 + g[j] * g[j] * a.omb2;
-      if (EIGHT && i + j >= n) m[j] = v[j] = 0.f;  // past the end: no part of the block's maximum
       const float den = __builtin_amdgcn_sqrtf(v[j] * inv_c2) + a.eps;
-      p[j] = p[j] * decay - rate * (m[j] * __builtin_amdgcn_rcpf(den));
+      p[j] = __builtin_fmaf(m[j] * __builtin_amdgcn_rcpf(den), -rate, p[j] * decay);
+    }
+    if (EIGHT && i + 8 > n) {  // past the end: no part of the block's maximum
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (i + j >= n) m[j] = v[j] = 0.f;
     }
     if constexpr (MASTER) store8<true>(t.master, i, n, p);
     store8<PF32>(t.param, i, n, p);
     if constexpr (EIGHT) {
       uint32_t rnd[4];
+      const uint32_t hash0 = (uint32_t)(i >> 1) * HASH_STEP + key;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) rnd[j] = pair_bits((uint32_t)(i >> 1) + j, key);
+      for (int j = 0; j < 4; ++j) rnd[j] = pair_bits(hash0 + j * HASH_STEP);
       u32x2 mc, vc;
       const float ms = encode8<true>(m, rnd, mc), vs = encode8<false>(v, rnd, vc);
       store_codes((uint8_t*)t.m, i, n, mc);
