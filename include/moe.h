@@ -332,7 +332,9 @@ moe_status_t moe_forward_noalloc(const moe_config_t* cfg, int64_t T, const void*
  *   dx_sorted = moe_grouped_gemm_dgrad(dg, gate, du, up) (fp32); dx = moe_combine(dx_sorted, ones)
  *   d_gate = moe_grouped_gemm_wgrad(dg, x by sorted_token); d_up likewise
  *   moe_adamw_step on the expert weights; moe_update_expert_bias on the selection bias
- * (The shared expert is a call with groups = 1 and offsets = expert_offsets + E.) */
+ * (The shared expert is a call with groups = 1 and offsets = expert_offsets + E.)
+ * Outputs must not overlap inputs or each other (MOE_ERR_INVALID_ARG); matrices of one row stride
+ * may lie side by side in the rows of one buffer. */
 typedef enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_FP32 = 1 } moe_dtype_t;
 
 /* Groups of positions: group g holds positions offsets[g] <= p < offsets[g+1] (the first

@@ -259,7 +259,7 @@ __global__ __launch_bounds__(WR* WC * 64, (WR * WC == 4 && NST * (BR + BC) * KS 
         w.e += n;
         if (n < 64) break;
       }
-      w.e = __builtin_amdgcn_readfirstlane(w.e);
+      w.e = min(__builtin_amdgcn_readfirstlane(w.e), G - 1);
       w.r0 = (w.tile - __builtin_amdgcn_readfirstlane(prefix[w.e])) * BR;
     }
     w.p0 = min(max(offsets[w.e], 0), a.rows);

@@ -51,18 +51,24 @@ constexpr int64_t MAX_ROWS = ((int64_t)1 << 31) - 1;
 constexpr int64_t MAX_LD = (int64_t)1 << 22;  // a tile's rows stay within a 32-bit offset
 constexpr int32_t MAX_FEATURES = 65536, MAX_GROUPS = 1025;
 
-// address range of a row-major matrix
+// a row-major matrix in memory: its address range, the bytes of a row and between rows
 struct Span {
-  uintptr_t lo, hi;
+  uintptr_t lo, hi, row, stride;
   const char* name;
 };
 Span span(const void* p, int64_t rows, int64_t ld, int64_t cols, int64_t size, const char* name) {
   const uintptr_t b = (uintptr_t)p;
-  return {b, rows > 0 ? b + (uintptr_t)(((rows - 1) * ld + cols) * size) : b, name};
+  return {b, rows > 0 ? b + (uintptr_t)(((rows - 1) * ld + cols) * size) : b, (uintptr_t)(cols * size), (uintptr_t)(ld * size), name};
 }
+// Whether an output shares no byte with another matrix.  Side by side in the rows of one buffer (equal
+// strides) is apart.
 moe_status_t apart(const Span& out, const Span& in) {
-  if (out.lo < in.hi && in.lo < out.hi) return fail(MOE_ERR_INVALID_ARG, "%s overlaps %s", out.name, in.name);
-  return MOE_OK;
+  if (out.lo >= in.hi || in.lo >= out.hi) return MOE_OK;
+  if (out.stride == in.stride) {
+    const uintptr_t s = out.stride, d = (out.lo % s + s - in.lo % s) % s;  // out's place in in's rows
+    if (d >= in.row && d + out.row <= s) return MOE_OK;
+  }
+  return fail(MOE_ERR_INVALID_ARG, "%s overlaps %s", out.name, in.name);
 }
 
 moe_status_t check_ld(int64_t ld, int64_t cols, const char* name) {
@@ -261,10 +267,7 @@ moe_status_t moe_swiglu_backward(int64_t n, int64_t mat_rows, int32_t cols, floa
       MOE_TRY(apart(og, i));
       MOE_TRY(apart(ou, i));
     }
-    // side by side in the rows of one buffer is fine
-    const uintptr_t gap = og.lo < ou.lo ? ou.lo - og.lo : og.lo - ou.lo, in_row = gap % (uintptr_t)(ldd * 2);
-    if (og.lo < ou.hi && ou.lo < og.hi && (in_row < (uintptr_t)cols * 2 || in_row > (uintptr_t)(ldd - cols) * 2))
-      return fail(MOE_ERR_INVALID_ARG, "dgate overlaps dup");
+    MOE_TRY(apart(og, ou));
   }
   moe::SwigluArgs a{};
   a.n = n;

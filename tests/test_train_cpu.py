@@ -79,6 +79,8 @@ def wgrad(g=None, dy=None, x=None, dw=at(3), dtype=0, acc=0):
     (lambda: forward(groups(out_features=65536, in_features=32768)), UNSUPPORTED, b"4 GiB"),
     (lambda: forward(x=rows(1, 128, ld=(1 << 22) + 8)), UNSUPPORTED, b"row stride"),
     (lambda: dgrad(dy2=rows(5, 64), w2=at(6), dx=at(6)), INVALID, b"dx overlaps w2"),
+    (lambda: forward(x=rows(1, 128, ld=256), y=at(1) + 240, ldy=256), INVALID, b"y overlaps x"),
+    (lambda: forward(x=rows(1, 128, ld=256), y=at(1) + 400, ldy=256), INVALID, b"y overlaps x"),
     (lambda: wgrad(x=rows(2, 128, rows=50)), INVALID, b"x: 50 rows"),
     (lambda: wgrad(dw=at(2)), INVALID, b"dw overlaps x"),
     (lambda: wgrad(acc=1), UNSUPPORTED, b"accumulation needs fp32"),

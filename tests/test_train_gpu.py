@@ -408,9 +408,11 @@ def test_grouped_operands_past_four_gibibytes():
     x, dy = buf[:, 8:8 + K], buf[:, 1024:1024 + N]
     x.copy_(randn(g, R, K))
     dy.copy_(randn(g, R, N))
+    dy2 = buf[:, 4096:4096 + N]
+    dy2.copy_(randn(g, R, N))
     counts = [500, 0, 350, 250]
     off, o = offsets_of(counts), offsets_of(counts).cpu().numpy()
-    w = randn(g, 4, N, K)
+    w, w2 = randn(g, 4, N, K), randn(g, 4, N, K)
     for mapped in (False, True):
         m = torch.randint(-1, R + 1, (R,), generator=g, dtype=torch.int32).cuda() if mapped else None
         mn = None if m is None else m.cpu().numpy()
@@ -423,6 +425,8 @@ def test_grouped_operands_past_four_gibibytes():
         check(y, *orc.grouped_forward(X, W, o, np.zeros((R, N)), mn), K, False)
         check(dx, *orc.grouped_dgrad(DY, W, o, np.zeros((R, K)), mn), N, False)
         check(dw, *orc.grouped_wgrad(DY, X, o, np.zeros((4, N, K)), mn, mn), 500, False)
+        moe.moe_grouped_gemm_dgrad(dy, w, off, dx, row_map=m, dy2=dy2, w2=w2)
+        check(dx, *orc.grouped_dgrad(DY, W, o, np.zeros((R, K)), mn, f64(dy2), f64(w2)), 2 * N, False)
 
 
 # ---- how the operators are called ----------------------------------------------------------------
@@ -715,3 +719,20 @@ def test_layer_with_shared_expert_matches_moe_forward():
     assert np.linalg.norm(f64(out) - f64(want)) <= 2 * 4 * HALF_BF16 * np.linalg.norm(f64(want))
     moe.moe_update_expert_bias(cfg, counts, torch.zeros(E, device="cuda"), 1e-3)
     torch.cuda.synchronize()
+
+
+def test_operands_and_results_side_by_side():
+    """Input and output columns of one buffer, as a training program packs them."""
+    g = gen(40)
+    counts, N, K, C = [20, 7, 0, 40], 40, 72, 40
+    off, P, o = offsets_of(counts), 67, offsets_of(counts).cpu().numpy()
+    buf, w = randn(g, P, K + N + 3 * C), randn(g, 4, N, K)
+    before = buf.clone()
+    x, y = buf[:, :K], buf[:, K:K + N]
+    moe.moe_grouped_gemm(x, w, off, y)
+    check(y, *orc.grouped_forward(f64(x), f64(w), o, np.zeros((P, N))), K, True)
+    gate, up, h = (buf[:, K + N + i * C:K + N + (i + 1) * C] for i in range(3))
+    moe.moe_swiglu(gate, up, h)
+    assert np.allclose(f64(h), orc.swiglu(f64(gate), f64(up), 0)[3], rtol=2.1 * HALF_BF16 / 2, atol=1e-6)
+    keep = [slice(0, K), slice(K + N, K + N + 2 * C)]
+    assert all(torch.equal(buf[:, k], before[:, k]) for k in keep)
