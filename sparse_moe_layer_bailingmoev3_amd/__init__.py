@@ -583,24 +583,30 @@ class MoEAdamWPlan:
         host = torch.empty(self.struct.image_bytes, dtype=torch.uint8)
         _check(lib.moe_adamw_plan(*args, host.data_ptr(), host.numel()))
         self.image = host.to(device)
+        self.at = self.image.data_ptr()
 
 
 def moe_adamw_step(plan: MoEAdamWPlan, lr, step, betas=(0.9, 0.999), eps=1e-8, seed=0, grad_scale=None, stream=None):
     """One AdamW step over the plan's tensors, in place.  lr and step (1 for the first) are numbers,
     or device tensors (fp32, int64) read when the step runs; grad_scale an fp32 device tensor that
     multiplies every gradient; seed that of the 8-bit states' stochastic rounding."""
-    torch, dev = _torch(), plan.device.index
-    cfg = _AdamWConfig(beta1=betas[0], beta2=betas[1], eps=eps, seed=seed & 0xFFFFFFFF)
-    for name, v, dtype in (("lr", lr, torch.float32), ("step", step, torch.int64), ("grad_scale", grad_scale, torch.float32)):
-        if isinstance(v, torch.Tensor):
-            if v.dtype != dtype or v.numel() != 1 or v.get_device() != dev:
-                _refuse(f"{name} must hold one {dtype} value on {plan.device}")
-            setattr(cfg, name if name == "grad_scale" else name + "_ptr", v.data_ptr())
-        elif name != "grad_scale":
-            setattr(cfg, name, v)
-        elif v is not None:
-            _refuse("grad_scale must be a device tensor")
-    _enqueue(load_library().moe_adamw_step, dev, stream, cfg, plan.struct, plan.image.data_ptr())
+    Tensor, dev = _torch().Tensor, plan.device.index
+    lr_at = step_at = scale_at = None
+    if isinstance(lr, Tensor):
+        lr, lr_at = 0.0, _scalar_at(lr, "lr", _torch().float32, dev)
+    if isinstance(step, Tensor):
+        step, step_at = 0, _scalar_at(step, "step", _torch().int64, dev)
+    if grad_scale is not None:
+        scale_at = _scalar_at(grad_scale, "grad_scale", _torch().float32, dev)
+    _enqueue(load_library().moe_adamw_step, dev, stream,
+             _AdamWConfig(lr, betas[0], betas[1], eps, step, seed & 0xFFFFFFFF, lr_at, step_at, scale_at), plan.struct, plan.at)
+
+
+def _scalar_at(t, name, dtype, dev):
+    """Address of a device tensor that holds one value."""
+    if not isinstance(t, _torch().Tensor) or t.dtype is not dtype or t.numel() != 1 or t.get_device() != dev:
+        _refuse(f"{name} must hold one {dtype} value on cuda:{dev}")
+    return t.data_ptr()
 
 
 def moe_adamw_dequantise(codes, scales, out, signed, stream=None):

@@ -502,7 +502,7 @@ def test_wrong_adamw_image_writes_nothing():
     """The device copy of another plan is recognised by the kernel."""
     mk = lambda n: moe.MoEAdamWPlan(*([torch.ones(n, device="cuda")] for _ in range(4)))  # noqa: E731
     a, b = mk(100), mk(20000)
-    a.image = b.image
+    a.image, a.at = b.image, b.at
     moe.moe_adamw_step(a, lr=1.0, step=1)
     for p in (a, b):
         assert all((t[0] == 1).all() for t in p._keep.values())
