@@ -547,34 +547,32 @@ class MoEAdamWPlan:
         types = {"params": cols["params"][0].dtype, "grads": cols["grads"][0].dtype if cols["grads"] else None,
                  "exp_avg": state, "exp_avg_sq": state, "master": torch.float32, "exp_avg_scale": torch.float32,
                  "exp_avg_sq_scale": torch.float32}
-        device = cols["params"][0].device
+        sizes = [t.numel() for t in cols["params"]]
+        blocks = [-(-k // 128) for k in sizes]
         for name, ts in cols.items():
             if len(ts) != n:
                 _refuse(f"{name} has {len(ts)} tensors, params {n}")
-            for i, t in enumerate(ts):
-                if t.dtype != types[name]:
-                    _refuse(f"{name}[{i}] must be {types[name]}, not {t.dtype}")
+            dtype, wanted = types[name], blocks if name.endswith("scale") else sizes
+            for i, (t, want) in enumerate(zip(ts, wanted)):
+                if t.dtype is not dtype:
+                    _refuse(f"{name}[{i}] must be {dtype}, not {t.dtype}")
                 if not t.is_contiguous():
                     _refuse(f"{name}[{i}] must be contiguous")
-                want = cols["params"][i].numel()
-                want = -(-want // 128) if name.endswith("scale") else want
                 if t.numel() != want:
                     _refuse(f"{name}[{i}] has {t.numel()} values, {want} needed")
-        decay = list(weight_decay) if hasattr(weight_decay, "__len__") else [weight_decay] * n
+        decay = [float(d) for d in weight_decay] if hasattr(weight_decay, "__len__") else [float(weight_decay)] * n
         if len(decay) != n:
             _refuse(f"weight_decay has {len(decay)} entries, params {n}")
+        device, dev = cols["params"][0].device, cols["params"][0].get_device()
         for name, ts in cols.items():
             for i, t in enumerate(ts):
-                if t.device != device or not t.is_cuda:
+                if t.get_device() != dev or dev < 0:
                     _refuse(f"{name}[{i}] lies on {t.device}; one GPU must hold them all")
         self._keep, self.device = cols, device
-        table = (_AdamWTensor * n)()
-        field = {"params": "param", "grads": "grad"}
-        for name, ts in cols.items():
-            for i, t in enumerate(ts):
-                setattr(table[i], field.get(name, name), t.data_ptr() or None)
-        for i, t in enumerate(cols["params"]):
-            table[i].numel, table[i].weight_decay = t.numel(), float(decay[i])
+        none = [None] * n
+        at = {name: [t.data_ptr() or None for t in ts] for name, ts in cols.items()}
+        table = (_AdamWTensor * n)(*zip(at["params"], at.get("master", none), at["grads"], at["exp_avg"], at["exp_avg_sq"],
+                                        at.get("exp_avg_scale", none), at.get("exp_avg_sq_scale", none), sizes, decay))
         self.struct = _AdamWPlan()
         args = (n, ctypes.byref(table), _dtype_code(cols["params"][0], "params"), _dtype_code(cols["grads"][0], "grads"),
                 MOE_STATE_8BIT if eight else MOE_STATE_FP32, ctypes.byref(self.struct))
