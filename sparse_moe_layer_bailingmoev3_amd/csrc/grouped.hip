@@ -678,10 +678,10 @@ hipError_t launch_grouped_rows(const GroupedArgs& a, bool dgrad, hipStream_t s) 
   static const Shape shapes[2][6] = {
       // the reduction along the weights' rows (forward): order of preference where memory bounds all
       {{16, 64, 128, 1, .30f, .48f, 1.f}, {128, 256, 64, 1, .6f, 1.13f, 3.f}, {64, 256, 64, 1, .42f, .86f, 2.5f},
-       {32, 128, 64, 2, .32f, .55f, 1.5f}, {64, 64, 64, 3, .33f, .77f, .7f}, {256, 256, 64, 1, .8f, 1.6f, 4.f}},
+       {32, 128, 64, 2, .32f, .55f, 1.5f}, {64, 64, 64, 3, .33f, .77f, .7f}, {256, 256, 64, 1, .8f, 1.5f, 7.f}},
       // across them (dgrad)
       {{128, 256, 64, 1, .6f, 1.25f, 3.f}, {64, 256, 64, 1, .42f, .82f, 2.5f}, {32, 128, 64, 2, .32f, .67f, 1.5f},
-       {16, 64, 128, 1, .30f, .42f, 1.f}, {64, 64, 64, 3, .33f, 1.1f, .7f}, {256, 256, 64, 1, .8f, 1.75f, 4.f}}};
+       {16, 64, 128, 1, .30f, .42f, 1.f}, {64, 64, 64, 3, .33f, 1.1f, .7f}, {256, 256, 64, 1, .8f, 1.6f, 7.5f}}};
   const double avg = (double)a.rows / a.groups, filled = a.groups * -std::expm1(-avg);
   const double floor = (filled * a.N * (double)a.K * 2 * pair + (double)a.rows * cols * (a.out_f32 ? 4 : 2)) / MEMORY_BYTES_PER_US;
   const Shape* best = nullptr;

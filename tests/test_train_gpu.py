@@ -453,7 +453,7 @@ def test_grouped_most_groups():
 SHAPES = [(1, 70, (768, 136)), (4, 40, (768, 136)), (16, 64, (264, 520)), (40, 24, (520, 264)), (70, 130, (264, 136)),
           (200, 12, (264, 136)), (300, 70, (264, 520)), (900, 2, (264, 136)), (64, 1, (2560, 768)), (3000, 1, (136, 72)),
           (60, 130, (776, 776)), (150, 200, (72, 136)), (40, 60, (136, 776)), (90, 130, (520, 136)), (300, 60, (136, 264)),
-          (20, 300, (520, 520))]
+          (20, 300, (520, 520)), (500, 100, (72, 136))]
 
 
 @pytest.mark.parametrize("rows,G,dims", SHAPES, ids=str)
