@@ -34,10 +34,10 @@
 // What bounds it, on one MI355X (a copy moves 4.9 TB/s here, reads alone 6.3, fills 6.9; the bf16
 // library product reaches 1.23 PFLOP/s), 512 groups of 768 x 2560 weights, 8 a token:
 //   few rows (forward, 64 tokens)          205 us, 6.3 TB/s of weights: the read rate
-//   forward down, 8192 tokens, fp32 out    557 us, 5.0 TB/s: the copy rate
+//   forward down, 8192 tokens, fp32 out    550 us, 5.1 TB/s: the copy rate
 //   dgrad down, 8192 tokens                460 us, 4.7 TB/s (5.3 as fetched: a token's row comes
 //                                          in once for each of its eight positions)
-//   wgrad added to fp32, 8192 tokens       1660 us, 4.9 TB/s: the copy rate
+//   wgrad added to fp32, 8192 tokens       1550-1660 us, 4.9-5.3 TB/s: the copy rate
 // With 1024 rows a group the products bound it: forward 0.95, dgrad 0.72, wgrad 0.81 PFLOP/s; LDS
 // reads and matrix instructions of a step do not overlap fully (one barrier a step).  LDS bank
 // conflicts are zero in every form.  Measured and not kept: steps of 32 values (dgrad +40 %: the
