@@ -736,3 +736,64 @@ def test_operands_and_results_side_by_side():
     assert np.allclose(f64(h), orc.swiglu(f64(gate), f64(up), 0)[3], rtol=2.1 * HALF_BF16 / 2, atol=1e-6)
     keep = [slice(0, K), slice(K + N, K + N + 2 * C)]
     assert all(torch.equal(buf[:, k], before[:, k]) for k in keep)
+
+
+def test_steps_from_two_host_threads():
+    """Two threads, each with a stream and a layer of its own: the results of each alone."""
+    import threading
+    solo = [Step(s, T=200) for s in (41, 42)]
+    for s in solo:
+        s.run()
+    torch.cuda.synchronize()
+    both, failed = [Step(s, T=200) for s in (41, 42)], []
+    torch.cuda.synchronize()
+
+    def work(s):
+        try:
+            st = torch.cuda.Stream()
+            with torch.cuda.stream(st):
+                s.run()
+            st.synchronize()
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(s,)) for s in both]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
+    for s, t in zip(solo, both):
+        for x, y in zip(s.results(), t.results()):
+            assert torch.equal(x, y)
+
+
+@pytest.mark.slow
+@pytest.mark.parametrize("skew", [0.0, 1.2])
+def test_grouped_full_layer_sampled(skew):
+    """512 groups of 768 x 2560 weights, 65,536 positions; sampled rows and whole sampled groups."""
+    E, N, K, P, T = 512, 768, 2560, 65536, 8192
+    gg = torch.Generator(device="cuda")
+    gg.manual_seed(43)
+    rnd = lambda *s: torch.randn(*s, generator=gg, device="cuda", dtype=torch.float32).to(BF)  # noqa: E731
+    share = torch.exp(torch.randn(E, generator=gg, device="cuda") * skew)
+    group = torch.multinomial(share, P, replacement=True, generator=gg).sort().values
+    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    off[1:] = torch.bincount(group, minlength=E).cumsum(0)
+    token = torch.randint(0, T, (P,), generator=gg, device="cuda", dtype=torch.int32)
+    x, dy, w = rnd(T, K), rnd(P, N), rnd(E, N, K)
+    y, dx = torch.empty(P, N, dtype=BF, device="cuda"), torch.empty(P, K, device="cuda")
+    dw = torch.empty(E, N, K, device="cuda")
+    moe.moe_grouped_gemm(x, w, off, y, row_map=token)
+    moe.moe_grouped_gemm_dgrad(dy, w, off, dx)
+    moe.moe_grouped_gemm_wgrad(dy, x, off, dw, x_map=token)
+    for p in [0, 1, P - 1, *torch.randint(0, P, (40,), generator=gg, device="cuda").tolist()]:
+        e = int(group[p])
+        we, xp, dp = f64(w[e]), f64(x[token[p].long()]), f64(dy[p])
+        check(y[p], we @ xp, np.abs(we) @ np.abs(xp), K, True)
+        check(dx[p], dp @ we, np.abs(dp) @ np.abs(we), N, False)
+    o = off.tolist()
+    sizes = np.diff(o)
+    for e in {0, E - 1, int(sizes.argmax()), int(sizes.argmin()), 200}:
+        d, xr = f64(dy[o[e]:o[e + 1]]), f64(x[token[o[e]:o[e + 1]].long()])
+        check(dw[e], d.T @ xr, np.abs(d).T @ np.abs(xr), max(1, int(sizes[e])), False)
