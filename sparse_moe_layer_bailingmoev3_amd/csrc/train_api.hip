@@ -300,7 +300,13 @@ moe_status_t moe_adamw_plan(int64_t n_tensors, const moe_adamw_tensor_t* tensors
   if (state_format != MOE_STATE_FP32 && state_format != MOE_STATE_8BIT)
     return fail(MOE_ERR_INVALID_ARG, "state_format %d is unknown", state_format);
   const bool eight = state_format == MOE_STATE_8BIT;
-  const bool master = n_tensors > 0 && tensors[0].master;
+  // said by the first tensor that holds values (an empty one's arrays may have no address)
+  bool master = false;
+  for (int64_t i = 0; i < n_tensors; ++i)
+    if (tensors[i].numel > 0) {
+      master = tensors[i].master != nullptr;
+      break;
+    }
   if (master && param_dtype == MOE_DTYPE_FP32)
     return fail(MOE_ERR_INVALID_ARG, "master weights belong to bf16 parameters");
   const int64_t psize = dsize(param_dtype), gsize = dsize(grad_dtype), ssize = eight ? 1 : 4;

@@ -318,3 +318,42 @@ def test_grouped_definitions_are_gradients_of_the_forward():
     assert np.allclose(gx, xp.grad.numpy())
     dw, _ = orc.grouped_wgrad(dy.numpy(), x.numpy(), off, np.zeros((3, N, K)), x_map=m)
     assert np.allclose(dw, wp.grad.numpy())
+
+
+# ---- plans with empty tensors --------------------------------------------------------------------
+
+def empty_tensor(i, **kw):
+    """A tensor of no values, whose arrays have no address (an empty torch tensor's is NULL)."""
+    return adamw_tensor(i, n=0, param=None, grad=None, exp_avg=None, exp_avg_sq=None, **kw)
+
+
+@needs_lib
+@pytest.mark.parametrize("empty_at", [(0,), (1,), (2,), (0, 1), (0, 2)], ids=str)
+@pytest.mark.parametrize("master", [False, True])
+def test_adamw_plan_takes_empty_tensors_anywhere(empty_at, master):
+    """Whether the plan has master weights is said by the tensors that hold values."""
+    ts = [empty_tensor(i) if i in empty_at else adamw_tensor(i, master=at(10 * i + 5) if master else None) for i in range(3)]
+    rc, p, image = plan(ts)
+    assert rc == 0, moe.load_library().moe_last_error()
+    assert p.n_chunks == 3 - len(empty_at)
+    flags = np.frombuffer(image, dtype=np.uint64, count=4)[3]
+    assert flags == p.flags and bool(flags & 8) == master
+
+
+@needs_lib
+@pytest.mark.parametrize("tensors,kw,words", [
+    (lambda: [empty_tensor(0, master=at(5)), adamw_tensor(1), adamw_tensor(2, master=at(25))], {}, b"tensor 2: master weights"),
+    (lambda: [empty_tensor(0), adamw_tensor(1, master=at(15)), adamw_tensor(2)], {}, b"tensor 2: master weights"),
+    (lambda: [empty_tensor(0), adamw_tensor(1, master=at(15))], dict(pd=1), b"belong to bf16 parameters"),
+])
+def test_adamw_plan_refuses_some_master_weights_behind_an_empty_tensor(tensors, kw, words):
+    assert plan(tensors(), **kw)[0] == INVALID
+    assert words in moe.load_library().moe_last_error()
+
+
+@needs_lib
+def test_adamw_plan_of_empty_tensors_only():
+    rc, p, _ = plan([empty_tensor(0), empty_tensor(1)])
+    assert rc == 0 and p.n_chunks == 0
+    cfg = moe._AdamWConfig(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, step=1)
+    assert moe.load_library().moe_adamw_step(ctypes.byref(cfg), ctypes.byref(p), None, None) == 0

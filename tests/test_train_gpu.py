@@ -797,3 +797,27 @@ def test_grouped_full_layer_sampled(skew):
     for e in {0, E - 1, int(sizes.argmax()), int(sizes.argmin()), 200}:
         d, xr = f64(dy[o[e]:o[e + 1]]), f64(x[token[o[e]:o[e + 1]].long()])
         check(dw[e], d.T @ xr, np.abs(d).T @ np.abs(xr), max(1, int(sizes[e])), False)
+
+
+# ---- plans with empty tensors --------------------------------------------------------------------
+
+@pytest.mark.parametrize("eight", [False, True], ids=["s32", "s8"])
+def test_adamw_with_an_empty_tensor_first(eight):
+    """Master weights and an empty tensor before the others: the step of the same tensors without
+    it, bit for bit (fp32 states), and every parameter the rounding of its master copy."""
+    sizes = [0, 129, 0, 1000]
+    a = adamw_inputs(13, BF, BF, eight, True, sizes)
+    b = adamw_inputs(13, BF, BF, eight, True, sizes)
+    mk = lambda t, keep: moe.MoEAdamWPlan(  # noqa: E731
+        *([x for x, n in zip(t[i], sizes) if n or keep] for i in (0, 1, 3, 4)), master=[x for x, n in zip(t[2], sizes) if n or keep],
+        **({k: [x for x, n in zip(t[i], sizes) if n or keep] for k, i in (("exp_avg_scale", 5), ("exp_avg_sq_scale", 6))} if eight else {}))
+    pa, pb = mk(a, True), mk(b, False)
+    old = [t.clone() for t in a[2]]
+    for p in (pa, pb):
+        moe.moe_adamw_step(p, lr=1e-2, step=1, seed=4)
+    for i, n in enumerate(sizes):
+        assert torch.equal(a[0][i], a[2][i].to(BF))
+        # the parameters do not depend on the states' rounding after the first step
+        assert torch.equal(a[2][i], b[2][i]) and (n == 0 or not torch.equal(a[2][i], old[i]))
+        if not eight:
+            assert torch.equal(a[3][i], b[3][i]) and torch.equal(a[4][i], b[4][i])
