@@ -613,7 +613,8 @@ __global__ __launch_bounds__(WR* WC * 64, (WR * WC == 4 && NST * (BR + BC) * KS 
     if (live) compute(lds + stage);
     stage = stage == (NST - 1) * ST_BYTES ? 0 : stage + ST_BYTES;
     if (++cs == cw.nsteps) {
-      if (live) epilogue();
+      // (adding, an empty group's gradient stays as it is: not even read)
+      if (live && !(OP == OP_WGRAD && F32 && a.accumulate && cw.cnt == 0)) epilogue();
       clear();
       cs = 0;
       if (!advance(cw)) break;

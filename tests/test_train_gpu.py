@@ -821,3 +821,29 @@ def test_adamw_with_an_empty_tensor_first(eight):
         assert torch.equal(a[2][i], b[2][i]) and (n == 0 or not torch.equal(a[2][i], old[i]))
         if not eight:
             assert torch.equal(a[3][i], b[3][i]) and torch.equal(a[4][i], b[4][i])
+
+
+# ---- gradients of empty groups -------------------------------------------------------------------
+
+@pytest.mark.parametrize("counts", [[0, 3, 0, 0, 70, 0], [0, 0, 0], [0] * 200 + [5] + [0] * 100], ids=["some", "none", "one_of_many"])
+@pytest.mark.parametrize("dims", [(8, 8), (136, 264), (520, 776)], ids=str)
+def test_wgrad_leaves_gradients_of_empty_groups(counts, dims):
+    """Adding, an empty group's gradient keeps its bits: negative zeros, NaN payloads and infinities."""
+    g = gen(50)
+    N, K = dims
+    off, P = offsets_of(counts, 1), 1 + sum(counts) + 2
+    dy, x = randn(g, P, N), randn(g, P, K)
+    bits = torch.randint(-2**31, 2**31 - 1, (len(counts), N, K), generator=g, dtype=torch.int64).to(torch.int32)
+    bits[:, 0] = -2**31                                        # -0.0
+    bits[:, 1] = torch.tensor(0x7F800001, dtype=torch.int32)   # a signalling NaN with a payload
+    full = [e for e, c in enumerate(counts) if c]
+    empty = [e for e, c in enumerate(counts) if not c]
+    dw = bits.cuda().view(F32)
+    dw[full] = randn(g, len(full), N, K, dtype=F32)
+    before = dw.clone()
+    moe.moe_grouped_gemm_wgrad(dy, x, off, dw, accumulate=True)
+    assert torch.equal(dw.view(torch.int32)[empty], before.view(torch.int32)[empty])
+    o = off.cpu().numpy()
+    for e in full:
+        d, r = f64(dy)[o[e]:o[e + 1]], f64(x)[o[e]:o[e + 1]]
+        check(dw[e], d.T @ r + f64(before[e]), np.abs(d).T @ np.abs(r) + np.abs(f64(before[e])), counts[e] + 1, False)
