@@ -333,8 +333,9 @@ moe_status_t moe_forward_noalloc(const moe_config_t* cfg, int64_t T, const void*
  *   d_gate = moe_grouped_gemm_wgrad(dg, x by sorted_token); d_up likewise
  *   moe_adamw_step on the expert weights; moe_update_expert_bias on the selection bias
  * (The shared expert is a call with groups = 1 and offsets = expert_offsets + E.)
- * Outputs must not overlap inputs or each other (MOE_ERR_INVALID_ARG); matrices of one row stride
- * may lie side by side in the rows of one buffer. */
+ * Outputs must not overlap inputs (offsets, maps, positions and weights among them) or each other:
+ * MOE_ERR_INVALID_ARG.  Matrices of one row stride may lie side by side in the rows of one buffer,
+ * and a vector between two rows of a matrix. */
 typedef enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_FP32 = 1 } moe_dtype_t;
 
 /* Groups of positions: group g holds positions offsets[g] <= p < offsets[g+1] (the first
@@ -437,6 +438,7 @@ typedef struct {
   double lr, beta1, beta2, eps;
   int64_t step;            /* 1 for the first step */
   uint32_t seed;           /* of the stochastic rounding */
+  /* device scalars outside the arrays that the step writes (which is not checked) */
   const float* lr_ptr;     /* device; if given, read when the step runs instead of lr */
   const int64_t* step_ptr; /* device; likewise for step (a captured step can then be replayed) */
   const float* grad_scale; /* device; if given, multiplies every gradient */

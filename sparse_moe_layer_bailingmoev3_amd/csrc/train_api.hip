@@ -60,12 +60,14 @@ Span span(const void* p, int64_t rows, int64_t ld, int64_t cols, int64_t size, c
   const uintptr_t b = (uintptr_t)p;
   return {b, rows > 0 ? b + (uintptr_t)(((rows - 1) * ld + cols) * size) : b, (uintptr_t)(cols * size), (uintptr_t)(ld * size), name};
 }
-// Whether an output shares no byte with another matrix.  Side by side in the rows of one buffer (equal
-// strides) is apart.
+Span span(const void* p, int64_t n, int64_t size, const char* name) { return span(p, 1, n, n, size, name); }
+// Whether an output shares no byte with another array.  Side by side in the rows of one buffer (equal
+// strides, or a single row between the rows of the other) is apart.
 moe_status_t apart(const Span& out, const Span& in) {
-  if (out.lo >= in.hi || in.lo >= out.hi) return MOE_OK;
-  if (out.stride == in.stride) {
-    const uintptr_t s = out.stride, d = (out.lo % s + s - in.lo % s) % s;  // out's place in in's rows
+  if (out.lo >= in.hi || in.lo >= out.hi || out.lo == out.hi || in.lo == in.hi) return MOE_OK;
+  const bool out_row = out.hi - out.lo == out.row, in_row = in.hi - in.lo == in.row;
+  if (out.stride == in.stride || out_row || in_row) {
+    const uintptr_t s = out_row ? in.stride : out.stride, d = (out.lo % s + s - in.lo % s) % s;  // out's place in in's rows
     if (d >= in.row && d + out.row <= s) return MOE_OK;
   }
   return fail(MOE_ERR_INVALID_ARG, "%s overlaps %s", out.name, in.name);
@@ -146,6 +148,8 @@ moe_status_t grouped_rows(bool dgrad, const moe_groups_t* g, const moe_rows_t* x
     MOE_TRY(apart(o, span(x2->data, x2->rows, x2->ld, red, 2, "dy2")));
     MOE_TRY(apart(o, span(w2, wrows, g->in_features, g->in_features, 2, "w2")));
   }
+  MOE_TRY(apart(o, span(g->offsets, g->groups + 1, 4, "offsets")));
+  if (x->row_map) MOE_TRY(apart(o, span(x->row_map, g->rows, 4, "row_map")));
   moe::GroupedArgs a{};
   a.offsets = g->offsets;
   a.groups = g->groups;
@@ -208,6 +212,9 @@ moe_status_t moe_grouped_gemm_wgrad(const moe_groups_t* g, const moe_rows_t* dy,
   const Span o = span(dw, (int64_t)g->groups * g->out_features, g->in_features, g->in_features, dsize(dw_dtype), "dw");
   MOE_TRY(apart(o, span(dy->data, dy->rows, dy->ld, g->out_features, 2, "dy")));
   MOE_TRY(apart(o, span(x->data, x->rows, x->ld, g->in_features, 2, "x")));
+  MOE_TRY(apart(o, span(g->offsets, g->groups + 1, 4, "offsets")));
+  if (dy->row_map) MOE_TRY(apart(o, span(dy->row_map, g->rows, 4, "the row map of dy")));
+  if (x->row_map) MOE_TRY(apart(o, span(x->row_map, g->rows, 4, "the row map of x")));
   moe::GroupedArgs a{};
   a.offsets = g->offsets;
   a.groups = g->groups;
@@ -232,6 +239,8 @@ moe_status_t moe_swiglu(int64_t n, int64_t mat_rows, int32_t cols, float limit, 
   const Span o = span(h, mat_rows, ldh, cols, 2, "h");
   MOE_TRY(apart(o, span(gate, mat_rows, ld, cols, 2, "gate")));
   MOE_TRY(apart(o, span(up, mat_rows, ld, cols, 2, "up")));
+  if (row_w) MOE_TRY(apart(o, span(row_w, n, 4, "row_w")));
+  if (pos) MOE_TRY(apart(o, span(pos, n, 4, "pos")));
   moe::SwigluArgs a{};
   a.n = n;
   a.mat_rows = mat_rows;
@@ -256,6 +265,10 @@ moe_status_t moe_swiglu_backward(int64_t n, int64_t mat_rows, int32_t cols, floa
   MOE_TRY(check_ld(ldd, cols, "dgate and dup"));
   MOE_TRY(need_opt(drow_w, "drow_w", 4));
   if (n == 0) return MOE_OK;
+  const Span w = span(row_w, row_w ? n : 0, 4, "row_w"), at = span(pos, pos ? n : 0, 4, "pos");
+  const Span dw = span(drow_w, drow_w ? n : 0, 4, "drow_w");
+  MOE_TRY(apart(dw, w));
+  MOE_TRY(apart(dw, at));
   if (mat_rows > 0) {
     MOE_TRY(need(dh, "dh"));
     MOE_TRY(need(dgate, "dgate"));
@@ -266,8 +279,14 @@ moe_status_t moe_swiglu_backward(int64_t n, int64_t mat_rows, int32_t cols, floa
     for (const Span& i : in) {
       MOE_TRY(apart(og, i));
       MOE_TRY(apart(ou, i));
+      MOE_TRY(apart(dw, i));
     }
     MOE_TRY(apart(og, ou));
+    for (const Span& o : {og, ou}) {
+      MOE_TRY(apart(o, w));
+      MOE_TRY(apart(o, at));
+      MOE_TRY(apart(dw, o));
+    }
   }
   moe::SwigluArgs a{};
   a.n = n;

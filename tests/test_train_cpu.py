@@ -357,3 +357,46 @@ def test_adamw_plan_of_empty_tensors_only():
     assert rc == 0 and p.n_chunks == 0
     cfg = moe._AdamWConfig(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, step=1)
     assert moe.load_library().moe_adamw_step(ctypes.byref(cfg), ctypes.byref(p), None, None) == 0
+
+
+# ---- what an output may not overlap --------------------------------------------------------------
+
+def swiglu_bwd_on(n=10, R=10, C=64, dgate=at(4), dup=at(5), row_w=at(6), pos=at(7), dw=at(8)):
+    return moe.load_library().moe_swiglu_backward(n, R, C, 0.0, at(1), at(2), C, at(3), C, row_w, pos, dgate, dup, C, dw, None)
+
+
+LAST = 10 * 64 * 2 - 4                     # the last four bytes of a [10, 64] bf16 matrix
+
+
+@needs_lib
+@pytest.mark.parametrize("call,words", [
+    # the offsets and row maps of a product
+    (lambda: forward(y=at(0)), b"y overlaps offsets"),
+    (lambda: forward(groups(offsets=at(3) + 99 * 128 + 124)), b"y overlaps offsets"),
+    (lambda: forward(x=rows(1, 128, row_map=at(3) + 16)), b"y overlaps row_map"),
+    (lambda: forward(y=at(4) + 400 - 16, x=rows(1, 128, row_map=at(4))), b"y overlaps row_map"),
+    (lambda: dgrad(dx=at(0) + 16), b"dx overlaps offsets"),
+    (lambda: dgrad(dy=rows(1, 64, row_map=at(3))), b"dx overlaps row_map"),
+    (lambda: wgrad(dw=at(0)), b"dw overlaps offsets"),
+    (lambda: wgrad(dy=rows(1, 64, row_map=at(3) + 4 * 64 * 128 * 2 - 4)), b"dw overlaps the row map of dy"),
+    (lambda: wgrad(x=rows(2, 128, row_map=at(3))), b"dw overlaps the row map of x"),
+    # weights and positions of the activation
+    (lambda: swiglu(w=at(3)), b"h overlaps row_w"),
+    (lambda: swiglu(w=at(3) + LAST), b"h overlaps row_w"),
+    (lambda: swiglu(pos=at(3) + 64), b"h overlaps pos"),
+    (lambda: swiglu_bwd_on(dgate=at(6)), b"dgate overlaps row_w"),
+    (lambda: swiglu_bwd_on(dup=at(6)), b"dup overlaps row_w"),
+    (lambda: swiglu_bwd_on(dgate=at(7)), b"dgate overlaps pos"),
+    (lambda: swiglu_bwd_on(dup=at(7)), b"dup overlaps pos"),
+    (lambda: swiglu_bwd_on(dw=at(1) + LAST), b"drow_w overlaps gate"),
+    (lambda: swiglu_bwd_on(dw=at(2)), b"drow_w overlaps up"),
+    (lambda: swiglu_bwd_on(dw=at(3)), b"drow_w overlaps dh"),
+    (lambda: swiglu_bwd_on(dw=at(4) + LAST), b"drow_w overlaps dgate"),
+    (lambda: swiglu_bwd_on(dw=at(5)), b"drow_w overlaps dup"),
+    (lambda: swiglu_bwd_on(dw=at(6) + 36), b"drow_w overlaps row_w"),
+    (lambda: swiglu_bwd_on(dw=at(7)), b"drow_w overlaps pos"),
+    (lambda: swiglu_bwd_on(R=0, dw=at(7)), b"drow_w overlaps pos"),
+])
+def test_overlap_refusals(call, words):
+    assert call() == INVALID
+    assert words in moe.load_library().moe_last_error()

@@ -847,3 +847,23 @@ def test_wgrad_leaves_gradients_of_empty_groups(counts, dims):
     for e in full:
         d, r = f64(dy)[o[e]:o[e + 1]], f64(x)[o[e]:o[e + 1]]
         check(dw[e], d.T @ r + f64(before[e]), np.abs(d).T @ np.abs(r) + np.abs(f64(before[e])), counts[e] + 1, False)
+
+
+def test_vectors_between_the_rows_of_a_result():
+    """Routing weights, positions and their gradient in the columns that a strided result leaves out."""
+    g = gen(51)
+    R, C, LD = 3, 16, 48
+    buf = torch.zeros(R, LD, dtype=BF, device="cuda")
+    h, dgate, dup = buf[:, :C], torch.zeros(R, LD, dtype=BF, device="cuda"), torch.zeros(R, LD, dtype=BF, device="cuda")
+    w, pos = buf.view(F32)[0, 8:8 + R], buf.view(torch.int32)[1, 8:8 + R]
+    drow = dgate.view(F32)[1, 8:8 + R]
+    w.copy_(torch.rand(R, generator=g) + 0.1)
+    pos.copy_(torch.tensor([2, 0, 1], dtype=torch.int32))
+    gate, up, dh = randn(g, R, C), randn(g, R, C), randn(g, R, C)
+    apart = [torch.empty(R, C, dtype=BF, device="cuda") for _ in range(3)] + [torch.empty(R, device="cuda")]
+    moe.moe_swiglu(gate, up, apart[0], row_w=w.clone(), pos=pos.clone())
+    moe.moe_swiglu_backward(gate, up, dh, apart[1], apart[2], row_w=w.clone(), pos=pos.clone(), drow_w=apart[3])
+    moe.moe_swiglu(gate, up, h, row_w=w, pos=pos)
+    moe.moe_swiglu_backward(gate, up, dh, dgate[:, :C], dup[:, :C], row_w=w, pos=pos, drow_w=drow)
+    for got, want in zip((h, dgate[:, :C], dup[:, :C], drow), apart):
+        assert torch.equal(got, want)
