@@ -377,7 +377,11 @@ def _explain(t, name, dtype, dim, dev):
 
 def _matrix(t, name, dtype, dev):
     """(rows, columns, row stride) of a matrix whose columns lie side by side."""
-    if (dtype is not None and t.dtype is not dtype) or t.dim() != 2 or t.get_device() != dev:
+    try:
+        wrong = dtype is not None and t.dtype is not dtype or t.dim() != 2 or t.get_device() != dev
+    except AttributeError:  # no tensor
+        wrong = True
+    if wrong:
         _explain(t, name, dtype, 2, dev)
     rows, cols = t.shape
     ld, unit = t.stride()
@@ -387,7 +391,11 @@ def _matrix(t, name, dtype, dev):
 
 
 def _vector(t, name, dtype, n, dev):
-    if t.dtype is not dtype or t.dim() != 1 or t.get_device() != dev:
+    try:
+        wrong = t.dtype is not dtype or t.dim() != 1 or t.get_device() != dev
+    except AttributeError:  # no tensor
+        wrong = True
+    if wrong:
         _explain(t, name, dtype, 1, dev)
     size = t.shape[0]
     if n is not None and size != n:
@@ -398,7 +406,11 @@ def _vector(t, name, dtype, n, dev):
 
 
 def _weights3(t, name, dtype, dev):
-    if (dtype is not None and t.dtype is not dtype) or t.dim() != 3 or t.get_device() != dev:
+    try:
+        wrong = dtype is not None and t.dtype is not dtype or t.dim() != 3 or t.get_device() != dev
+    except AttributeError:  # no tensor
+        wrong = True
+    if wrong:
         _explain(t, name, dtype, 3, dev)
     if not t.is_contiguous():
         _refuse(f"{name} must be contiguous")
@@ -424,6 +436,14 @@ def _operand(t, name, cols, row_map, positions, dev):
         _vector(row_map, f"the row map of {name}", torch.int32, positions, dev)
         at = row_map.data_ptr()
     return _Rows(t.data_ptr() if rows else None, rows, ld, at)
+
+
+def _positions(t, row_map, name, dev):
+    """Positions that an operand covers: the entries of its row map, or its rows."""
+    t, name, dim = (t, name, 2) if row_map is None else (row_map, f"the row map of {name}", 1)
+    if not isinstance(t, _torch().Tensor) or t.dim() != dim:
+        _explain(t, name, None, dim, dev)
+    return t.shape[0]
 
 
 def moe_grouped_gemm(x, w, offsets, y, row_map=None, accumulate=False, stream=None):
@@ -466,7 +486,7 @@ def moe_grouped_gemm_wgrad(dy, x, offsets, dw, dy_map=None, x_map=None, accumula
     [.., in], dw bf16 or fp32 [G, out, in] (added to with accumulate, fp32 only)."""
     torch, dev = _torch(), _device_of(dw, "dw")
     G, N, K = _weights3(dw, "dw", None, dev)
-    P, px = (t.shape[0] if m is None else m.shape[0] for t, m in ((dy, dy_map), (x, x_map)))
+    P, px = _positions(dy, dy_map, "dy", dev), _positions(x, x_map, "x", dev)
     if P != px:
         _refuse(f"dy and x cover different numbers of positions: {P} and {px}")
     _vector(offsets, "offsets", torch.int32, G + 1, dev)
@@ -534,15 +554,19 @@ class MoEAdamWPlan:
                  weight_decay=0.0):
         torch = _torch()
         cols = {"params": list(params), "grads": list(grads), "exp_avg": list(exp_avg), "exp_avg_sq": list(exp_avg_sq)}
-        n = len(cols["params"])
-        if n == 0:
-            _refuse("params must not be empty")
-        eight = len(cols["exp_avg"]) > 0 and cols["exp_avg"][0].dtype == torch.uint8
-        if (exp_avg_scale is not None) != eight or (exp_avg_sq_scale is not None) != eight:
-            _refuse("scales belong to uint8 states, and both must be given")
         for name, t in (("master", master), ("exp_avg_scale", exp_avg_scale), ("exp_avg_sq_scale", exp_avg_sq_scale)):
             if t is not None:
                 cols[name] = list(t)
+        n = len(cols["params"])
+        if n == 0:
+            _refuse("params must not be empty")
+        for name, ts in cols.items():
+            for i, t in enumerate(ts):
+                if not isinstance(t, torch.Tensor):
+                    _refuse(f"{name}[{i}] must be a tensor")
+        eight = len(cols["exp_avg"]) > 0 and cols["exp_avg"][0].dtype == torch.uint8
+        if (exp_avg_scale is not None) != eight or (exp_avg_sq_scale is not None) != eight:
+            _refuse("scales belong to uint8 states, and both must be given")
         state = torch.uint8 if eight else torch.float32
         types = {"params": cols["params"][0].dtype, "grads": cols["grads"][0].dtype if cols["grads"] else None,
                  "exp_avg": state, "exp_avg_sq": state, "master": torch.float32, "exp_avg_scale": torch.float32,
@@ -560,7 +584,8 @@ class MoEAdamWPlan:
                     _refuse(f"{name}[{i}] must be contiguous")
                 if t.numel() != want:
                     _refuse(f"{name}[{i}] has {t.numel()} values, {want} needed")
-        decay = [float(d) for d in weight_decay] if hasattr(weight_decay, "__len__") else [float(weight_decay)] * n
+        one = isinstance(weight_decay, torch.Tensor) and weight_decay.dim() == 0 or not hasattr(weight_decay, "__len__")
+        decay = [float(weight_decay)] * n if one else [float(d) for d in weight_decay]
         if len(decay) != n:
             _refuse(f"weight_decay has {len(decay)} entries, params {n}")
         device, dev = cols["params"][0].device, cols["params"][0].get_device()
@@ -588,6 +613,8 @@ def moe_adamw_step(plan: MoEAdamWPlan, lr, step, betas=(0.9, 0.999), eps=1e-8, s
     """One AdamW step over the plan's tensors, in place.  lr and step (1 for the first) are numbers,
     or device tensors (fp32, int64) read when the step runs; grad_scale an fp32 device tensor that
     multiplies every gradient; seed that of the 8-bit states' stochastic rounding."""
+    if not isinstance(plan, MoEAdamWPlan):
+        _refuse("plan must be a MoEAdamWPlan")
     Tensor, dev = _torch().Tensor, plan.device.index
     lr_at = step_at = scale_at = None
     if isinstance(lr, Tensor):

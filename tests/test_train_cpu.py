@@ -400,3 +400,61 @@ LAST = 10 * 64 * 2 - 4                     # the last four bytes of a [10, 64] b
 def test_overlap_refusals(call, words):
     assert call() == INVALID
     assert words in moe.load_library().moe_last_error()
+
+
+# ---- arguments that are no tensors ---------------------------------------------------------------
+
+F8 = torch.zeros(8)
+
+
+@needs_lib
+@pytest.mark.parametrize("wrong", [None, 3, [1.0, 2.0], np.zeros((4, 16), np.float32)], ids=["none", "number", "list", "array"])
+@pytest.mark.parametrize("call,name", [
+    (lambda t: moe.moe_grouped_gemm(t, bf(2, 8, 16), OFF, bf(4, 8)), "x"),
+    (lambda t: moe.moe_grouped_gemm(bf(4, 16), t, OFF, bf(4, 8)), "w"),
+    (lambda t: moe.moe_grouped_gemm(bf(4, 16), bf(2, 8, 16), t, bf(4, 8)), "offsets"),
+    (lambda t: moe.moe_grouped_gemm(bf(4, 16), bf(2, 8, 16), OFF, t), "y"),
+    (lambda t: moe.moe_grouped_gemm_dgrad(t, bf(2, 8, 16), OFF, bf(4, 16)), "dy"),
+    (lambda t: moe.moe_grouped_gemm_dgrad(bf(4, 8), bf(2, 8, 16), OFF, t), "dx"),
+    (lambda t: moe.moe_grouped_gemm_wgrad(t, bf(4, 16), OFF, bf(2, 8, 16)), "dy"),
+    (lambda t: moe.moe_grouped_gemm_wgrad(bf(4, 8), t, OFF, bf(2, 8, 16)), "x"),
+    (lambda t: moe.moe_grouped_gemm_wgrad(t, bf(4, 16), OFF, bf(2, 8, 16), dy_map=i32(0, 1, 2, 3)), "dy"),
+    (lambda t: moe.moe_grouped_gemm_wgrad(bf(4, 8), bf(4, 16), OFF, t), "dw"),
+    (lambda t: moe.moe_swiglu(t, bf(4, 8), bf(4, 8)), "gate"),
+    (lambda t: moe.moe_swiglu(bf(4, 8), t, bf(4, 8)), "up"),
+    (lambda t: moe.moe_swiglu(bf(4, 8), bf(4, 8), t), "h"),
+    (lambda t: moe.moe_swiglu_backward(bf(4, 8), bf(4, 8), t, bf(4, 8), bf(4, 8)), "dh"),
+    (lambda t: moe.moe_swiglu_backward(bf(4, 8), bf(4, 8), bf(4, 8), bf(4, 8), t), "dup"),
+    (lambda t: moe.MoEAdamWPlan([t], [bf(8)], [F8], [F8]), "params[0]"),
+    (lambda t: moe.MoEAdamWPlan([bf(8), bf(8)], [bf(8), t], [F8, F8], [F8, F8]), "grads[1]"),
+    (lambda t: moe.MoEAdamWPlan([bf(8)], [bf(8)], [t], [F8]), "exp_avg[0]"),
+    (lambda t: moe.MoEAdamWPlan([bf(8)], [bf(8)], [F8], [F8], master=[t]), "master[0]"),
+    (lambda t: moe.moe_adamw_dequantise(t, F8, F8, True), "codes"),
+    (lambda t: moe.moe_adamw_dequantise(u8(8), t, F8, True), "scales"),
+    (lambda t: moe.moe_adamw_dequantise(u8(8), torch.zeros(1), t, True), "out"),
+])
+def test_binding_refuses_what_is_no_tensor(call, name, wrong):
+    with pytest.raises(moe.MoEError) as e:
+        call(wrong)
+    assert e.value.status == INVALID and f"{name} must be a tensor" in str(e.value)
+
+
+@needs_lib
+@pytest.mark.parametrize("call,words", [
+    (lambda: moe.moe_grouped_gemm(bf(4, 16), bf(2, 8, 16), OFF, bf(4, 8), row_map=[0, 1, 2, 3]), "the row map of x must be a tensor"),
+    (lambda: moe.moe_grouped_gemm_wgrad(bf(4, 8), bf(4, 16), OFF, bf(2, 8, 16), x_map=[0, 1, 2, 3]), "the row map of x must be a tensor"),
+    (lambda: moe.moe_grouped_gemm_dgrad(bf(4, 8), bf(2, 8, 16), OFF, bf(4, 16), dy2=[0], w2=bf(2, 8, 16)), "dy2 must be a tensor"),
+    (lambda: moe.moe_grouped_gemm_dgrad(bf(4, 8), bf(2, 8, 16), OFF, bf(4, 16), dy2=bf(4, 8), w2=[0]), "w2 must be a tensor"),
+    (lambda: moe.moe_grouped_gemm_wgrad(torch.tensor(1.0), bf(4, 16), OFF, bf(2, 8, 16)), "dy must have 2 dimension"),
+    (lambda: moe.moe_grouped_gemm_wgrad(bf(4, 8), bf(4, 16), OFF, bf(2, 8, 16), x_map=torch.tensor(1)), "the row map of x must have 1 dimension"),
+    (lambda: moe.moe_swiglu(bf(4, 8), bf(4, 8), bf(4, 8), pos=[0, 1]), "pos must be a tensor"),
+    (lambda: moe.moe_swiglu(bf(4, 8), bf(4, 8), bf(4, 8), row_w=[0.5] * 4), "row_w must be a tensor"),
+    (lambda: moe.moe_swiglu_backward(bf(4, 8), bf(4, 8), bf(4, 8), bf(4, 8), bf(4, 8), drow_w=[0.0] * 4), "drow_w must be a tensor"),
+    (lambda: moe.MoEAdamWPlan([bf(8)], [bf(8)], [F8], [F8], weight_decay=[0.1, 0.2]), "weight_decay has 2 entries, params 1"),
+    (lambda: moe.MoEAdamWPlan([bf(8)], [bf(8)], [F8], [F8], weight_decay=torch.tensor(0.1)), "one GPU must hold them all"),
+    (lambda: moe.moe_adamw_step(None, lr=1e-3, step=1), "plan must be a MoEAdamWPlan"),
+])
+def test_binding_refuses_other_wrong_arguments(call, words):
+    with pytest.raises(moe.MoEError) as e:
+        call()
+    assert e.value.status == INVALID and words in str(e.value)
