@@ -162,6 +162,20 @@ __device__ __forceinline__ void store_codes(uint8_t* p, int64_t i, int64_t n, co
   }
 }
 
+// m / (sqrt(v inv_c2) + eps).  The hardware's square root and reciprocal take values below 2^-126 as
+// zero.  With eps of 2^-39 or more that is at most 2^-63 / 2^-39 of the quotient, a rounding; with less
+// (EXACT), v is scaled up under its root and the quotient is divided out.  A branch of the whole launch:
+// the division alone is ten operations a value.
+template <bool EXACT>
+__device__ __forceinline__ float quotient(float m, float v, float inv_c2, float eps) {
+#pragma clang fp contract(off)
+  if constexpr (!EXACT) return m * __builtin_amdgcn_rcpf(__builtin_amdgcn_sqrtf(v * inv_c2) + eps);
+  const bool small = v < 0x1p-96f;
+  const float root = __builtin_amdgcn_sqrtf((small ? v * 0x1p32f : v) * inv_c2);
+  return m / ((small ? root * 0x1p-16f : root) + eps);
+}
+constexpr float EPS_EXACT = 0x1p-39f;
+
 template <bool PF32, bool GF32, bool EIGHT, bool MASTER>
 __global__ __launch_bounds__(256) void adamw_kernel(AdamWArgs a) {
 #pragma clang fp contract(off)
@@ -222,8 +236,13 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamWArgs a) {
     for (int j = 0; j < 8; ++j) {
       m[j] = m[j] * a.b1 + g[j] * a.omb1;
       v[j] = v[j] * a.b2 + g[j] * g[j] * a.omb2;
-      const float den = __builtin_amdgcn_sqrtf(v[j] * inv_c2) + a.eps;
-      p[j] = __builtin_fmaf(m[j] * __builtin_amdgcn_rcpf(den), -rate, p[j] * decay);
+    }
+    if (a.eps >= EPS_EXACT) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) p[j] = __builtin_fmaf(quotient<false>(m[j], v[j], inv_c2, a.eps), -rate, p[j] * decay);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) p[j] = __builtin_fmaf(quotient<true>(m[j], v[j], inv_c2, a.eps), -rate, p[j] * decay);
     }
     if (EIGHT && i + 8 > n) {  // past the end: no part of the block's maximum
 #pragma unroll

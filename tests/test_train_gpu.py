@@ -867,3 +867,41 @@ def test_vectors_between_the_rows_of_a_result():
     moe.moe_swiglu_backward(gate, up, dh, dgate[:, :C], dup[:, :C], row_w=w, pos=pos, drow_w=drow)
     for got, want in zip((h, dgate[:, :C], dup[:, :C], drow), apart):
         assert torch.equal(got, want)
+
+
+# ---- small and zero eps --------------------------------------------------------------------------
+
+@pytest.mark.parametrize("eps", [0.0, 1e-40, 1e-30, 1e-20, 1e-15, 2.0 ** -40, 2.0 ** -39, 1e-8])
+@pytest.mark.parametrize("pdt,master", [(BF, True), (F32, False)], ids=["bf16_master", "fp32"])
+def test_adamw_small_gradients_and_eps(eps, pdt, master):
+    """Gradients down to where the second moment is subnormal: the update still divides by its root.
+    Zero gradients leave the parameters but for the decay, unless eps is zero too (then 0 / 0)."""
+    g = gen(60)
+    n, lr, betas, wd = 4096, 1e-2, (0.9, 0.999), 0.1
+    size = torch.logspace(-20.9, 0, n, dtype=torch.float64).float()
+    grad = (size * torch.sign(torch.randn(n, generator=g))).cuda()
+    grad[::64] = 0.0
+    param = [randn(g, n, dtype=pdt)]
+    ms = [param[0].float()] if master else None
+    m, v = ([torch.zeros(n, device="cuda")] for _ in range(2))
+    plan = moe.MoEAdamWPlan(param, [grad], m, v, master=ms, weight_decay=wd)
+    for step in (1, 2, 40):
+        before = f64((ms or param)[0])
+        wm, wv = orc.adamw_moments(m[0].cpu().numpy(), v[0].cpu().numpy(), grad.cpu().numpy(), betas)
+        moe.moe_adamw_step(plan, lr=lr, step=step, betas=betas, eps=eps)
+        assert np.array_equal(m[0].cpu().numpy(), wm) and np.array_equal(v[0].cpu().numpy(), wv)
+        got = f64((ms or param)[0])
+        with np.errstate(invalid="ignore", divide="ignore"):
+            want = orc.adamw_param(before, wm, wv, lr, step, betas, float(np.float32(eps)), wd)
+        zero = (wm == 0) & (wv == 0)
+        assert zero.any() and (wv[~zero] > 0).all()
+        assert (wv[~zero] < 2.0 ** -126).any()
+        ok = ~zero if eps == 0.0 else np.ones(n, bool)
+        assert np.isfinite(want[ok]).all()
+        # about ten fp32 operations on the update and three on the parameter, as in test_adamw
+        tol = 16 * U32 * (np.abs(want - before) + lr) + 4 * U32 * np.abs(before)
+        assert (np.abs(got - want) <= tol)[ok].all()
+        assert ok.all() or np.isnan(got[~ok]).all()
+        if not ok.all():  # the elements without a gradient go on from where they were
+            for t in (ms or []) + param:
+                t[torch.from_numpy(~ok).cuda()] = 1.0
