@@ -440,7 +440,8 @@ typedef struct {
   uint32_t seed;           /* of the stochastic rounding */
   /* device scalars outside the arrays that the step writes (which is not checked) */
   const float* lr_ptr;     /* device; if given, read when the step runs instead of lr */
-  const int64_t* step_ptr; /* device; likewise for step (a captured step can then be replayed) */
+  const int64_t* step_ptr; /* device; likewise for step (a captured step can then be replayed); below 1
+                              the step writes nothing */
   const float* grad_scale; /* device; if given, multiplies every gradient */
 } moe_adamw_config_t;
 

@@ -611,7 +611,8 @@ class MoEAdamWPlan:
 
 def moe_adamw_step(plan: MoEAdamWPlan, lr, step, betas=(0.9, 0.999), eps=1e-8, seed=0, grad_scale=None, stream=None):
     """One AdamW step over the plan's tensors, in place.  lr and step (1 for the first) are numbers,
-    or device tensors (fp32, int64) read when the step runs; grad_scale an fp32 device tensor that
+    or device tensors (fp32, int64) read when the step runs (which writes nothing if it then finds a
+    step below 1); grad_scale an fp32 device tensor that
     multiplies every gradient; seed that of the 8-bit states' stochastic rounding."""
     if not isinstance(plan, MoEAdamWPlan):
         _refuse("plan must be a MoEAdamWPlan")

@@ -193,6 +193,7 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamWArgs a) {
   if (a.step_ptr) {
     __shared__ float corr[2];
     const int64_t st = *a.step_ptr;
+    if (st < 1) return;  // no step: its bias corrections would make every parameter infinite or NaN
     if (threadIdx.x == 0) {
       corr[0] = (float)(1.0 / (1.0 - pow(a.beta1, (double)st)));
       corr[1] = (float)(1.0 / (1.0 - pow(a.beta2, (double)st)));

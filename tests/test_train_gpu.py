@@ -905,3 +905,21 @@ def test_adamw_small_gradients_and_eps(eps, pdt, master):
         if not ok.all():  # the elements without a gradient go on from where they were
             for t in (ms or []) + param:
                 t[torch.from_numpy(~ok).cuda()] = 1.0
+
+
+@pytest.mark.parametrize("step", [0, -3, -2**40])
+@pytest.mark.parametrize("eight", [False, True], ids=["s32", "s8"])
+def test_adamw_device_step_below_one_writes_nothing(step, eight):
+    """A step count that is read on the device is checked there: before the first step nothing moves."""
+    params, grads, ms, m, v, sc, sv = adamw_inputs(61, BF, BF, eight, True)
+    plan = moe.MoEAdamWPlan(params, grads, m, v, master=ms, exp_avg_scale=sc, exp_avg_sq_scale=sv, weight_decay=0.1)
+    arrays = [t for ts in (params, ms, m, v, sc or [], sv or []) for t in ts]
+    before = [t.clone() for t in arrays]
+    at = torch.tensor([step], device="cuda")
+    moe.moe_adamw_step(plan, lr=1e-2, step=at)
+    for t, b in zip(arrays, before):
+        assert torch.equal(t, b)
+    at.fill_(1)
+    moe.moe_adamw_step(plan, lr=1e-2, step=at)
+    assert all(torch.isfinite(t).all() for t in params + ms)
+    assert all(not torch.equal(t, b) for t, b in zip(params, before) if t.numel() >= 128)
