@@ -606,7 +606,15 @@ class MoEAdamWPlan:
         host = torch.empty(self.struct.image_bytes, dtype=torch.uint8)
         _check(lib.moe_adamw_plan(*args, host.data_ptr(), host.numel()))
         self.image = host.to(device)
-        self.at = self.image.data_ptr()
+        self.at, self.home = self.image.data_ptr(), _raw_stream(dev)
+
+    def _used_on(self, stream):
+        """The table is the plan's own: its memory stays until the work on `stream` (None: the device's
+        current one) is done, also where the plan goes before that."""
+        raw = _raw_stream(self.device.index) if stream is None else _stream(stream)
+        if raw != self.home:
+            cuda = _torch().cuda
+            self.image.record_stream(cuda.ExternalStream(raw, device=self.device) if raw else cuda.default_stream(self.device))
 
 
 def moe_adamw_step(plan: MoEAdamWPlan, lr, step, betas=(0.9, 0.999), eps=1e-8, seed=0, grad_scale=None, stream=None):
@@ -626,6 +634,7 @@ def moe_adamw_step(plan: MoEAdamWPlan, lr, step, betas=(0.9, 0.999), eps=1e-8, s
         scale_at = _scalar_at(grad_scale, "grad_scale", _torch().float32, dev)
     _enqueue(load_library().moe_adamw_step, dev, stream,
              _AdamWConfig(lr, betas[0], betas[1], eps, step, seed & 0xFFFFFFFF, lr_at, step_at, scale_at), plan.struct, plan.at)
+    plan._used_on(stream)
 
 
 def _scalar_at(t, name, dtype, dev):

@@ -923,3 +923,39 @@ def test_adamw_device_step_below_one_writes_nothing(step, eight):
     moe.moe_adamw_step(plan, lr=1e-2, step=at)
     assert all(torch.isfinite(t).all() for t in params + ms)
     assert all(not torch.equal(t, b) for t, b in zip(params, before) if t.numel() >= 128)
+
+
+# ---- a plan dropped while its step is still to run -----------------------------------------------
+
+def two_plans_arrays():
+    return [[torch.ones(20000, device="cuda")] for _ in range(4)]
+
+
+@pytest.mark.parametrize("how", ["given", "current", "handle"])
+def test_plan_table_outlives_a_plan_that_is_dropped(how):
+    """A step on a stream of its own reads the plan's table after the plan is gone: the table's memory
+    is not handed out again before that (addresses are compared, nothing is overwritten)."""
+    arrays, want = two_plans_arrays(), two_plans_arrays()
+    moe.moe_adamw_step(moe.MoEAdamWPlan(*want), lr=1e-2, step=1)
+    st = torch.cuda.Stream()
+    plan = moe.MoEAdamWPlan(*arrays)
+    at, size = plan.image.data_ptr(), plan.image.numel()
+    big = torch.randn(4096, 4096, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(st):
+        for _ in range(20):                # the step waits behind these
+            big = big @ big
+    if how == "current":
+        with torch.cuda.stream(st):
+            moe.moe_adamw_step(plan, lr=1e-2, step=1)
+    else:
+        moe.moe_adamw_step(plan, lr=1e-2, step=1, stream=st if how == "given" else st.cuda_stream)
+    del plan
+    busy = not st.query()
+    taken = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    if busy:
+        assert all(t.data_ptr() != at for t in taken)
+    torch.cuda.synchronize()
+    assert busy, "the products ended before the step was enqueued"
+    for a, b in zip(arrays, want):
+        assert torch.equal(a[0], b[0])
