@@ -411,8 +411,12 @@ moe_status_t moe_swiglu_backward(int64_t n, int64_t mat_rows, int32_t cols, floa
  *   exp_avg     code = sign << 7 | e << 3 | f: (1 + f/8) 2^(e-15) scale, zero for e = f = 0
  *   exp_avg_sq  code = e << 3 | f:             (1 + f/8) 2^(e-31) scale
  * rounded stochastically by a hash of (seed, step, tensor's index in the plan, value's index):
- * the same call gives the same codes.  Both moments start as zero codes with zero scales.  A block
- * with an infinite or NaN value, which has no code, reads back as not finite. */
+ * the same call gives the same codes.  Rounding is unbiased from 1.125 2^-15 (exp_avg) and 2^-31
+ * (exp_avg_sq) of the scale on.  Smaller second moments are raised to 2^-31; first moments up to 2^-15 of
+ * the scale become zero, so an element whose gradients stay below 1.6e-5 of its block's largest is not
+ * moved: tensors that mix such sizes within 128 values keep MOE_STATE_FP32.  Both moments start as
+ * zero codes with zero scales.  A block with an infinite or NaN value, which has no code, reads back
+ * as not finite. */
 typedef enum { MOE_STATE_FP32 = 0, MOE_STATE_8BIT = 1 } moe_state_format_t;
 
 typedef struct {           /* device arrays of one tensor, 16-byte aligned (scales 4-byte) */
@@ -452,8 +456,9 @@ moe_status_t moe_adamw_plan(int64_t n_tensors, const moe_adamw_tensor_t* tensors
                             int32_t grad_dtype, int32_t state_format, moe_adamw_plan_t* plan, void* image,
                             size_t image_bytes);
 
-/* One step.  image: the device copy of the plan's image; an image that is not this plan's is
- * recognised by the kernel, which then writes nothing. */
+/* One step.  image: the device copy of the plan's image.  Memory that does not hold an image, or one
+ * of other numbers of tensors and chunks or other types, is recognised by the kernel, which then
+ * writes nothing (an image of the same numbers and types is taken for this plan's). */
 moe_status_t moe_adamw_step(const moe_adamw_config_t* cfg, const moe_adamw_plan_t* plan, const void* image,
                             void* stream);
 

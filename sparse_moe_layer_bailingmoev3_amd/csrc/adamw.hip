@@ -13,7 +13,13 @@
 //                  the block is, so the quotient m / sqrt(v) cannot run away)
 // A moment moves by 0.1 % a step where its code's step is 6-12 %, so rounding to the nearest
 // would hold it in place; the codes are rounded stochastically instead, by 16 bits of a hash of
-// (seed, step, tensor, element) added below the kept bits: unbiased, and the same on every run.
+// (seed, step, tensor, element) added below the kept bits: the same on every run, and unbiased within
+// the codes' range.  Below it the rounding is not: a first moment of at most 2^-15 of its block's scale
+// (1.6e-5 of the largest magnitude) becomes zero, and between that and the smallest code, 1.125 2^-15,
+// the mean read back rises from zero to the value; a second moment below 2^-31 of its scale is raised
+// to it.  So an element whose gradients stay 60,000 times below its block's largest is not moved.
+// The two moments of an element are rounded by the same bits: each alone is unbiased, their errors are
+// not independent.
 //
 // One workgroup takes a chunk of 8192 values found by one load from the plan; a lane takes 8
 // consecutive values at a time, so 16 lanes (one DPP row) hold a block and its maximum takes four
@@ -42,7 +48,9 @@ __device__ __forceinline__ uint32_t dpp_max16(uint32_t v) {
 }
 
 // 32 random bits of a pair of values: an index hash of multiplications by odd constants and shifts
-// (`x`: pair * HASH_STEP + key, which the pairs of a lane reach by additions)
+// (`x`: pair * HASH_STEP + key, which the pairs of a lane reach by additions).  The three multipliers are
+// those of the grid-cell hash in Ericson, Real-Time Collision Detection (2005), chapter 7; the key's
+// (0x9E3779B9, 0x7F4A7C15) are the halves of 2^64 divided by the golden ratio.
 constexpr uint32_t HASH_STEP = 0x8DA6B343u;
 __device__ __forceinline__ uint32_t pair_bits(uint32_t x) {
   x ^= x >> 15;
@@ -180,7 +188,7 @@ template <bool PF32, bool GF32, bool EIGHT, bool MASTER>
 __global__ __launch_bounds__(256) void adamw_kernel(AdamWArgs a) {
 #pragma clang fp contract(off)
   const AdamWHeader* hd = (const AdamWHeader*)a.image;
-  // an image that is not this plan's is not followed
+  // what is no image, or one of other sizes or types, is not followed
   if (hd->magic != ADAMW_MAGIC || hd->n_tensors != a.n_tensors || hd->n_chunks != a.n_chunks || hd->flags != a.flags)
     return;
   const AdamWTensor* ts = (const AdamWTensor*)(hd + 1);

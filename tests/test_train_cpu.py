@@ -458,3 +458,28 @@ def test_binding_refuses_other_wrong_arguments(call, words):
     with pytest.raises(moe.MoEError) as e:
         call()
     assert e.value.status == INVALID and words in str(e.value)
+
+
+# ---- the range of the 8-bit states ---------------------------------------------------------------
+
+@pytest.mark.parametrize("ratio", [0.25, 0.99, 1.0, 1.03, 1.0625, 1.1, 1.125, 1.3, 2.0, 100.0])
+@pytest.mark.parametrize("signed", [True, False])
+def test_state_rounding_at_the_low_end(ratio, signed):
+    """Read-back means of a value of `ratio` times the format's low end (2^-15 of the scale for the
+    first moment, 2^-31 for the second).  First moment: zero up to 2^-15, rising to the value at
+    1.125 2^-15 (the smallest code), unbiased from there.  Second: raised to 2^-31 below it, unbiased
+    above.  A rounding has two outcomes, at most 1/8 of the lower one or (at the zero code) 1.125 2^-15
+    apart, so N of them have a mean within 5 (apart / 2) / sqrt(N) of its expectation; the 16 random
+    bits move the expectation by at most apart 2^-16, and fp32 rounds the value by 2^-22 of it."""
+    low, N = 2.0 ** (-15 if signed else -31), 127 * 200
+    value = ratio * low
+    x = np.full(128, value, np.float32)
+    x[0] = 1.875                                      # a scale of 1 (but for its rounding)
+    got = np.mean([orc.state_decode(*orc.state_encode(x, signed, 0, s, 1), signed)[1:].astype(np.float64).mean() for s in range(200)])
+    if signed:
+        want = 0.0 if ratio <= 1 else min(9 * (ratio - 1) * low, value) if ratio < 1.125 else value
+        apart = 0.0 if ratio < 1 else 1.125 * low if ratio < 1.125 else value / 8
+    else:
+        want, apart = max(value, low), 0.0 if ratio < 1 else value / 8
+    # (at 2^-15 itself the rounding of the scale decides the side)
+    assert abs(got - want) <= 5 * apart / 2 / N ** 0.5 + apart * 2.0 ** -16 + 9 * 2.0 ** -22 * value

@@ -959,3 +959,59 @@ def test_plan_table_outlives_a_plan_that_is_dropped(how):
     assert busy, "the products ended before the step was enqueued"
     for a, b in zip(arrays, want):
         assert torch.equal(a[0], b[0])
+
+
+# ---- the range of the 8-bit states ---------------------------------------------------------------
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf"), 1e25], ids=str)
+def test_adamw_nonfinite_block_is_not_finite_in_both_moments(bad):
+    """Every value of a block with an infinite or NaN moment reads back as not finite (1e25: only its
+    square is infinite), every value of the blocks beside it as finite, and stays so at the next step."""
+    params, grads, _, m, v, sc, sv = adamw_inputs(12, BF, F32, True, False, [512])
+    grads[0][130] = bad
+    plan = moe.MoEAdamWPlan(params, grads, m, v, exp_avg_scale=sc, exp_avg_sq_scale=sv)
+    for step in (1, 2):
+        moe.moe_adamw_step(plan, lr=1e-3, step=step)
+        for codes, scales, signed in ((m[0], sc[0], True), (v[0], sv[0], False)):
+            out = torch.empty(512, device="cuda")
+            moe.moe_adamw_dequantise(codes, scales, out, signed)
+            hit = torch.isfinite(out[128:256])
+            assert hit.all() if signed and bad == 1e25 else not hit.any()
+            assert torch.isfinite(out[:128]).all() and torch.isfinite(out[256:]).all()
+        grads[0][130] = 0.01
+        fine = torch.cat([params[0][:128], params[0][256:]])
+        assert torch.isfinite(fine).all()
+
+
+@pytest.mark.parametrize("ratio", [0.25, 0.9, 1.03, 1.0625, 1.2, 3.0, 1000.0])
+def test_adamw_state_range(ratio):
+    """What a block keeps of values far below its largest, in one step with beta1 = beta2 = 0 (the
+    moments are g and g^2): a first moment up to 2^-15 of the scale is zero, so its parameter stays
+    where it is, rising to unbiased at 1.125 2^-15; a second moment below 2^-31 is raised to it.  The
+    bound is that of the rounding's mean over N values (two outcomes `apart` from each other)."""
+    blocks, N = 400, 400 * 127
+    low = 2.0 ** -15
+    g = torch.full((blocks, 128), ratio * low, device="cuda")
+    g[:, 0] = 1.875
+    p = [torch.ones(blocks * 128, device="cuda")]
+    m, v = ([torch.zeros(blocks * 128, dtype=torch.uint8, device="cuda")] for _ in range(2))
+    sc, sv = ([torch.zeros(blocks, device="cuda")] for _ in range(2))
+    plan = moe.MoEAdamWPlan(p, [g.view(-1)], m, v, exp_avg_scale=sc, exp_avg_sq_scale=sv)
+    moe.moe_adamw_step(plan, lr=0.0, step=1, betas=(0.0, 0.0), seed=8)
+    out = torch.empty(blocks * 128, device="cuda")
+    moe.moe_adamw_dequantise(m[0], sc[0], out, True)
+    got = out.view(blocks, 128)[:, 1:].double()
+    value = float(g[0, 1])
+    want = 0.0 if ratio <= 1 else 9 * (ratio - 1) * low if ratio < 1.125 else value
+    apart = 0.0 if ratio <= 1 else 1.125 * low if ratio < 1.125 else value / 8
+    assert abs(got.mean().item() - want) <= 5 * apart / 2 / N ** 0.5 + apart * 2.0 ** -16 + 9 * 2.0 ** -22 * value
+    moe.moe_adamw_dequantise(v[0], sv[0], out, False)
+    got, scale = out.view(blocks, 128)[:, 1:].double(), 1.875
+    value = float(g[0, 1]) ** 2
+    want = max(value, scale * 2.0 ** -31)
+    apart = value / 8 if want == value else 0.0
+    assert abs(got.mean().item() - want) <= 5 * apart / 2 / N ** 0.5 + apart * 2.0 ** -16 + 9 * 2.0 ** -22 * want
+    if ratio <= 1:                        # the next step's first moment is all that would move it
+        g[:, 1:] = 0.0
+        moe.moe_adamw_step(plan, lr=1e-2, step=2, betas=(0.5, 0.999), seed=8)
+        assert (p[0].view(blocks, 128)[:, 1:] == 1).all()
