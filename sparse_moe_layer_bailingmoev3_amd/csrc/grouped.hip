@@ -6,10 +6,10 @@
 //
 // for the positions offsets[g] <= p < offsets[g+1] of group g (bf16 operands, fp32 accumulation).
 // One engine: an output tile of BR rows by BC contiguous columns is the sum over reduction steps
-// of 64, each step one X tile (feeding the rows) and one Y tile (feeding the columns) that direct
-// global->LDS loads bring into a ring of NST stages.  The operands differ in which way their
-// reduction index runs in memory:
-//   * along a row (forward's x and W, dgrad's dy): LDS rows of 64 values, 16-byte fragments read
+// of KS values (64; 128 in the 16 x 64 form for few rows), each step one X tile (feeding the rows)
+// and one Y tile (feeding the columns) that direct global->LDS loads bring into a ring of NST
+// stages.  The operands differ in which way their reduction index runs in memory:
+//   * along a row (forward's x and W, dgrad's dy): LDS rows of KS values, 16-byte fragments read
 //     as they lie;
 //   * across rows (dgrad's W, both operands of wgrad): LDS keeps the rows as they come and the
 //     fragments are read through gfx950's transposing LDS load (each 16 lanes turn a 4 x 16 block
@@ -114,9 +114,9 @@ template <int KS>
 __device__ __forceinline__ int swz_k(int row) { return KS == 64 ? (row >> 1) & 7 : row & 15; }
 template <int W>
 __device__ __forceinline__ int swz_tr(int row) {
+  static_assert(W >= 64, "rows of at least 128 bytes");
   if constexpr (W >= 128) return ((row & 3) | ((row >> 1) & 4)) << 1;
-  if constexpr (W == 64) return (((row >> 1) & 1) | ((row >> 2) & 2)) << 1;  // 128-byte rows: bit 0 is the half
-  return (((row >> 3) & 1)) << 1;                                            // 64-byte rows
+  return (((row >> 1) & 1) | ((row >> 2) & 2)) << 1;  // 128-byte rows: bit 0 is the half
 }
 
 // v[j] of lane b of every quad <-> v[b] of lane j
@@ -600,11 +600,9 @@ __global__ __launch_bounds__(WR* WC * 64, (WR * WC == 4 && NST * (BR + BC) * KS 
     } else if constexpr (OP == OP_WGRAD || XN == 1) {
       wait_vmcnt<(D - 1) * (XN + YN)>();
     } else {
-      static_assert(OP == OP_WGRAD || XN == 1 || (D <= 2 && XN <= 4), "counts of one later step");
+      static_assert(D == 1 || (D == 2 && XN == 2), "counts of one later step");
       if (D == 1) wait_vmcnt<0>();
-      else if (n_last >= 4) wait_vmcnt<(XN < 4 ? XN : 4) + YN>();
-      else if (n_last == 3) wait_vmcnt<(XN < 3 ? XN : 3) + YN>();
-      else if (n_last == 2) wait_vmcnt<(XN < 2 ? XN : 2) + YN>();
+      else if (n_last == 2) wait_vmcnt<2 + YN>();
       else wait_vmcnt<1 + YN>();
     }
     lds_barrier();
