@@ -332,7 +332,11 @@ moe_status_t moe_forward_noalloc(const moe_config_t* cfg, int64_t T, const void*
  *   dx_sorted = moe_grouped_gemm_dgrad(dg, gate, du, up) (fp32); dx = moe_combine(dx_sorted, ones)
  *   d_gate = moe_grouped_gemm_wgrad(dg, x by sorted_token); d_up likewise
  *   moe_adamw_step on the expert weights; moe_update_expert_bias on the selection bias
- * (The shared expert is a call with groups = 1 and offsets = expert_offsets + E.)
+ * The shared expert's T rows are one group at position T*K of every buffer, whatever the routing: its
+ * calls take the matrices from that row on, x and dout by token without a map, groups = 1, rows = T
+ * and offsets {0, T}.  (groups = 1 with offsets = expert_offsets + E on the whole buffers computes the
+ * same, but tiles are chosen for groups of rows / groups positions, here all P: 44 us instead of 18
+ * for the gate product of 1024 tokens at 2560 x 768.)
  * Outputs must not overlap inputs (offsets, maps, positions and weights among them) or each other:
  * MOE_ERR_INVALID_ARG.  Matrices of one row stride may lie side by side in the rows of one buffer,
  * and a vector between two rows of a matrix. */
@@ -364,7 +368,8 @@ typedef struct {
  *   x  [.., in_features]; w device bf16 [groups, out_features, in_features]
  *   y  device bf16 or fp32 (y_dtype) [rows, out_features], row stride ldy (multiple of 8).  Rows
  *      of no group are left as they are.  accumulate != 0 adds to y (fp32 only).
- * No workspace; results do not depend on the launch (no atomics).  An infinity or NaN of one row
+ * No workspace; results do not depend on the launch (no atomics).  `rows` and `groups` choose the
+ * tiles, so rows should be about what the groups hold.  An infinity or NaN of one row
  * or group reaches that row's or group's results only. */
 moe_status_t moe_grouped_gemm(const moe_groups_t* groups, const moe_rows_t* x, const void* w, void* y, int64_t ldy,
                               int32_t y_dtype, int32_t accumulate, void* stream);
@@ -385,7 +390,8 @@ moe_status_t moe_grouped_gemm_wgrad(const moe_groups_t* groups, const moe_rows_t
 /* SwiGLU with clamp and routing weight over stored products: for i < n and row r = pos[i] (i
  * with pos NULL),  h[r] = row_w[i] * clamp(silu(gate[r]) * up[r], -limit, limit), rounded once.
  *   gate, up  device bf16 [mat_rows, cols], row stride ld; h likewise with ldh; cols a multiple
- *             of 8, strides multiples of 8
+ *             of 8, strides multiples of 8.  (bf16 only: the products are kept for the backward
+ *             pass, and in fp32 they would double what both directions read and what is kept.)
  *   limit     > 0: clamp; 0, negative or infinite: none
  *   row_w     device fp32 [n] or NULL (1);  pos device int32 [n] or NULL, entries distinct; an
  *             entry outside [0, mat_rows) is skipped (moe_dispatch's -1)

@@ -1015,3 +1015,59 @@ def test_adamw_state_range(ratio):
         g[:, 1:] = 0.0
         moe.moe_adamw_step(plan, lr=1e-2, step=2, betas=(0.5, 0.999), seed=8)
         assert (p[0].view(blocks, 128)[:, 1:] == 1).all()
+
+
+# ---- the shared expert on its own rows -----------------------------------------------------------
+
+@pytest.mark.parametrize("T", [1, 50, 300])
+def test_shared_expert_on_its_own_rows(T):
+    """Forward, gradients and weight gradients of the shared expert from row T*K of the dispatch's
+    buffers on, some slots routed nowhere: the float64 definitions, and the same as the calls on the
+    whole buffers with the dispatch's own offsets and map; the routed experts' rows are left alone."""
+    from moe_case import cfg_for
+    from synthetic import CONFIGS
+    sc = CONFIGS["tiny"]
+    cfg, H, I, E, K = cfg_for(sc), sc.H, sc.I, sc.E, sc.K
+    g = gen(70)
+    P, s = T * K + T, T * K
+    idx = torch.stack([torch.randperm(E, generator=g)[:K] for _ in range(T)]).to(torch.int32)
+    idx[::5, 0] = -1                       # pairs that the dispatch ignores
+    i32 = dict(dtype=torch.int32, device="cuda")
+    counts, off = torch.empty(E + 1, **i32), torch.empty(E + 2, **i32)
+    token, inv = torch.empty(P, **i32), torch.empty(T, K, **i32)
+    ws = torch.empty(moe.moe_workspace_size(cfg, T), dtype=torch.uint8, device="cuda")
+    moe.moe_dispatch(cfg, T, idx.cuda(), counts, off, token, inv, ws)
+    assert off[E:].tolist() == [s, P] and token[s:].tolist() == list(range(T))
+    x, dout = randn(g, T, H), randn(g, T, H)
+    wg, wu, wd = randn(g, 1, I, H, scale=H ** -0.5), randn(g, 1, I, H, scale=H ** -0.5), randn(g, 1, H, I, scale=I ** -0.5)
+    own, one = offsets_of([T]), np.array([0, T])
+
+    def buffers():
+        bf = [torch.full((P, I), 3.0, dtype=BF, device="cuda") for _ in range(6)]
+        return bf + [torch.full((P, H), 3.0, device="cuda") for _ in range(2)] + [torch.ones_like(t, dtype=F32) for t in (wg, wu, wd)]
+
+    a, b = buffers(), buffers()
+    for whole, (gb, ub, hb, dhb, dgb, dub, y, dx, d_gate, d_up, d_down) in ((False, a), (True, b)):
+        v, o, m = (lambda t: t, off[E:], token) if whole else (lambda t: t[s:], own, None)
+        moe.moe_grouped_gemm(x, wg, o, v(gb), row_map=m)
+        moe.moe_grouped_gemm(x, wu, o, v(ub), row_map=m)
+        moe.moe_swiglu(gb[s:], ub[s:], hb[s:], limit=2.0)
+        moe.moe_grouped_gemm(v(hb), wd, o, v(y))
+        moe.moe_grouped_gemm_dgrad(dout, wd, o, v(dhb), row_map=m)
+        moe.moe_grouped_gemm_wgrad(dout, v(hb), o, d_down, dy_map=m, accumulate=True)
+        moe.moe_swiglu_backward(gb[s:], ub[s:], dhb[s:], dgb[s:], dub[s:], limit=2.0)
+        moe.moe_grouped_gemm_dgrad(v(dgb), wg, o, v(dx), dy2=v(dub), w2=wu)
+        moe.moe_grouped_gemm_wgrad(v(dgb), x, o, d_gate, x_map=m, accumulate=True)
+        moe.moe_grouped_gemm_wgrad(v(dub), x, o, d_up, x_map=m, accumulate=True)
+    for t in a[:8]:
+        assert (t[:s] == 3.0).all()
+    X, DO, WG, WU, WD = (f64(t) for t in (x, dout, wg, wu, wd))
+    for gb, ub, hb, dhb, dgb, dub, y, dx, d_gate, d_up, d_down in (a, b):
+        z = np.zeros
+        check(gb[s:], *orc.grouped_forward(X, WG, one, z((T, I))), H, True)
+        check(ub[s:], *orc.grouped_forward(X, WU, one, z((T, I))), H, True)
+        check(y[s:], *orc.grouped_forward(f64(hb)[s:], WD, one, z((T, H))), I, False)
+        check(dhb[s:], *orc.grouped_dgrad(DO, WD, one, z((T, I))), H, True)
+        check(dx[s:], *orc.grouped_dgrad(f64(dgb)[s:], WG, one, z((T, H)), None, f64(dub)[s:], WU), 2 * I, False)
+        for dw, d, r in ((d_gate, f64(dgb)[s:], X), (d_up, f64(dub)[s:], X), (d_down, DO, f64(hb)[s:])):
+            check(dw, *orc.grouped_wgrad(d, r, one, np.ones(dw.shape), None, None, True), T + 1, False)
