@@ -1071,3 +1071,27 @@ def test_shared_expert_on_its_own_rows(T):
         check(dx[s:], *orc.grouped_dgrad(f64(dgb)[s:], WG, one, z((T, H)), None, f64(dub)[s:], WU), 2 * I, False)
         for dw, d, r in ((d_gate, f64(dgb)[s:], X), (d_up, f64(dub)[s:], X), (d_down, DO, f64(hb)[s:])):
             check(dw, *orc.grouped_wgrad(d, r, one, np.ones(dw.shape), None, None, True), T + 1, False)
+
+
+# ---- offsets outside the positions ---------------------------------------------------------------
+
+@pytest.mark.parametrize("raw", [[-5, 3, 20, 20, 400], [0, 0, 60, 2**31 - 1, 2**31 - 1], [-2**31, -1, 0, 61, 62], [70, 80, 90, 100, 110]], ids=str)
+@pytest.mark.parametrize("mapped", [False, True])
+def test_grouped_offsets_are_clamped(raw, mapped):
+    """Offsets are taken as clamped to [0, rows]: groups end with the positions, rows of no group stay."""
+    g = gen(80)
+    P, N, K, G = 61, 40, 72, 4
+    off = torch.tensor(raw, dtype=torch.int32).cuda()
+    o = np.clip(np.array(raw, dtype=np.int64), 0, P)
+    T = 9 if mapped else P
+    m = torch.randint(-1, T + 1, (P,), generator=g, dtype=torch.int32).cuda() if mapped else None
+    mn = None if m is None else m.cpu().numpy()
+    x, dy, w = randn(g, T, K), randn(g, T, N), randn(g, G, N, K)
+    y, dx, dw = randn(g, P, N, dtype=F32), randn(g, P, K, dtype=F32), randn(g, G, N, K, dtype=F32)
+    by, bx, bw = f64(y), f64(dx), f64(dw)
+    moe.moe_grouped_gemm(x, w, off, y, row_map=m)
+    moe.moe_grouped_gemm_dgrad(dy, w, off, dx, row_map=m)
+    moe.moe_grouped_gemm_wgrad(dy, x, off, dw, dy_map=m, x_map=m, accumulate=True)
+    check(y, *orc.grouped_forward(f64(x), f64(w), o, by, mn), K, False)
+    check(dx, *orc.grouped_dgrad(f64(dy), f64(w), o, bx, mn), N, False)
+    check(dw, *orc.grouped_wgrad(f64(dy), f64(x), o, bw, mn, mn, True), P + 1, False)
