@@ -25,9 +25,9 @@
 // consecutive values at a time, so 16 lanes (one DPP row) hold a block and its maximum takes four
 // lane permutations, no LDS.  Streaming: 10 + 16/128 bytes per value with bf16 parameters and
 // 8-bit states, 22 with 32-bit states, 28 with master weights besides.  755 M values of 384 tensors
-// in 8 bits on one MI355X: 1.43 ms, 5.3 TB/s; both moments read out as fp32: 1.26 ms, 6.0 TB/s
-// (a copy moves 4.9, a fill 6.9).  The vector units are near their limit there (about 60
-// operations a value), which is why the codes are packed by byte permutes.
+// in 8 bits on one MI355X: 1.42-1.48 ms, 5.2-5.4 TB/s (eps 1e-15: 1.55 ms); both moments read out as
+// fp32: 1.27 ms, 6.0 TB/s (a copy moves 4.9, a fill 6.9).  The vector units are near their limit there
+// (about 60 operations a value), which is why the codes are packed by byte permutes.
 #include "moe_common.h"
 #include "moe_internal.h"
 

@@ -33,17 +33,22 @@
 //
 // What bounds it, on one MI355X (a copy moves 4.9 TB/s here, reads alone 6.3, fills 6.9; the bf16
 // library product reaches 1.23 PFLOP/s), 512 groups of 768 x 2560 weights, 8 a token:
-//   few rows (forward, 64 tokens)          205 us, 6.3 TB/s of weights: the read rate
-//   forward down, 8192 tokens, fp32 out    550 us, 5.1 TB/s: the copy rate
-//   dgrad down, 8192 tokens                460 us, 4.7 TB/s (5.3 as fetched: a token's row comes
+//   few rows (forward, 64 tokens)          204-212 us, 6.0-6.3 TB/s of weights: the read rate
+//   forward down, 8192 tokens, fp32 out    554 us, 5.0 TB/s: the copy rate
+//   dgrad down, 8192 tokens                463-470 us, 4.6 TB/s (5.2 as fetched: a token's row comes
 //                                          in once for each of its eight positions)
-//   wgrad added to fp32, 8192 tokens       1550-1660 us, 4.9-5.3 TB/s: the copy rate
-// With 1024 rows a group the products bound it: forward 0.95, dgrad 0.72, wgrad 0.81 PFLOP/s; LDS
-// reads and matrix instructions of a step do not overlap fully (one barrier a step).  LDS bank
-// conflicts are zero in every form.  Measured and not kept: steps of 32 values (dgrad +40 %: the
-// barriers), nontemporal results (wgrad +22 %), fragments read a sub-step ahead (no change, or
-// slower by the registers they hold), 128 x 128 tiles per wave (spills), a group's row tiles before
-// its column tiles (skewed dgrad +6 %), raised wave priority around the products (no change).
+//   wgrad added to fp32, 8192 tokens       1660 us, 4.9 TB/s: the copy rate
+//   the same, 64 tokens (324 groups)       1060 us, 4.9 TB/s; 1 token (8 groups): 162 us, in which
+//                                          every workgroup steps through 60 tiles, most of them of
+//                                          empty groups (read and written: nothing)
+// With 1024 rows a group (64 groups) the products bound it: forward 1.02, dgrad 0.87 (0.73 with fp32
+// results), wgrad 0.80 PFLOP/s; LDS reads and matrix instructions of a step do not overlap fully (one
+// barrier a step), and the 256 x 256 dgrad form with fp32 results spills 6 vector registers (28 bytes
+// a lane; it and wgrad's also keep 60-75 scalar values in lanes).  LDS bank conflicts are zero in every
+// form.  Measured and not kept: steps of 32 values (dgrad +40 %: the barriers), nontemporal results
+// (wgrad +22 %), fragments read a sub-step ahead (no change, or slower by the registers they hold),
+// 128 x 128 tiles per wave (78-540 vector registers spilled), a group's row tiles before its column
+// tiles (skewed dgrad +6 %), raised wave priority around the products (no change).
 #include <atomic>
 #include <cmath>
 #include <utility>

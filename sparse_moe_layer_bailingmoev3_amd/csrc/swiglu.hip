@@ -12,7 +12,7 @@
 // Pure streaming: 6 (forward) or 10 (backward) bytes per value.  LPR lanes share a row, each
 // taking 8 consecutive values (16 bytes) at a time, so a row's reads are contiguous.  65,536 rows
 // of 768 on one MI355X: 63 us forward, 105 us backward, both 4.8 TB/s, the rate of a copy; 776
-// rows of 136: 8.5 us a call, the host's cost of a call (the kernel takes 3.6).
+// rows of 136: 7.8-8.5 us a call, the host's cost of a call (the kernel takes 3.6).
 #include "moe_common.h"
 #include "moe_internal.h"
 
