@@ -553,10 +553,15 @@ class MoEAdamWPlan:
     def __init__(self, params, grads, exp_avg, exp_avg_sq, master=None, exp_avg_scale=None, exp_avg_sq_scale=None,
                  weight_decay=0.0):
         torch = _torch()
-        cols = {"params": list(params), "grads": list(grads), "exp_avg": list(exp_avg), "exp_avg_sq": list(exp_avg_sq)}
-        for name, t in (("master", master), ("exp_avg_scale", exp_avg_scale), ("exp_avg_sq_scale", exp_avg_sq_scale)):
-            if t is not None:
-                cols[name] = list(t)
+        cols = {}
+        for name, ts, must in (("params", params, True), ("grads", grads, True), ("exp_avg", exp_avg, True),
+                               ("exp_avg_sq", exp_avg_sq, True), ("master", master, False),
+                               ("exp_avg_scale", exp_avg_scale, False), ("exp_avg_sq_scale", exp_avg_sq_scale, False)):
+            if must or ts is not None:
+                try:
+                    cols[name] = list(ts)
+                except TypeError:
+                    _refuse(f"{name} must be a list of tensors")
         n = len(cols["params"])
         if n == 0:
             _refuse("params must not be empty")
@@ -585,7 +590,10 @@ class MoEAdamWPlan:
                 if t.numel() != want:
                     _refuse(f"{name}[{i}] has {t.numel()} values, {want} needed")
         one = isinstance(weight_decay, torch.Tensor) and weight_decay.dim() == 0 or not hasattr(weight_decay, "__len__")
-        decay = [float(weight_decay)] * n if one else [float(d) for d in weight_decay]
+        try:
+            decay = [float(weight_decay)] * n if one else [float(d) for d in weight_decay]
+        except (TypeError, ValueError):
+            _refuse("weight_decay must be a number or one for each tensor")
         if len(decay) != n:
             _refuse(f"weight_decay has {len(decay)} entries, params {n}")
         device, dev = cols["params"][0].device, cols["params"][0].get_device()

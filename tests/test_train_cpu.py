@@ -483,3 +483,19 @@ def test_state_rounding_at_the_low_end(ratio, signed):
         want, apart = max(value, low), 0.0 if ratio < 1 else value / 8
     # (at 2^-15 itself the rounding of the scale decides the side)
     assert abs(got - want) <= 5 * apart / 2 / N ** 0.5 + apart * 2.0 ** -16 + 9 * 2.0 ** -22 * value
+
+
+@needs_lib
+@pytest.mark.parametrize("call,words", [
+    (lambda: moe.MoEAdamWPlan(None, [bf(8)], [F8], [F8]), "params must be a list of tensors"),
+    (lambda: moe.MoEAdamWPlan([bf(8)], 7, [F8], [F8]), "grads must be a list of tensors"),
+    (lambda: moe.MoEAdamWPlan([bf(8)], [bf(8)], torch.tensor(1.0), [F8]), "exp_avg must be a list of tensors"),
+    (lambda: moe.MoEAdamWPlan([bf(8)], [bf(8)], [F8], [F8], master=1.5), "master must be a list of tensors"),
+    (lambda: moe.MoEAdamWPlan([bf(8)], [bf(8)], [F8], [F8], weight_decay=None), "weight_decay must be a number"),
+    (lambda: moe.MoEAdamWPlan([bf(8)], [bf(8)], [F8], [F8], weight_decay=[None]), "weight_decay must be a number"),
+    (lambda: moe.MoEAdamWPlan([bf(8)], [bf(8)], [F8], [F8], weight_decay="fast"), "weight_decay must be a number"),
+])
+def test_adamw_plan_refuses_what_is_no_list(call, words):
+    with pytest.raises(moe.MoEError) as e:
+        call()
+    assert e.value.status == INVALID and words in str(e.value)
