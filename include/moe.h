@@ -410,6 +410,7 @@ moe_status_t moe_swiglu_backward(int64_t n, int64_t mat_rows, int32_t cols, floa
  *   m' = beta1 m + (1 - beta1) g;  v' = beta2 v + (1 - beta2) g^2      (each operation rounded
  *        to fp32; g = grad, times *grad_scale if that is given)
  *   p' = p (1 - lr weight_decay) - lr m' / (1 - beta1^step) / (sqrt(v' / (1 - beta2^step)) + eps)
+ * (with eps 0, a value that never had a gradient becomes NaN: 0 / 0).
  * Parameters and gradients are bf16 or fp32; with bf16 parameters an fp32 master copy may hold
  * the exact values (then the parameters are its rounding).  States are fp32, or 8 bits:
  * MOE_STATE_8BIT keeps blocks of 128 consecutive values of a tensor as one code byte each and an

@@ -1095,3 +1095,61 @@ def test_grouped_offsets_are_clamped(raw, mapped):
     check(y, *orc.grouped_forward(f64(x), f64(w), o, by, mn), K, False)
     check(dx, *orc.grouped_dgrad(f64(dy), f64(w), o, bx, mn), N, False)
     check(dw, *orc.grouped_wgrad(f64(dy), f64(x), o, bw, mn, mn, True), P + 1, False)
+
+
+# ---- elements past 32 bits -----------------------------------------------------------------------
+
+def test_swiglu_rows_past_four_gibibytes():
+    """Rows far apart in buffers of more than 4 GiB, forward and backward."""
+    g = gen(90)
+    R, LD, C = 700, 1 << 22, 40
+    buf, out = (torch.empty(R, LD, dtype=BF, device="cuda") for _ in range(2))     # 5.9 GB each
+    gate, up, dh = buf[:, 8:8 + C], buf[:, 128:128 + C], buf[:, 1 << 20:(1 << 20) + C]
+    for t in (gate, up, dh):
+        t.copy_(randn(g, R, C))
+    pos, w = torch.randperm(R, generator=g).to(torch.int32).cuda(), (torch.rand(R, generator=g) + 0.1).cuda()
+    h, dgate, dup = out[:, :C], out[:, 64:64 + C], out[:, 128:128 + C]
+    drow, drow2 = torch.empty(R, device="cuda"), torch.empty(R, device="cuda")
+    moe.moe_swiglu(gate, up, h, limit=2.0, row_w=w, pos=pos)
+    moe.moe_swiglu_backward(gate, up, dh, dgate, dup, limit=2.0, row_w=w, pos=pos, drow_w=drow)
+    near = [t.contiguous() for t in (gate, up, dh)] + [torch.empty(R, C, dtype=BF, device="cuda") for _ in range(3)]
+    moe.moe_swiglu(near[0], near[1], near[3], limit=2.0, row_w=w, pos=pos)
+    moe.moe_swiglu_backward(near[0], near[1], near[2], near[4], near[5], limit=2.0, row_w=w, pos=pos, drow_w=drow2)
+    for a, b in ((h, near[3]), (dgate, near[4]), (dup, near[5]), (drow, drow2)):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("eight", [False, True], ids=["s32", "s8"])
+def test_adamw_tensor_past_two_to_the_32_values(eight):
+    """One tensor of more than 2^32 values: its first and last values take the step of a small tensor
+    (8 bits: one that holds the same blocks; read-outs within a code, at most 1/8, of the moments)."""
+    n, tail, lr = (1 << 32) + 8192 + 77, 8192 + 77, 1e-2
+    g = gen(91)
+    small = randn(g, 2 * 8192 + 77, dtype=BF, scale=0.05), randn(g, 2 * 8192 + 77, dtype=BF, scale=1e-2)
+    p, gr = (torch.zeros(n, dtype=BF, device="cuda") for _ in range(2))                # 8.6 GB each
+    for big, s in zip((p, gr), small):
+        big[:8192], big[-tail:] = s[:8192], s[8192:]
+    z = lambda k: torch.zeros(k, dtype=torch.uint8 if eight else F32, device="cuda")  # noqa: E731
+    m, v, ms, vs = z(n), z(n), z(len(small[0])), z(len(small[0]))
+    sc = lambda k: [torch.zeros(-(-k // 128), device="cuda") for _ in range(2)] if eight else [None, None]  # noqa: E731
+    big_sc, small_sc = sc(n), sc(len(small[0]))
+    kw = lambda s: dict(exp_avg_scale=[s[0]], exp_avg_sq_scale=[s[1]]) if eight else {}  # noqa: E731
+    moe.moe_adamw_step(moe.MoEAdamWPlan([p], [gr], [m], [v], **kw(big_sc)), lr=lr, step=1, seed=3)
+    want = small[0].clone()
+    moe.moe_adamw_step(moe.MoEAdamWPlan([want], [small[1]], [ms], [vs], **kw(small_sc)), lr=lr, step=1, seed=3)
+    assert torch.equal(p[:8192], want[:8192]) and torch.equal(p[-tail:], want[8192:])
+    assert not p[8192:16384].any() and not p[-tail - 8192:-tail].any()
+    if not eight:
+        for a, b in ((m, ms), (v, vs)):
+            assert torch.equal(a[:8192], b[:8192]) and torch.equal(a[-tail:], b[8192:])
+        return
+    assert torch.equal(m[:8192], ms[:8192]) and torch.equal(v[:8192], vs[:8192])
+    wm, wv = orc.adamw_moments(np.zeros(tail), np.zeros(tail), small[1][8192:].float().cpu().numpy(), (0.9, 0.999))
+    for codes, scales, signed, x in ((m, big_sc[0], True, wm), (v, big_sc[1], False, wv)):
+        assert torch.equal(scales[-65:], (small_sc[0] if signed else small_sc[1])[-65:])
+        out = torch.empty(n, device="cuda")                                            # 17 GB
+        moe.moe_adamw_dequantise(codes, scales, out, signed)
+        got, floor = f64(out[-tail:]), np.repeat(scales[-65:].cpu().numpy(), 128)[:tail] * 1.125 * 2.0 ** -15
+        assert (np.abs(got - x) <= np.abs(x) / 8 * (1 + 2.0 ** -20) + floor).all()
+        assert not out[8192:16384].any()
+        del out
