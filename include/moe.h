@@ -474,6 +474,116 @@ moe_status_t moe_adamw_step(const moe_adamw_config_t* cfg, const moe_adamw_plan_
 moe_status_t moe_adamw_dequantise(const uint8_t* codes, const float* scales, int64_t numel, int32_t is_signed,
                                   float* out, void* stream);
 
+/* ---- Training the router ------------------------------------------------------------------
+ * moe_swiglu_backward ends at the gradient of the mixing weights.  The rest of a step:
+ *   topk_idx, topk_w, logits = moe_route_logits(x, router_w)      in place of moe_route
+ *   counts, loss = moe_balance_loss(logits, topk_idx)             added to the model's loss
+ *   d_router_w, dx = moe_router_backward(d_topk_w and counts)     dx added to the layer's input gradient:
+ *     in fp32 to the rows T*K .. of moe_grouped_gemm_dgrad's result, where the shared expert's rows
+ *     lie, so that moe_combine rounds the sum once
+ *   norm, coef = moe_grad_norm(all gradients)
+ *   moe_adamw_step(grad_scale = coef), or moe_grad_clip and any other step
+ * Outputs and the workspace must not overlap inputs or each other: MOE_ERR_INVALID_ARG. */
+
+/* moe_route that keeps the logits for the backward pass: the same arguments and results (bit for bit),
+ * and
+ *   logits  device fp32 [T,E]   the raw scores before the sigmoid */
+moe_status_t moe_route_logits(const moe_config_t* cfg, int64_t T, const void* x, const float* router_w,
+                              const float* expert_bias, int32_t* topk_idx, float* topk_w, float* logits, void* ws,
+                              size_t ws_bytes, void* stream);
+
+/* The sequences of a batch of T tokens: sequence b is the run of tokens offsets[b] <= t < offsets[b+1],
+ * of which the first lens[b] belong to it; the others of the run, and tokens of no run, are padding.
+ * The arrays are read on the device, offsets taken as clamped to [0, T], lens to the run. */
+typedef struct {
+  int32_t n_seq;          /* 1..65536 */
+  const int32_t* offsets; /* device [n_seq + 1], not decreasing; NULL with n_seq 1: one run of all T tokens */
+  const int32_t* lens;    /* device [n_seq], or NULL: whole runs */
+} moe_sequences_t;
+
+/* Bytes of device workspace (256-byte aligned) that moe_balance_loss and moe_router_backward need for T
+ * tokens in n_seq sequences (host call).  It holds nothing between calls. */
+moe_status_t moe_router_workspace_size(const moe_config_t* cfg, int64_t T, int32_t n_seq, size_t* bytes);
+
+/* Balance loss: how evenly each sequence loads the experts.  With s = sigmoid(logits), sequence b of
+ * n_b tokens and N = sum of n_b:
+ *   counts[b,e] = (token, slot) pairs of b's tokens with topk_idx == e  (ids outside [0, E): ignored)
+ *   probs[b,e]  = mean over b's tokens of s_te / sum_j s_tj
+ *   loss        = coef sum_b (n_b / N) sum_e f_be probs[b,e],   f_be = E counts[b,e] / (K n_b)
+ * (coef for a perfectly even load).  An empty sequence has zeros and no part in the loss; without any
+ * token the loss is 0.  A token whose scores are all zero counts as zeros.
+ *   sequences  host pointer, or NULL: one sequence of all tokens
+ *   counts     device int32 [n_seq,E]; with one sequence the first E entries of moe_dispatch's
+ *   probs      device fp32 [n_seq,E]      loss device fp32 [1]
+ * T = 0 writes zeros.  Sums have a fixed order. */
+moe_status_t moe_balance_loss(const moe_config_t* cfg, int64_t T, const moe_sequences_t* sequences, const float* logits,
+                              const int32_t* topk_idx, float coef, int32_t* counts, float* probs, float* loss, void* ws,
+                              size_t ws_bytes, void* stream);
+
+typedef struct {
+  const float* logits;      /* device [T,E] of moe_route_logits */
+  const int32_t* topk_idx;  /* device [T,K], a token's ids distinct; ids outside [0, E) have no part */
+  const float* dtopk_w;     /* device [T,K]: gradient of the mixing weights, or NULL */
+  const int32_t* counts;    /* device [n_seq,E] of moe_balance_loss, or NULL: no balance loss */
+  float balance_coef;       /* its coef */
+  const float* dloss;       /* device scalar: gradient of the balance loss; NULL: 1 */
+  const void* x;            /* device bf16 [T,H]; needed for drouter_w */
+  const float* router_w;    /* device [E,H]; needed for dx */
+  float* dlogits;           /* device [T,E], or NULL */
+  float* drouter_w;         /* device [E,H], or NULL */
+  int32_t accumulate_w;     /* nonzero: added to drouter_w */
+  void* dx;                 /* device bf16 or fp32 [T,H], or NULL */
+  int32_t dx_dtype;         /* moe_dtype_t */
+  int32_t accumulate_x;     /* nonzero: added to dx (fp32 only) */
+} moe_router_backward_t;
+
+/* Backward pass of the router.  The gradient of the logits has two parts: through the mixing weights
+ * (w = routed_scaling_factor s_k, divided by the chosen scores' sum with norm_topk_prob; the selection
+ * itself has no gradient, nor has the bias) and through the balance loss, whose counts are constants:
+ *   dlogits = dw/dl^T dtopk_w + dloss dloss/dl;   drouter_w = dlogits^T x;   dx = dlogits router_w
+ * dtopk_w or counts must be given, and one of the outputs.  ws may be NULL if only dlogits is wanted.
+ * An infinity or NaN in a token's logits or gradients makes that token's dlogits and dx, and drouter_w, not finite.
+ * T = 0 writes zeros to drouter_w (or leaves it, accumulating).  Results have a fixed order of sums. */
+moe_status_t moe_router_backward(const moe_config_t* cfg, int64_t T, const moe_sequences_t* sequences,
+                                 const moe_router_backward_t* grads, void* ws, size_t ws_bytes, void* stream);
+
+/* ---- Norm over many gradients, and clipping -------------------------------------------------
+ * A plan lists the gradients once, as moe_adamw_plan lists its tensors; types may differ from tensor
+ * to tensor.  Clipping writes `out`, or the gradients themselves. */
+typedef struct {           /* device arrays of one tensor, 16-byte aligned */
+  void* grad;              /* [numel] grad_dtype; written by the clipping where out is NULL */
+  void* out;               /* [numel] out_dtype; NULL (or grad): in place, out_dtype = grad_dtype */
+  int64_t numel;           /* may be 0 */
+  int32_t grad_dtype, out_dtype;  /* moe_dtype_t */
+} moe_grad_tensor_t;
+
+typedef struct {
+  int64_t n_tensors, n_chunks;
+  size_t image_bytes;      /* size of the plan's image */
+  size_t workspace_bytes;  /* of moe_grad_norm */
+} moe_grad_plan_t;
+
+/* Host call: fills *plan and, with image (host memory, plan->image_bytes), the table that the two calls
+ * below read; the caller copies it to device memory once (16-byte aligned) and keeps it as long as the
+ * arrays stay where they are.  Arrays that the clipping writes must overlap no other. */
+moe_status_t moe_grad_plan(int64_t n_tensors, const moe_grad_tensor_t* tensors, moe_grad_plan_t* plan, void* image,
+                           size_t image_bytes);
+
+/* norm = |scale| sqrt(sum of all gradients' squares), coef = scale if norm <= max_norm, else
+ * scale max_norm / norm: what the gradients are multiplied with so that their norm is at most max_norm
+ * (moe_adamw_step's grad_scale, or moe_grad_clip).  scale: of the gradients as they lie, 1 / micro-batches
+ * for sums over micro-batches.  max_norm may be infinite.  Squares are added so that no finite gradient
+ * overflows or vanishes; an infinite gradient makes norm infinite and coef 0, a NaN both NaN.
+ *   norm, coef  device fp32 [1] (coef may be NULL)
+ *   ws          device, 256-byte aligned, plan->workspace_bytes; holds nothing between calls
+ * Memory that does not hold the plan's image is recognised as by moe_adamw_step: nothing is written. */
+moe_status_t moe_grad_norm(const moe_grad_plan_t* plan, const void* image, double max_norm, double scale, float* norm,
+                           float* coef, void* ws, size_t ws_bytes, void* stream);
+
+/* out = *coef grad for every tensor of the plan, rounded once to out's type.  In place, a coef of 1 is
+ * found on the device and nothing is read or written.  coef lies outside the plan's arrays. */
+moe_status_t moe_grad_clip(const moe_grad_plan_t* plan, const void* image, const float* coef, void* stream);
+
 /* Static text for a status code. */
 const char* moe_status_string(moe_status_t status);
 

@@ -25,6 +25,8 @@ __all__ = ["MoEConfig", "MoEExpertWeights", "MoEError", "lib_path", "load_librar
            "MOE_DTYPE_BF16", "MOE_DTYPE_FP32", "MOE_STATE_FP32", "MOE_STATE_8BIT",
            "moe_grouped_gemm", "moe_grouped_gemm_dgrad", "moe_grouped_gemm_wgrad", "moe_swiglu", "moe_swiglu_backward",
            "MoEAdamWPlan", "moe_adamw_step", "moe_adamw_dequantise",
+           "moe_route_logits", "moe_router_workspace_size", "moe_balance_loss", "moe_router_backward", "MoEGradPlan",
+           "moe_grad_norm", "moe_grad_clip",
            "EXPORTED_SYMBOLS"]
 
 MOE_WEIGHTS_BF16 = 0
@@ -44,7 +46,8 @@ EXPORTED_SYMBOLS = ("moe_workspace_size", "moe_route", "moe_dispatch", "moe_expe
                     "moe_dense_ffn_workspace_size", "moe_dense_ffn", "moe_forward_noalloc", "moe_quantise_mxfp8",
                     "moe_pack_mxfp4", "moe_pack_mxfp8", "moe_grouped_gemm", "moe_grouped_gemm_dgrad",
                     "moe_grouped_gemm_wgrad", "moe_swiglu", "moe_swiglu_backward", "moe_adamw_plan", "moe_adamw_step",
-                    "moe_adamw_dequantise", "moe_status_string", "moe_last_error")
+                    "moe_adamw_dequantise", "moe_route_logits", "moe_router_workspace_size", "moe_balance_loss",
+                    "moe_router_backward", "moe_grad_plan", "moe_grad_norm", "moe_grad_clip", "moe_status_string", "moe_last_error")
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 
@@ -95,6 +98,28 @@ class _AdamWConfig(ctypes.Structure):
                 ("step_ptr", ctypes.c_void_p), ("grad_scale", ctypes.c_void_p)]
 
 
+class _Sequences(ctypes.Structure):
+    _fields_ = [("n_seq", ctypes.c_int32), ("offsets", ctypes.c_void_p), ("lens", ctypes.c_void_p)]
+
+
+class _RouterBackward(ctypes.Structure):
+    _fields_ = [("logits", ctypes.c_void_p), ("topk_idx", ctypes.c_void_p), ("dtopk_w", ctypes.c_void_p),
+                ("counts", ctypes.c_void_p), ("balance_coef", ctypes.c_float), ("dloss", ctypes.c_void_p),
+                ("x", ctypes.c_void_p), ("router_w", ctypes.c_void_p), ("dlogits", ctypes.c_void_p),
+                ("drouter_w", ctypes.c_void_p), ("accumulate_w", ctypes.c_int32), ("dx", ctypes.c_void_p),
+                ("dx_dtype", ctypes.c_int32), ("accumulate_x", ctypes.c_int32)]
+
+
+class _GradTensor(ctypes.Structure):
+    _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("numel", ctypes.c_int64),
+                ("grad_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
+
+
+class _GradPlan(ctypes.Structure):
+    _fields_ = [("n_tensors", ctypes.c_int64), ("n_chunks", ctypes.c_int64), ("image_bytes", ctypes.c_size_t),
+                ("workspace_bytes", ctypes.c_size_t)]
+
+
 class MoEExpertWeights:
     """moe_expert_weights_t built from device tensors (references are kept alive here)."""
 
@@ -124,6 +149,7 @@ def load_library():
     P, I64, SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t
     C = ctypes.POINTER(MoEConfig)
     W = ctypes.POINTER(_Weights)
+    SQ = ctypes.POINTER(_Sequences)
     I32, GR, RW = ctypes.c_int32, ctypes.POINTER(_Groups), ctypes.POINTER(_Rows)
     sigs = {
         "moe_workspace_size": [C, I64, ctypes.POINTER(SZ)],
@@ -150,6 +176,13 @@ def load_library():
         "moe_adamw_plan": [I64, P, I32, I32, I32, ctypes.POINTER(_AdamWPlan), P, SZ],
         "moe_adamw_step": [ctypes.POINTER(_AdamWConfig), ctypes.POINTER(_AdamWPlan), P, P],
         "moe_adamw_dequantise": [P, P, I64, I32, P, P],
+        "moe_route_logits": [C, I64, P, P, P, P, P, P, P, SZ, P],
+        "moe_router_workspace_size": [C, I64, I32, ctypes.POINTER(SZ)],
+        "moe_balance_loss": [C, I64, SQ, P, P, ctypes.c_float, P, P, P, P, SZ, P],
+        "moe_router_backward": [C, I64, SQ, ctypes.POINTER(_RouterBackward), P, SZ, P],
+        "moe_grad_plan": [I64, P, ctypes.POINTER(_GradPlan), P, SZ],
+        "moe_grad_norm": [ctypes.POINTER(_GradPlan), P, ctypes.c_double, ctypes.c_double, P, P, P, SZ, P],
+        "moe_grad_clip": [ctypes.POINTER(_GradPlan), P, P, P],
     }
     for name, args in sigs.items():
         fn = getattr(lib, name)
@@ -661,3 +694,173 @@ def moe_adamw_dequantise(codes, scales, out, signed, stream=None):
     _vector(out, "out", torch.float32, n, dev)
     _enqueue(load_library().moe_adamw_dequantise, dev, stream, codes.data_ptr(), scales.data_ptr(), n, 1 if signed else 0,
              out.data_ptr())
+
+
+# ---- training the router ---------------------------------------------------------------------------
+
+def _exact(t, name, dtype, shape, dev):
+    """Address of a contiguous tensor of that type and shape."""
+    try:
+        wrong = t.dtype is not dtype or t.dim() != len(shape) or t.get_device() != dev
+    except AttributeError:  # no tensor
+        wrong = True
+    if wrong:
+        _explain(t, name, dtype, len(shape), dev)
+    if t.shape != shape:
+        _refuse(f"{name} is {tuple(t.shape)}, {tuple(shape)} needed")
+    if not t.is_contiguous():
+        _refuse(f"{name} must be contiguous")
+    return t.data_ptr() or None
+
+
+def _workspace(ws, dev):
+    if ws is None:
+        return None, 0
+    if not isinstance(ws, _torch().Tensor) or ws.get_device() != dev or not ws.is_contiguous():
+        _refuse("ws must be a contiguous tensor on the device of the others")
+    return ws.data_ptr() or None, ws.numel() * ws.element_size()
+
+
+def _sequences(seq_offsets, seq_lens, dev):
+    """(moe_sequences_t or None, number of sequences)"""
+    if seq_offsets is None and seq_lens is None:
+        return None, 1
+    int32 = _torch().int32
+    n = 1
+    if seq_offsets is not None:
+        n = _vector(seq_offsets, "seq_offsets", int32, None, dev) - 1
+    if seq_lens is not None:
+        _vector(seq_lens, "seq_lens", int32, n, dev)
+    return _Sequences(n, None if seq_offsets is None else seq_offsets.data_ptr(), None if seq_lens is None else seq_lens.data_ptr()), n
+
+
+def _config(cfg):
+    if not isinstance(cfg, MoEConfig):
+        _refuse("cfg must be a MoEConfig")
+    return cfg.num_experts, cfg.num_experts_per_tok, cfg.hidden_size
+
+
+def moe_route_logits(cfg, T, x, router_w, expert_bias, topk_idx, topk_w, logits, ws, stream=None):
+    """moe_route that keeps the logits: fp32 [T, E]."""
+    E, K, H = _config(cfg)
+    torch, dev = _torch(), _device_of(logits, "logits")
+    p, n = _workspace(ws, dev)
+    _enqueue(load_library().moe_route_logits, dev, stream, cfg, T, _exact(x, "x", torch.bfloat16, (T, H), dev),
+             _exact(router_w, "router_w", torch.float32, (E, H), dev),
+             None if expert_bias is None else _exact(expert_bias, "expert_bias", torch.float32, (E,), dev),
+             _exact(topk_idx, "topk_idx", torch.int32, (T, K), dev), _exact(topk_w, "topk_w", torch.float32, (T, K), dev),
+             _exact(logits, "logits", torch.float32, (T, E), dev), p, n)
+
+
+def moe_router_workspace_size(cfg, T, n_seq=1) -> int:
+    """Bytes of workspace that moe_balance_loss and moe_router_backward need."""
+    n = ctypes.c_size_t()
+    _check(load_library().moe_router_workspace_size(ctypes.byref(cfg), T, n_seq, ctypes.byref(n)))
+    return n.value
+
+
+def moe_balance_loss(cfg, T, logits, topk_idx, coef, counts, probs, loss, ws, seq_offsets=None, seq_lens=None, stream=None):
+    """Balance loss of the router: logits fp32 [T, E] and topk_idx int32 [T, K] -> counts int32 [B, E],
+    probs fp32 [B, E], loss fp32 [1].  seq_offsets int32 [B+1] (None: one sequence of all tokens),
+    seq_lens int32 [B]: tokens of each run that are no padding (None: all)."""
+    E, K, _ = _config(cfg)
+    torch, dev = _torch(), _device_of(logits, "logits")
+    seqs, B = _sequences(seq_offsets, seq_lens, dev)
+    p, n = _workspace(ws, dev)
+    _enqueue(load_library().moe_balance_loss, dev, stream, cfg, T, seqs, _exact(logits, "logits", torch.float32, (T, E), dev),
+             _exact(topk_idx, "topk_idx", torch.int32, (T, K), dev), coef, _exact(counts, "counts", torch.int32, (B, E), dev),
+             _exact(probs, "probs", torch.float32, (B, E), dev), _exact(loss, "loss", torch.float32, (1,), dev), p, n)
+
+
+def moe_router_backward(cfg, T, logits, topk_idx, dtopk_w=None, counts=None, coef=0.0, dloss=None, seq_offsets=None,
+                        seq_lens=None, dlogits=None, x=None, router_w=None, drouter_w=None, accumulate_w=False, dx=None,
+                        accumulate_x=False, ws=None, stream=None):
+    """Backward pass of the router from the gradient of the mixing weights (dtopk_w fp32 [T, K]) and of the
+    balance loss (its counts int32 [B, E] and coef; dloss fp32 [1], None: 1) to dlogits fp32 [T, E],
+    drouter_w fp32 [E, H] (needs x bf16 [T, H]) and dx bf16 or fp32 [T, H] (needs router_w fp32 [E, H]),
+    those that are given; accumulate_w and accumulate_x (fp32 only) add to what lies there."""
+    E, K, H = _config(cfg)
+    torch, dev = _torch(), _device_of(logits, "logits")
+    F = torch.float32
+    seqs, B = _sequences(seq_offsets, seq_lens, dev)
+    if drouter_w is not None and x is None or dx is not None and router_w is None:
+        _refuse("drouter_w needs x, and dx needs router_w")
+    opt = lambda t, name, dtype, shape: None if t is None else _exact(t, name, dtype, shape, dev)  # noqa: E731
+    p, n = _workspace(ws, dev)
+    dx_at, dx_type = None, 0
+    if dx is not None:
+        dx_type = _dtype_code(dx, "dx") if isinstance(dx, torch.Tensor) else 0
+        dx_at = _exact(dx, "dx", F if dx_type else torch.bfloat16, (T, H), dev)
+    g = _RouterBackward(_exact(logits, "logits", F, (T, E), dev), opt(topk_idx, "topk_idx", torch.int32, (T, K)),
+                        opt(dtopk_w, "dtopk_w", F, (T, K)), opt(counts, "counts", torch.int32, (B, E)), coef,
+                        None if dloss is None else _scalar_at(dloss, "dloss", F, dev), opt(x, "x", torch.bfloat16, (T, H)),
+                        opt(router_w, "router_w", F, (E, H)), opt(dlogits, "dlogits", F, (T, E)),
+                        opt(drouter_w, "drouter_w", F, (E, H)), 1 if accumulate_w else 0, dx_at, dx_type, 1 if accumulate_x else 0)
+    _enqueue(load_library().moe_router_backward, dev, stream, cfg, T, seqs, g, p, n)
+
+
+class MoEGradPlan:
+    """The table of a norm over many gradients (moe_grad_plan): built once, kept with its tensors, which
+    must stay where they are.  grads: contiguous tensors on one device, bf16 or fp32; out: as many of the
+    same sizes, bf16 or fp32, that moe_grad_clip writes (None: the gradients themselves)."""
+
+    def __init__(self, grads, out=None):
+        torch = _torch()
+        try:
+            grads, out = list(grads), None if out is None else list(out)
+        except TypeError:
+            _refuse("grads and out must be lists of tensors")
+        if not grads:
+            _refuse("grads must not be empty")
+        if out is not None and len(out) != len(grads):
+            _refuse(f"out has {len(out)} tensors, grads {len(grads)}")
+        dev = _device_of(grads[0], "grads[0]")
+        for name, ts in (("grads", grads), ("out", out or [])):
+            for i, t in enumerate(ts):
+                if not isinstance(t, torch.Tensor):
+                    _refuse(f"{name}[{i}] must be a tensor")
+                if t.get_device() != dev or dev < 0:
+                    _refuse(f"{name}[{i}] lies on {t.device}; one GPU must hold them all")
+                if not t.is_contiguous():
+                    _refuse(f"{name}[{i}] must be contiguous")
+                if t.numel() != grads[i].numel():
+                    _refuse(f"{name}[{i}] has {t.numel()} values, {grads[i].numel()} needed")
+        types = [_dtype_code(t, f"grads[{i}]") for i, t in enumerate(grads)]
+        kept = types if out is None else [_dtype_code(t, f"out[{i}]") for i, t in enumerate(out)]
+        at = [None] * len(grads) if out is None else [t.data_ptr() or None for t in out]
+        table = (_GradTensor * len(grads))(*zip([t.data_ptr() or None for t in grads], at, [t.numel() for t in grads], types, kept))
+        self._keep, self.device, self.struct = (grads, out), grads[0].device, _GradPlan()
+        lib, args = load_library(), (len(grads), ctypes.byref(table), ctypes.byref(self.struct))
+        _check(lib.moe_grad_plan(*args, None, 0))
+        host = torch.empty(self.struct.image_bytes, dtype=torch.uint8)
+        _check(lib.moe_grad_plan(*args, host.data_ptr(), host.numel()))
+        self.image = host.to(self.device)
+        self.at, self.home = self.image.data_ptr(), _raw_stream(dev)
+
+    @property
+    def workspace_size(self) -> int:
+        """Bytes of workspace that moe_grad_norm needs."""
+        return self.struct.workspace_bytes
+
+    _used_on = MoEAdamWPlan._used_on
+
+
+def moe_grad_norm(plan: MoEGradPlan, max_norm, norm, coef, ws, scale=1.0, stream=None):
+    """norm (fp32 [1]) of the plan's gradients times |scale|, and coef (fp32 [1] or None), what they are
+    multiplied with so that it is at most max_norm: scale, or scale max_norm / norm."""
+    if not isinstance(plan, MoEGradPlan):
+        _refuse("plan must be a MoEGradPlan")
+    dev, F = plan.device.index, _torch().float32
+    p, n = _workspace(ws, dev)
+    _enqueue(load_library().moe_grad_norm, dev, stream, plan.struct, plan.at, max_norm, scale, _scalar_at(norm, "norm", F, dev),
+             None if coef is None else _scalar_at(coef, "coef", F, dev), p, n)
+    plan._used_on(stream)
+
+
+def moe_grad_clip(plan: MoEGradPlan, coef, stream=None):
+    """out = coef grad for every tensor of the plan (in place where it has no out); coef fp32 [1]."""
+    if not isinstance(plan, MoEGradPlan):
+        _refuse("plan must be a MoEGradPlan")
+    dev = plan.device.index
+    _enqueue(load_library().moe_grad_clip, dev, stream, plan.struct, plan.at, _scalar_at(coef, "coef", _torch().float32, dev))
+    plan._used_on(stream)

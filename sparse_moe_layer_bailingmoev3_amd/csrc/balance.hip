@@ -1,0 +1,276 @@
+// Balance loss of a router: how evenly the tokens of each sequence load the experts.
+//
+//   p_te = s_te / sum_j s_tj,  s = sigmoid(logits)      P_be = mean of p_te over the tokens of sequence b
+//   c_be = (token, slot) pairs of sequence b at e       f_be = E c_be / (K n_b)
+//   loss = coef sum_b (n_b / N) sum_e f_be P_be  =  coef E / (K N) sum_be c_be P_be
+//
+// Two launches.  The first cuts the tokens into chunks; a workgroup walks the sequences that its
+// chunk touches, its waves taking a token each (a lane EPL experts of it), and leaves one row of
+// sums and counts per (chunk c, sequence b) in slot c + b of the workspace.  (Both grow along the
+// walk and one of them at every step, so no two pairs share a slot.)  The second adds a sequence's
+// slots, 64 experts a workgroup, and its last workgroup to finish adds the parts of the loss.
+// Every sum has a fixed order.
+//
+// Counts are integers: LDS atomics, whose order does not matter.
+#include "router_scores.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int BAL_WAVES = 8;
+
+template <int EPL>
+__global__ __launch_bounds__(BAL_WAVES * 64) void balance_partial_kernel(BalanceArgs a) {
+  constexpr int E = EPL * 64;
+  __shared__ __align__(16) float sums[BAL_WAVES][E];
+  __shared__ int hist[E];
+  __shared__ int first;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.done = 0;
+  const int t0 = blockIdx.x * a.chunk, t1 = (int)min((int64_t)t0 + a.chunk, (int64_t)a.seq.T);
+  for (int i = threadIdx.x; i < E; i += BAL_WAVES * 64) hist[i] = 0;
+  int b = seq_of(a.seq, t0, &first);
+  __syncthreads();
+  for (; b < a.seq.n; ++b) {
+    const Seq q = seq_at(a.seq, b);
+    if (q.begin >= t1) break;
+    const int lo = max(q.begin, t0), hi = min(q.end, t1);
+    if (lo < hi) {
+      float acc[EPL] = {};
+      for (int t = lo + wave; t < hi; t += BAL_WAVES) {
+        float l[EPL], s[EPL], total = 0.f;
+        Row<EPL>::load(a.logits + (int64_t)t * E, lane, l);
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+          s[i] = score_of(l[i]).s;
+          total += s[i];
+        }
+        total = wave_sum(total);
+        const float inv = total == 0.f ? 0.f : 1.0f / total;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) acc[i] += s[i] * inv;
+      }
+      const int64_t p1 = (int64_t)hi * a.K;
+      for (int64_t p = (int64_t)lo * a.K + threadIdx.x; p < p1; p += BAL_WAVES * 64) {
+        const int e = a.topk_idx[p];
+        if ((unsigned)e < (unsigned)E) atomicAdd(&hist[e], 1);
+      }
+      Row<EPL>::store(sums[wave], lane, acc);
+      __syncthreads();
+      const int64_t slot = (int64_t)blockIdx.x + b;
+      for (int e = threadIdx.x; e < E; e += BAL_WAVES * 64) {
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < BAL_WAVES; ++w) v += sums[w][e];
+        a.psum[slot * E + e] = v;
+        a.pcnt[slot * E + e] = hist[e];
+        hist[e] = 0;
+      }
+      __syncthreads();
+    }
+    if (q.next >= t1) break;
+  }
+}
+
+// Sequence blockIdx.x, experts 64 blockIdx.y ..; the waves take every 16th slot.
+__global__ __launch_bounds__(1024) void balance_finish_kernel(BalanceArgs a) {
+  __shared__ double sums[16][64];
+  __shared__ int cnts[16][64];
+  __shared__ int tokens, last;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int b = blockIdx.x, e = blockIdx.y * 64 + lane;
+  const Seq q = seq_at(a.seq, b);
+  double sum = 0;
+  int cnt = 0;
+  if (q.begin < q.end) {
+    const int c1 = (q.end - 1) / a.chunk;
+#pragma unroll 4
+    for (int c = q.begin / a.chunk + wave; c <= c1; c += 16) {
+      const int64_t at = ((int64_t)c + b) * a.E + e;
+      sum += a.psum[at];
+      cnt += a.pcnt[at];
+    }
+  }
+  sums[wave][lane] = sum;
+  cnts[wave][lane] = cnt;
+  __syncthreads();
+  if (wave == 0) {
+    for (int w = 1; w < 16; ++w) {
+      sum += sums[w][lane];
+      cnt += cnts[w][lane];
+    }
+    const int n = q.end - q.begin;
+    const double mean = n > 0 ? sum / n : 0.0;
+    const int64_t at = (int64_t)b * a.E + e;
+    a.counts[at] = cnt;
+    a.probs[at] = (float)mean;
+    double part = cnt * mean;
+#pragma unroll
+    for (int m = 32; m >= 1; m >>= 1) part += __shfl_xor(part, m, WAVE);
+    if (lane == 0) {
+      a.part[(int64_t)b * gridDim.y + blockIdx.y] = part;
+      __threadfence();
+      last = atomicAdd(a.done, 1) == (int)(gridDim.x * gridDim.y) - 1;
+    }
+  }
+  __syncthreads();
+  if (!last) return;
+  // the last workgroup: all parts in order, read past the caches that do not see other dies' stores
+  __threadfence();
+  double total = 0;
+  const int64_t n = (int64_t)gridDim.x * gridDim.y;
+  for (int64_t i = threadIdx.x; i < n; i += 1024)
+    total += __hip_atomic_load(a.part + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+  for (int m = 32; m >= 1; m >>= 1) total += __shfl_xor(total, m, WAVE);
+  const int N = seq_tokens(a.seq, &tokens);
+  __syncthreads();
+  if (lane == 0) sums[0][wave] = total;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    total = 0;
+    for (int w = 0; w < 16; ++w) total += sums[0][w];
+    *a.loss = N > 0 ? (float)((double)a.coef * a.E * total / ((double)a.K * N)) : 0.f;
+  }
+}
+
+// ---- the gradient of the logits ------------------------------------------------------------------
+//   through the mixing weights, w_k = c s_k / sum_j s_j (or c s_k):
+//     dl_k = (g_k - sum_j g_j q_j) q_k (1 - s_k),  g = c dw, q = s / sum s      (or g_k s_k (1 - s_k))
+//   through the balance loss (the counts are constants to it):
+//     dl_e += dloss coef / N (f_e - sum_j f_j p_j) p_e (1 - s_e)
+// A wave takes `run` consecutive tokens, a lane EPL experts of each; the K chosen experts' part is
+// computed by K lanes and handed to the experts' lanes through LDS.
+template <int EPL>
+__global__ __launch_bounds__(256) void dlogits_kernel(DlogitsArgs a) {
+  constexpr int E = EPL * 64;
+  __shared__ __align__(16) float rows[4][E];
+  __shared__ int first, tokens;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t base = (int64_t)blockIdx.x * 4 * a.run;
+  int b = 0;
+  float g0 = 0.f;
+  if (a.counts) {
+    b = seq_of(a.seq, (int)base, &first);
+    const int N = seq_tokens(a.seq, &tokens);
+    g0 = N > 0 ? a.coef / (float)N : 0.f;
+    if (a.dloss) g0 *= *a.dloss;
+  }
+  Seq q{0, 0, 0};
+  float f[EPL] = {};
+  bool have = false;
+  const int64_t t0 = base + (int64_t)wave * a.run, t1 = min(t0 + a.run, (int64_t)a.seq.T);
+  for (int64_t t = t0; t < t1; ++t) {
+    float l[EPL], d[EPL];
+    Row<EPL>::load(a.logits + t * E, lane, l);
+    Score s[EPL];
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      s[i] = score_of(l[i]);
+      d[i] = 0.f;
+    }
+    if (a.counts) {
+      while (b < a.seq.n && (!have || q.next <= t)) {  // on to the token's sequence
+        if (have) ++b;
+        if (b >= a.seq.n) break;
+        q = seq_at(a.seq, b);
+        have = true;
+        if (q.next <= t) continue;
+        int32_t c[EPL];
+        Row<EPL>::load(a.counts + (int64_t)b * E, lane, c);
+        const float per = q.end > q.begin ? (float)E / ((float)a.K * (float)(q.end - q.begin)) : 0.f;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) f[i] = (float)c[i] * per;
+      }
+      if (b < a.seq.n && t >= q.begin && t < q.end) {
+        float total = 0.f, load = 0.f;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+          total += s[i].s;
+          load += f[i] * s[i].s;
+        }
+        total = wave_sum(total);
+        load = wave_sum(load);
+        const float inv = total == 0.f ? 0.f : 1.0f / total;
+        const float mean = load * inv, g = g0 * inv;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) d[i] = g * (f[i] - mean) * s[i].s * s[i].r;
+      }
+    }
+    if (a.dtopk_w) {
+      const float zero[EPL] = {};
+      Row<EPL>::store(rows[wave], lane, zero);
+      float v = 0.f;
+      int e = -1;
+      if (lane < a.K) {
+        e = a.topk_idx[t * a.K + lane];
+        if ((unsigned)e >= (unsigned)E) e = -1;
+      }
+      Score k{0.f, 0.f};
+      float g = 0.f;
+      if (e >= 0) {
+        k = score_of(a.logits[t * E + e]);
+        g = a.dtopk_w[t * a.K + lane] * a.scale;
+      }
+      if (a.norm) {
+        const float total = lane_of(row_sum(k.s), 0);  // (K <= 16: one row of lanes)
+        const float share = total == 0.f ? 0.f : k.s / total;
+        const float mean = lane_of(row_sum(g * share), 0);
+        v = (g - mean) * share * k.r;
+      } else {
+        v = g * k.s * k.r;
+      }
+      // (a wave's LDS accesses run in order; the compiler, which sees one lane, must keep them so)
+      asm volatile("" ::: "memory");
+      if (e >= 0) atomicAdd(&rows[wave][e], v);
+      asm volatile("" ::: "memory");
+      float add[EPL];
+      Row<EPL>::load(rows[wave], lane, add);
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) d[i] += add[i];
+    }
+    Row<EPL>::store(a.dlogits + t * E, lane, d);
+  }
+}
+
+}  // namespace
+
+int balance_chunk(int64_t T) {
+  int c = 32;
+  while (c < 256 && T > (int64_t)c * 1024) c *= 2;
+  return c;
+}
+
+#define MOE_EPL(E, F)          \
+  switch ((E) / WAVE) {        \
+    case 1: F(1); break;       \
+    case 2: F(2); break;       \
+    case 4: F(4); break;       \
+    case 8: F(8); break;       \
+    case 16: F(16); break;     \
+    default: return hipErrorInvalidValue; \
+  }
+
+hipError_t launch_balance(const BalanceArgs& a, hipStream_t s) {
+  const unsigned chunks = (unsigned)std::max<int64_t>(((int64_t)a.seq.T + a.chunk - 1) / a.chunk, 1);
+#define MOE_BAL(N) hipLaunchKernelGGL(balance_partial_kernel<N>, dim3(chunks), dim3(BAL_WAVES * 64), 0, s, a)
+  MOE_EPL(a.E, MOE_BAL)
+#undef MOE_BAL
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(balance_finish_kernel, dim3((unsigned)a.seq.n, (unsigned)(a.E / 64)), dim3(1024), 0, s, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_dlogits(DlogitsArgs a, hipStream_t s) {
+  if (a.seq.T == 0) return hipSuccess;
+  a.run = (int)std::min<int64_t>(std::max<int64_t>(a.seq.T / 4096, 1), 8);
+  const unsigned grid = (unsigned)(((int64_t)a.seq.T + 4 * a.run - 1) / (4 * a.run));
+#define MOE_DL(N) hipLaunchKernelGGL(dlogits_kernel<N>, dim3(grid), dim3(256), 0, s, a)
+  MOE_EPL(a.E, MOE_DL)
+#undef MOE_DL
+  return hipGetLastError();
+}
+
+}  // namespace moe

@@ -281,6 +281,7 @@ moe_status_t do_combine(const moe_config_t* c, int64_t T, const void* y, const i
 
 namespace moe {
 void set_last_error(const char* msg) { g_last_error = msg; }
+moe_status_t check_config(const moe_config_t* c, int64_t T) { return validate_config(c, T); }
 }  // namespace moe
 
 extern "C" {
@@ -323,6 +324,35 @@ moe_status_t moe_route(const moe_config_t* cfg, int64_t T, const void* x, const 
   Layout L;
   if ((st = check_ws(cfg, T, ws, ws_bytes, &L)) != MOE_OK) return st;
   return do_route(cfg, T, x, router_w, expert_bias, topk_idx, topk_w, L, ws, (hipStream_t)stream);
+}
+
+moe_status_t moe_route_logits(const moe_config_t* cfg, int64_t T, const void* x, const float* router_w,
+                              const float* expert_bias, int32_t* topk_idx, float* topk_w, float* logits, void* ws,
+                              size_t ws_bytes, void* stream) {
+  g_last_error.clear();
+  moe_status_t st = validate_config(cfg, T);
+  if (st != MOE_OK) return st;
+  if (T == 0) return MOE_OK;
+  MOE_CHECK_PTR(x, "x");
+  MOE_CHECK_PTR(router_w, "router_w");
+  MOE_CHECK_OPT_PTR(expert_bias, "expert_bias");
+  MOE_CHECK_PTR(topk_idx, "topk_idx");
+  MOE_CHECK_PTR(topk_w, "topk_w");
+  MOE_CHECK_PTR(logits, "logits");
+  Layout L;
+  if ((st = check_ws(cfg, T, ws, ws_bytes, &L)) != MOE_OK) return st;
+  const int E = cfg->num_experts;
+  const moe::RouterPlan p = moe::router_plan(T, cfg->hidden_size, E);
+  float* partial = p.nsplit > 1 ? (float*)at(ws, L.partial) : logits;
+  hipStream_t s = (hipStream_t)stream;
+  hipError_t e = moe::launch_router_logits(p, (const uint16_t*)x, router_w, (int)T, cfg->hidden_size, E, partial, nullptr, 0, s);
+  if (e != hipSuccess) return hip_fail(e, "router logits launch");
+  if (p.nsplit > 1) e = moe::launch_sum_logits(partial, p.nsplit, T * E, logits, s);
+  if (e != hipSuccess) return hip_fail(e, "router logits sum launch");
+  e = moe::launch_router_topk(logits, 1, (int)T, E, expert_bias, cfg->n_group, cfg->topk_group, cfg->num_experts_per_tok,
+                              cfg->norm_topk_prob, cfg->routed_scaling_factor, topk_idx, topk_w, nullptr, moe::FusedDispatch(), s);
+  if (e != hipSuccess) return hip_fail(e, "router top-k launch");
+  return MOE_OK;
 }
 
 moe_status_t moe_dispatch(const moe_config_t* cfg, int64_t T, const int32_t* topk_idx, int32_t* expert_counts,

@@ -5,6 +5,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "moe.h"
+
 namespace moe {
 
 // routed-expert weight formats (moe_weight_format_t values)
@@ -188,6 +190,9 @@ hipError_t launch_dense_ffn_small(const uint16_t* x, const uint16_t* gate, const
 // compute units of the current device (asked once per device); 0 if there is none
 int device_cu_count();
 
+// the checks of a layer's configuration for T tokens; a refusal is recorded as the last error
+moe_status_t check_config(const moe_config_t* c, int64_t T);
+
 // records `msg` as the calling thread's last error (moe_last_error) and returns nothing
 void set_last_error(const char* msg);
 
@@ -253,6 +258,70 @@ enum { ADAMW_PARAM_F32 = 1, ADAMW_GRAD_F32 = 2, ADAMW_EIGHT = 4, ADAMW_MASTER = 
 hipError_t launch_adamw(const AdamWArgs& a, hipStream_t s);
 hipError_t launch_adamw_dequantise(const uint8_t* codes, const float* scales, int64_t n, bool is_signed, float* out,
                                    hipStream_t s);
+
+// ---- training the router (balance.hip, router_grad.hip) --------------------------------
+// the sequences of T tokens: b holds tokens offsets[b] <= t < offsets[b+1], of these the first lens[b]
+struct SeqArgs {
+  const int32_t* offsets;  // [n + 1]; NULL: one sequence of all T
+  const int32_t* lens;     // [n] or NULL: all
+  int n, T;
+};
+struct BalanceArgs {
+  SeqArgs seq;
+  int E, K;
+  float coef;
+  const float* logits; const int32_t* topk_idx;
+  int chunk;               // tokens of a workgroup (balance_chunk)
+  float* psum; int32_t* pcnt;  // [chunks + n, E]: sums and counts of chunk c and sequence b in row c + b
+  double* part;            // [n, E / 64]: parts of the loss
+  int* done;               // workgroups of the second launch that have finished
+  int32_t* counts; float* probs; float* loss;
+};
+int balance_chunk(int64_t T);
+hipError_t launch_balance(const BalanceArgs& a, hipStream_t s);
+
+struct DlogitsArgs {
+  SeqArgs seq;
+  int E, K, norm;
+  float scale;             // routed_scaling_factor
+  const float* logits; const int32_t* topk_idx;
+  const float* dtopk_w;    // or NULL
+  const int32_t* counts;   // [n, E] or NULL: no balance loss
+  float coef; const float* dloss;
+  float* dlogits;
+  int run;                 // tokens of a wave (set by the launch)
+};
+hipError_t launch_dlogits(DlogitsArgs a, hipStream_t s);
+
+struct RouterGradArgs {
+  int T, E, H;
+  const float* dl;         // [T, E]
+  const uint16_t* x; const float* w;
+  float* dw; int acc_w;    // or NULL
+  void* dx; int dx_f32, acc_x;
+};
+hipError_t launch_router_grad(const RouterGradArgs& a, hipStream_t s);
+// out[t,e] = the partial logits added in split order
+hipError_t launch_sum_logits(const float* partial, int nsplit, int64_t n, float* out, hipStream_t s);
+
+// ---- norm over many gradients, clipping (grad_norm.hip) --------------------------------
+constexpr int GRAD_CHUNK = 16384;        // values of one table entry
+constexpr int GRAD_MAX_PARTIALS = 4096;  // workgroups of the norm: one sum each in the workspace
+constexpr uint64_t GRAD_MAGIC = 0x314e44415247454dull;
+struct GradHeader { uint64_t magic; int64_t n_tensors, n_chunks, pad; };  // plan image: header, tensors, chunks
+struct GradTensor { const void* in; void* out; int64_t numel; int64_t flags; };
+struct GradChunk { int32_t tensor, chunk; };
+enum { GRAD_IN_F32 = 1, GRAD_OUT_F32 = 2 };
+struct GradArgs {
+  const uint8_t* image;
+  int64_t n_tensors, n_chunks;
+  double scale, max_norm;
+  double* partial;
+  float* norm; float* coef_out;
+  const float* coef;
+};
+hipError_t launch_grad_norm(const GradArgs& a, hipStream_t s);
+hipError_t launch_grad_clip(const GradArgs& a, hipStream_t s);
 
 // ---- combine -----------------------------------------------------------------
 // y16: y_sorted holds fp16 values (the tile kernels' y16 output) instead of fp32

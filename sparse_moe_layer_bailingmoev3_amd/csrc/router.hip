@@ -21,6 +21,7 @@
 //                         top-k selection entirely in registers with wave shuffles; for up to
 //                         256 tokens the last workgroup to finish also builds the dispatch.
 //   expert_bias_update_kernel  the sign-rule bias step from a step's expert counts.
+//   sum_logits_kernel     the logits' partial sums added up, where the caller keeps the logits.
 #include "moe_common.h"
 #include "moe_internal.h"
 
@@ -567,7 +568,24 @@ __global__ __launch_bounds__(1024) void expert_bias_update_kernel(const int32_t*
   }
 }
 
+// The partial logits of the hidden dimension's splits added in the top-k kernel's order (0 + p0 + p1 ..:
+// the same bits), for a caller that keeps them.
+__global__ __launch_bounds__(256) void sum_logits_kernel(const float* __restrict__ partial, int nsplit, int64_t n,
+                                                         float* __restrict__ out) {
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= n) return;
+  floatx4 l{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int p = 0; p < nsplit; ++p) l += *(const floatx4*)(partial + (int64_t)p * n + i);
+  *(floatx4*)(out + i) = l;
+}
+
 }  // namespace
+
+hipError_t launch_sum_logits(const float* partial, int nsplit, int64_t n, float* out, hipStream_t s) {
+  hipLaunchKernelGGL(sum_logits_kernel, dim3((unsigned)((n + 1023) / 1024)), dim3(256), 0, s, partial, nsplit, n, out);
+  return hipGetLastError();
+}
 
 hipError_t launch_expert_bias_update(const int32_t* counts, int E, float gamma, float* bias, hipStream_t s) {
   if (E <= 0 || E > 1024) return hipErrorInvalidValue;

@@ -1,0 +1,125 @@
+// Device code shared by the kernels that read the router's logits: sigmoid scores, sums over a
+// wave, the sequences of a batch.
+#pragma once
+#include "moe_common.h"
+#include "moe_internal.h"
+
+namespace moe {
+
+// sigmoid of a logit and its complement, both to a few ulp of themselves whatever their size: from
+// e = exp(-|l|) <= 1 the larger is 1 / (1 + e), the smaller e times that.  exp through the hardware's
+// power of two; the product |l| log2(e) is carried with its rounding (else its 2^-24 would be
+// multiplied by |l|).
+struct Score {
+  float s, r;  // sigmoid(l), 1 - sigmoid(l)
+};
+__device__ __forceinline__ Score score_of(float l) {
+  float a = -fabsf(l);
+  a = a < -200.f ? -200.f : a;  // e is zero from -104 on; NaN stays
+  const float t = a * 1.44269504f;
+  const float lo = __builtin_fmaf(a, 1.44269504f, -t) + a * 1.92596299e-8f;
+  float e = __builtin_amdgcn_exp2f(t);
+  e = __builtin_fmaf(e, lo * 0.693147181f, e);
+  const float big = __builtin_amdgcn_rcpf(1.0f + e), small = e * big;
+  return l < 0.f ? Score{small, big} : Score{big, small};
+}
+
+// sum over the wave, in every lane: rows of 16 lanes by lane permutations (xor 1, xor 2, mirrors of 8
+// and 16), the four rows by lane reads
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float v) {
+  return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, true));
+}
+__device__ __forceinline__ float row_sum(float v) {  // over 16 lanes
+  v = dpp_add<0xB1>(v);
+  v = dpp_add<0x4E>(v);
+  v = dpp_add<0x141>(v);
+  return dpp_add<0x140>(v);
+}
+__device__ __forceinline__ float lane_of(float v, int l) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), l));
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  v = row_sum(v);
+  return (lane_of(v, 0) + lane_of(v, 16)) + (lane_of(v, 32) + lane_of(v, 48));
+}
+
+// A lane's experts of a row of E = 64 EPL values: pieces j of V consecutive ones, j * 64 V + lane * V,
+// so that a piece of the wave is contiguous.
+template <int EPL>
+struct Row {
+  static constexpr int V = EPL < 4 ? EPL : 4, NJ = EPL / V;
+  typedef float vec __attribute__((ext_vector_type(V)));
+  typedef int32_t ivec __attribute__((ext_vector_type(V)));
+  static __device__ __forceinline__ int at(int lane, int j) { return j * 64 * V + lane * V; }
+  static __device__ __forceinline__ void load(const float* p, int lane, float (&v)[EPL]) {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const vec x = *(const vec*)(p + at(lane, j));
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[j * V + i] = x[i];
+    }
+  }
+  static __device__ __forceinline__ void load(const int32_t* p, int lane, int32_t (&v)[EPL]) {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const ivec x = *(const ivec*)(p + at(lane, j));
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[j * V + i] = x[i];
+    }
+  }
+  static __device__ __forceinline__ void store(float* p, int lane, const float (&v)[EPL]) {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      vec x;
+#pragma unroll
+      for (int i = 0; i < V; ++i) x[i] = v[j * V + i];
+      *(vec*)(p + at(lane, j)) = x;
+    }
+  }
+};
+
+// The tokens of sequence b (begin <= t < end) and where the next sequence's run begins; all within
+// [0, T] whatever the arrays hold.
+struct Seq {
+  int begin, end, next;
+};
+__device__ __forceinline__ Seq seq_at(const SeqArgs& q, int b) {
+  Seq r{0, q.T, q.T};
+  if (q.offsets) {
+    r.begin = min(max(q.offsets[b], 0), q.T);
+    r.next = r.end = min(max(q.offsets[b + 1], r.begin), q.T);
+  }
+  if (q.lens) r.end = r.begin + min(max(q.lens[b], 0), r.end - r.begin);
+  return r;
+}
+
+// The first sequence whose run ends behind token t (n if none): the ends up to t are counted by the
+// whole workgroup.  `count`: one int in LDS.
+__device__ __forceinline__ int seq_of(const SeqArgs& q, int t, int* count) {
+  if (!q.offsets) return 0;
+  if (threadIdx.x == 0) *count = 0;
+  __syncthreads();
+  int c = 0;
+  for (int b = threadIdx.x; b < q.n; b += blockDim.x) c += q.offsets[b + 1] <= t;
+  if (c) atomicAdd(count, c);
+  __syncthreads();
+  return *count;
+}
+
+// Tokens of all sequences.  `count`: one int in LDS, not that of seq_of.
+__device__ __forceinline__ int seq_tokens(const SeqArgs& q, int* count) {
+  if (!q.lens) return q.offsets ? max(min(q.offsets[q.n], q.T) - max(q.offsets[0], 0), 0) : q.T;
+  if (threadIdx.x == 0) *count = 0;
+  __syncthreads();
+  int c = 0;
+  for (int b = threadIdx.x; b < q.n; b += blockDim.x) {
+    const Seq s = seq_at(q, b);
+    c += s.end - s.begin;
+  }
+  if (c) atomicAdd(count, c);
+  __syncthreads();
+  return *count;
+}
+
+}  // namespace moe
