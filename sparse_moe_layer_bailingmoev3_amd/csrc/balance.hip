@@ -135,6 +135,90 @@ __global__ __launch_bounds__(1024) void balance_finish_kernel(BalanceArgs a) {
   }
 }
 
+// ---- fp32 values in 16-bit pieces -------------------------------------------------------------
+
+// the exponent that brings values of magnitude up to `top` (as bits) below 2^15, the largest to 2^14 or
+// more (subnormal ones too, whose largest is below 2^-126)
+__device__ __forceinline__ int half_exponent(uint32_t top) { return 14 + 127 - (int)(top >> 23); }
+// two values times 2^ex -> two fp16 pieces each; infinities and NaN end as NaN
+__device__ __forceinline__ void half_pieces(float v0, float v1, int ex, uint32_t& hi, uint32_t& lo) {
+  typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+  v0 = __builtin_amdgcn_ldexpf(v0, ex);
+  v1 = __builtin_amdgcn_ldexpf(v1, ex);
+  const f16x2 h = {(_Float16)v0, (_Float16)v1};
+  const f16x2 l = {(_Float16)(v0 - (float)h[0]), (_Float16)(v1 - (float)h[1])};
+  hi = __builtin_bit_cast(uint32_t, h);
+  lo = __builtin_bit_cast(uint32_t, l);
+}
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, true));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, true));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, true));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, true));
+  auto at = [&](int l) { return (uint32_t)__builtin_amdgcn_readlane((int)v, l); };
+  return max(max(at(0), at(16)), max(at(32), at(48)));
+}
+
+// three bf16 (upper halves of words) that add up to v exactly; infinities and NaN end as NaN
+__device__ __forceinline__ void bf16_pieces(float v, uint32_t (&p)[3]) {
+  p[0] = __float_as_uint(v) & 0xFFFF0000u;
+  v -= __uint_as_float(p[0]);
+  p[1] = __float_as_uint(v) & 0xFFFF0000u;
+  p[2] = __float_as_uint(v - __uint_as_float(p[1])) & 0xFFFF0000u;
+}
+
+// a lane's share of a row in P planes of 16-bit pieces
+template <int EPL, int P>
+struct Pieces {
+  uint32_t w[P][(EPL + 1) / 2];
+  __device__ __forceinline__ void store(uint16_t* row, int64_t plane, int lane) const {
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+#pragma unroll
+      for (int j = 0; j < Row<EPL>::NJ; ++j) {
+        uint16_t* const at = row + p * plane + Row<EPL>::at(lane, j);
+        if constexpr (EPL == 1) *at = (uint16_t)w[p][0];
+        else if constexpr (EPL == 2) *(uint32_t*)at = w[p][0];
+        else *(u32x2*)at = u32x2{w[p][2 * j], w[p][2 * j + 1]};
+      }
+  }
+};
+
+// 16 columns of router_w, transposed, in scaled fp16 pieces: a thread takes 4 EPL consecutive experts of
+// a column.  `lds`: 256 words.
+template <int EPL>
+__device__ __forceinline__ void split_weight(const DlogitsArgs& a, int block, uint32_t* lds) {
+  constexpr int E = EPL * 64, N = 4 * EPL;
+  const int col = threadIdx.x & 15, grp = threadIdx.x >> 4, h = block * 16 + col;
+  float v[N];
+  uint32_t top = 0;
+  const float* src = a.w + (int64_t)grp * N * a.H + h;
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = src[(int64_t)i * a.H];
+#pragma unroll
+  for (int i = 0; i < N; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  lds[threadIdx.x] = top;
+  __syncthreads();
+#pragma unroll
+  for (int g = 0; g < 16; ++g) top = max(top, lds[g * 16 + col]);
+  const int ex = half_exponent(top);
+  if (grp == 0) a.wexp[h] = ex;
+  uint16_t* const out = a.wt + (int64_t)h * E + grp * N;
+#pragma unroll
+  for (int i = 0; i < N; i += 4) {
+    u32x2 hi, lo;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      uint32_t x, y;
+      half_pieces(v[i + 2 * j], v[i + 2 * j + 1], ex, x, y);
+      hi[j] = x;
+      lo[j] = y;
+    }
+    *(u32x2*)(out + i) = hi;
+    *(u32x2*)(out + (int64_t)a.H * E + i) = lo;
+  }
+}
+
 // ---- the gradient of the logits ------------------------------------------------------------------
 //   through the mixing weights, w_k = c s_k / sum_j s_j (or c s_k):
 //     dl_k = (g_k - sum_j g_j q_j) q_k (1 - s_k),  g = c dw, q = s / sum s      (or g_k s_k (1 - s_k))
@@ -147,6 +231,10 @@ __global__ __launch_bounds__(256) void dlogits_kernel(DlogitsArgs a) {
   constexpr int E = EPL * 64;
   __shared__ __align__(16) float rows[4][E];
   __shared__ int first, tokens;
+  if ((int)blockIdx.x >= a.token_blocks) {
+    split_weight<EPL>(a, (int)blockIdx.x - a.token_blocks, (uint32_t*)&rows[0][0]);
+    return;
+  }
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t base = (int64_t)blockIdx.x * 4 * a.run;
   int b = 0;
@@ -230,7 +318,31 @@ __global__ __launch_bounds__(256) void dlogits_kernel(DlogitsArgs a) {
 #pragma unroll
       for (int i = 0; i < EPL; ++i) d[i] += add[i];
     }
-    Row<EPL>::store(a.dlogits + t * E, lane, d);
+    if (a.dlogits) Row<EPL>::store(a.dlogits + t * E, lane, d);
+    const int64_t plane = (int64_t)a.seq.T * E;
+    if (a.bf) {
+      Pieces<EPL, 3> p;
+#pragma unroll
+      for (int i = 0; i < EPL; i += 2) {
+        uint32_t x[3], y[3];
+        bf16_pieces(d[i], x);
+        bf16_pieces(i + 1 < EPL ? d[i + 1] : 0.f, y);
+#pragma unroll
+        for (int k = 0; k < 3; ++k) p.w[k][i / 2] = x[k] >> 16 | y[k];
+      }
+      p.store(a.bf + t * E, plane, lane);
+    }
+    if (a.hf) {
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) top = max(top, __float_as_uint(d[i]) & 0x7FFFFFFFu);
+      const int ex = half_exponent(wave_max_u32(top));
+      Pieces<EPL, 2> p;
+#pragma unroll
+      for (int i = 0; i < EPL; i += 2) half_pieces(d[i], i + 1 < EPL ? d[i + 1] : 0.f, ex, p.w[0][i / 2], p.w[1][i / 2]);
+      p.store(a.hf + t * E, plane, lane);
+      if (lane == 0) a.hexp[t] = ex;
+    }
   }
 }
 
@@ -266,7 +378,8 @@ hipError_t launch_balance(const BalanceArgs& a, hipStream_t s) {
 hipError_t launch_dlogits(DlogitsArgs a, hipStream_t s) {
   if (a.seq.T == 0) return hipSuccess;
   a.run = (int)std::min<int64_t>(std::max<int64_t>(a.seq.T / 4096, 1), 8);
-  const unsigned grid = (unsigned)(((int64_t)a.seq.T + 4 * a.run - 1) / (4 * a.run));
+  a.token_blocks = (int)(((int64_t)a.seq.T + 4 * a.run - 1) / (4 * a.run));
+  const unsigned grid = (unsigned)(a.token_blocks + (a.hf ? a.H / 16 : 0));
 #define MOE_DL(N) hipLaunchKernelGGL(dlogits_kernel<N>, dim3(grid), dim3(256), 0, s, a)
   MOE_EPL(a.E, MOE_DL)
 #undef MOE_DL

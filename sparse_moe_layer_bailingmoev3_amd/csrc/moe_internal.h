@@ -288,19 +288,36 @@ struct DlogitsArgs {
   const float* dtopk_w;    // or NULL
   const int32_t* counts;   // [n, E] or NULL: no balance loss
   float coef; const float* dloss;
-  float* dlogits;
-  int run;                 // tokens of a wave (set by the launch)
+  float* dlogits;          // fp32, or NULL
+  // the pieces that the products read (each NULL if not wanted), planes one behind the other
+  uint16_t* bf;            // bf16 [3, T, E]
+  uint16_t* hf;            // fp16 [2, T, E], row t times 2^hexp[t]
+  int32_t* hexp;           // [T]
+  const float* w; int H;   // router_w [E, H], taken apart by the same launch (hf given)
+  uint16_t* wt;            // fp16 [2, H, E], row h times 2^wexp[h]
+  int32_t* wexp;           // [H]
+  int run, token_blocks;   // tokens of a wave, workgroups of the tokens (set by the launch)
 };
 hipError_t launch_dlogits(DlogitsArgs a, hipStream_t s);
 
+constexpr int ROUTER_TILE_MAX = 256;  // largest tile of the products: the exponents' arrays reach to its end
+struct RouterGradPlan {
+  int dw_tile, dx_tile;      // square tiles
+  int nsplit, split_steps;   // d router_w: parts of the reduction over tokens, steps of 32 in each
+};
+RouterGradPlan router_grad_plan(int64_t T, int E, int H);
 struct RouterGradArgs {
   int T, E, H;
-  const float* dl;         // [T, E]
-  const uint16_t* x; const float* w;
-  float* dw; int acc_w;    // or NULL
-  void* dx; int dx_f32, acc_x;
+  const uint16_t* dl;        // bf16 [3, T, E]
+  const uint16_t* x;         // bf16 [T, H]
+  float* dw; int acc_w;      // or NULL
+  float* part;               // [nsplit, E, H], with nsplit > 1
+  int nsplit, split_steps;   // set by the launch
+  const uint16_t* dh; const int32_t* dexp;  // fp16 [2, T, E]
+  const uint16_t* wt; const int32_t* wexp;  // fp16 [2, H, E]
+  void* dx; int dx_f32, acc_x;  // or NULL
 };
-hipError_t launch_router_grad(const RouterGradArgs& a, hipStream_t s);
+hipError_t launch_router_grad(RouterGradArgs a, hipStream_t s);
 // out[t,e] = the partial logits added in split order
 hipError_t launch_sum_logits(const float* partial, int nsplit, int64_t n, float* out, hipStream_t s);
 

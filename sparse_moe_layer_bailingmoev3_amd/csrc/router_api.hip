@@ -13,6 +13,7 @@
 namespace {
 
 constexpr int32_t MAX_SEQ = 65536;
+constexpr int32_t MAX_HIDDEN = 65536;  // of the products: 32 rows of a tile within 32-bit offsets, tiles counted in 32 bits
 
 size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 
@@ -34,8 +35,8 @@ moe_status_t check_sequences(int64_t T, const moe_sequences_t* q, moe::SeqArgs* 
 }
 
 struct Layout {
-  size_t done, part, psum, pcnt, balance;  // balance loss
-  size_t dlogits, backward;                // backward pass
+  size_t done, parts, psum, pcnt, balance;  // balance loss
+  size_t bf, hf, wt, hexp, wexp, part, backward;  // backward pass
 };
 Layout layout(const moe_config_t* c, int64_t T, int n_seq) {
   const size_t E = c->num_experts;
@@ -48,12 +49,19 @@ Layout layout(const moe_config_t* c, int64_t T, int n_seq) {
     return o;
   };
   L.done = take(4);
-  L.part = take((size_t)n_seq * (E / 64) * 8);
+  L.parts = take((size_t)n_seq * (E / 64) * 8);
   L.psum = take(slots * E * 4);
   L.pcnt = take(slots * E * 4);
   L.balance = off;
   off = 0;
-  L.dlogits = take((size_t)T * E * 4);
+  const size_t H = c->hidden_size, end = moe::ROUTER_TILE_MAX;
+  const moe::RouterGradPlan p = moe::router_grad_plan(T, (int)E, (int)H);
+  L.bf = take((size_t)T * E * 6);
+  L.hf = take((size_t)T * E * 4);
+  L.wt = take(H * E * 4);
+  L.hexp = take((T + end) * 4);
+  L.wexp = take((H + end) * 4);
+  L.part = take(p.nsplit > 1 ? p.nsplit * E * H * 4 : 0);
   L.backward = off;
   return L;
 }
@@ -142,7 +150,7 @@ moe_status_t moe_balance_loss(const moe_config_t* cfg, int64_t T, const moe_sequ
   a.topk_idx = topk_idx;
   a.chunk = moe::balance_chunk(T);
   a.done = (int*)(w + L.done);
-  a.part = (double*)(w + L.part);
+  a.part = (double*)(w + L.parts);
   a.psum = (float*)(w + L.psum);
   a.pcnt = (int32_t*)(w + L.pcnt);
   a.counts = counts;
@@ -160,6 +168,8 @@ moe_status_t moe_router_backward(const moe_config_t* cfg, int64_t T, const moe_s
   MOE_TRY(check_sequences(T, sequences, &d.seq));
   if (!g->dtopk_w && !g->counts) return fail(MOE_ERR_INVALID_ARG, "dtopk_w or counts must be given");
   if (!g->dlogits && !g->drouter_w && !g->dx) return fail(MOE_ERR_INVALID_ARG, "dlogits, drouter_w or dx must be given");
+  if ((g->drouter_w || g->dx) && cfg->hidden_size > MAX_HIDDEN)
+    return fail(MOE_ERR_UNSUPPORTED, "hidden_size %d is above %d", cfg->hidden_size, MAX_HIDDEN);
   if (!std::isfinite(g->balance_coef)) return fail(MOE_ERR_INVALID_ARG, "balance_coef is not finite");
   if (g->dx && g->dx_dtype != MOE_DTYPE_BF16 && g->dx_dtype != MOE_DTYPE_FP32)
     return fail(MOE_ERR_INVALID_ARG, "dx: dtype %d is unknown", g->dx_dtype);
@@ -206,16 +216,29 @@ moe_status_t moe_router_backward(const moe_config_t* cfg, int64_t T, const moe_s
   d.counts = g->counts;
   d.coef = g->balance_coef;
   d.dloss = g->dloss;
-  d.dlogits = g->dlogits ? g->dlogits : (float*)(w + L.dlogits);
+  d.dlogits = g->dlogits;
+  if (g->drouter_w) d.bf = (uint16_t*)(w + L.bf);
+  if (g->dx) {
+    d.hf = (uint16_t*)(w + L.hf);
+    d.hexp = (int32_t*)(w + L.hexp);
+    d.w = g->router_w;
+    d.H = (int)H;
+    d.wt = (uint16_t*)(w + L.wt);
+    d.wexp = (int32_t*)(w + L.wexp);
+  }
   MOE_TRY(done(moe::launch_dlogits(d, (hipStream_t)stream), "router backward launch"));
   if (!products) return MOE_OK;
   moe::RouterGradArgs a{};
   a.T = (int)T;
   a.E = (int)E;
   a.H = (int)H;
-  a.dl = d.dlogits;
+  a.dl = d.bf;
   a.x = (const uint16_t*)g->x;
-  a.w = g->router_w;
+  a.part = (float*)(w + L.part);
+  a.dh = d.hf;
+  a.dexp = d.hexp;
+  a.wt = d.wt;
+  a.wexp = d.wexp;
   a.dw = g->drouter_w;
   a.acc_w = g->accumulate_w != 0;
   a.dx = g->dx;

@@ -2,62 +2,281 @@
 //
 //   d router_w[e,h] = sum_t dl[t,e] x[t,h]        dx[t,h] = sum_e dl[t,e] router_w[e,h]
 //
-// A 64 x 64 tile a workgroup, 4 x 4 values a thread, fp32.
+// dl and router_w are fp32, the matrix units take 16 bits.  Each fp32 value is taken apart into 16-bit
+// pieces, and products are formed piece by piece with fp32 accumulation:
+//   * d router_w: dl in three bf16 pieces (exactly: 8 bits each), x is bf16 itself.  Three products.
+//     (Two rounded pieces lose 2.4e-6 in the norm, twice what a product in fp32 throughout loses.)
+//   * dx: both operands in fp16 pieces (22 bits and more), each row of dl and each column of router_w
+//     scaled by a power of two that brings its largest value to 2^14..2^15, so that fp16's range
+//     covers 2^-38 of the largest; the result is scaled back.  hi hi + hi lo + lo hi: what is left out is 2^-22
+//     of the magnitudes.  Three products, against six with three bf16 pieces each.
+// The pieces are written by the kernel that computes dl (balance.hip), router_w's transposed.
+//
+// One tile engine: BR rows by BC columns of the result, reduction steps of 32 values, both operands'
+// planes brought into a ring of NST LDS stages by direct loads.  dx's planes run along the reduction
+// and are read as they lie; d router_w's run across it and are read through the transposing LDS load.
+// Rows past the end are offsets past a buffer descriptor's end: zeros.
 #include "moe_common.h"
 #include "moe_internal.h"
+#include "tile_ops.h"
 
 namespace moe {
 
 namespace {
 
-template <bool DW, bool F32>
-__global__ __launch_bounds__(256) void router_product_kernel(RouterGradArgs a) {
-  constexpr int KS = 16;
-  __shared__ float A[KS][68], B[KS][68];
-  const int tr = threadIdx.x / 16, tc = threadIdx.x % 16;
-  const int64_t r0 = (int64_t)blockIdx.y * 64;
-  const int c0 = blockIdx.x * 64;
-  const int64_t rows = DW ? a.E : a.T, red = DW ? a.T : a.E;
-  float acc[4][4] = {};
-  for (int64_t k0 = 0; k0 < red; k0 += KS) {
-    for (int i = threadIdx.x; i < KS * 64; i += 256) {
-      if constexpr (DW) {
-        const int k = i / 64, c = i % 64;
-        const int64_t t = k0 + k;
-        A[k][c] = t < red && r0 + c < rows ? a.dl[t * a.E + r0 + c] : 0.f;
-        B[k][c] = t < red ? bf16_bits_to_f32(a.x[t * a.H + c0 + c]) : 0.f;
+constexpr int OP_DW = 0, OP_DX = 1;
+
+template <int OP, int BR, int BC, int WR, int WC, int NST, bool F32>
+__global__ __launch_bounds__(WR* WC * 64, 2) void router_tile_kernel(RouterGradArgs a) {
+  constexpr int NW = WR * WC, PX = OP == OP_DX ? 2 : 3, PY = OP == OP_DX ? 2 : 1, KS = 32;
+  constexpr int X_BYTES = BR * KS * 2, Y_BYTES = BC * KS * 2, ST_BYTES = PX * X_BYTES + PY * Y_BYTES;
+  constexpr int XN = X_BYTES / (NW * 1024), YN = Y_BYTES / (NW * 1024), LN = PX * XN + PY * YN;  // loads per wave
+  static_assert(XN * NW * 1024 == X_BYTES && YN * NW * 1024 == Y_BYTES, "a plane must split evenly over the waves");
+  constexpr int RJ = BR / WR / 16, CJ = BC / WC / 16;
+  __shared__ __align__(16) uint8_t lds[NST * ST_BYTES];
+
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r16 = lane & 15, q = lane >> 4;
+  const int wr = wave / WC, wc = wave % WC;
+
+  // ---- which tile: consecutive ones (the column tiles of a row tile, the tiles of a split) on one XCD
+  const int nct = (a.H + BC - 1) / BC;
+  const int nrt = ((OP == OP_DW ? a.E : a.T) + BR - 1) / BR;
+  const int tiles = nct * nrt, total = OP == OP_DW ? tiles * a.nsplit : tiles;
+  const int per = (total + 7) >> 3;
+  const int item = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+  if ((int)(blockIdx.x >> 3) >= per || item >= total) return;
+  const int split = item / tiles, tile = item - split * tiles;
+  const int rt = tile / nct, r0 = rt * BR, c0 = (tile - rt * nct) * BC;
+  const int red0 = OP == OP_DW ? split * a.split_steps * KS : 0;
+  const int red = OP == OP_DW ? max(min(a.T - red0, a.split_steps * KS), 0) : a.E;
+  const int nsteps = (red + KS - 1) / KS;
+
+  // ---- loads
+  uint64_t xb[PX], yb[PY];
+  uint32_t xo[XN], yo[YN], xstep, ystep;
+  int xrow[XN], yrow[YN];  // reduction row of the loads (d router_w: masked in the last step)
+  if constexpr (OP == OP_DX) {
+    xb[0] = (uint64_t)(a.dh + (int64_t)r0 * a.E);
+    xb[1] = xb[0] + (uint64_t)a.T * a.E * 2;
+    yb[0] = (uint64_t)(a.wt + (int64_t)c0 * a.E);
+    yb[1] = yb[0] + (uint64_t)a.H * a.E * 2;
+    xstep = ystep = KS * 2;
+    auto offset = [&](int load, int rows) {
+      const int row = load * 16 + lane / 4;
+      return row < rows ? (uint32_t)(row * a.E * 2 + (((lane & 3) ^ ((row >> 2) & 3)) << 4)) : BUF_OUT;
+    };
+    each<XN>([&](auto i) { xo[i] = offset(wave * XN + i, a.T - r0); });
+    each<YN>([&](auto i) { yo[i] = offset(wave * YN + i, a.H - c0); });
+  } else {
+    constexpr int XL = BR / 8, YL = BC / 8;
+    each<PX>([&](auto p) { xb[p] = (uint64_t)(a.dl + ((int64_t)p * a.T + red0) * a.E + r0); });
+    yb[0] = (uint64_t)(a.x + (int64_t)red0 * a.H + c0);
+    xstep = KS * a.E * 2;
+    ystep = KS * a.H * 2;
+    each<XN>([&](auto i) {
+      const int row = xrow[i] = (wave * XN + i) * (64 / XL) + lane / XL, ch = (lane % XL) ^ swz_tr<BR>(row);
+      xo[i] = r0 + ch * 8 < a.E ? (uint32_t)(row * a.E * 2 + ch * 16) : BUF_OUT;
+    });
+    each<YN>([&](auto i) {
+      const int row = yrow[i] = (wave * YN + i) * (64 / YL) + lane / YL, ch = (lane % YL) ^ swz_tr<BC>(row);
+      yo[i] = c0 + ch * 8 < a.H ? (uint32_t)(row * a.H * 2 + ch * 16) : BUF_OUT;
+    });
+  }
+  const uint32_t lds0 = lds_offset(lds);
+  int left = red;  // reduction values from the next step to load on
+  uint32_t lst = lds0;
+  auto issue = [&]() {
+    const uint32_t st = __builtin_amdgcn_readfirstlane(lst);
+    const bool whole = OP == OP_DX || left >= KS;
+    each<PX>([&](auto p) {
+      const u32x4 rs = buffer_at(xb[p]);
+      each<XN>([&](auto i) {
+        dma16(whole || xrow[i] < left ? xo[i] : BUF_OUT, rs, st + p * X_BYTES + (wave * XN + i) * 1024);
+      });
+      xb[p] += xstep;
+    });
+    each<PY>([&](auto p) {
+      const u32x4 rs = buffer_at(yb[p]);
+      each<YN>([&](auto i) {
+        dma16(whole || yrow[i] < left ? yo[i] : BUF_OUT, rs, st + PX * X_BYTES + p * Y_BYTES + (wave * YN + i) * 1024);
+      });
+      yb[p] += ystep;
+    });
+    left -= KS;
+    lst = lst == lds0 + (NST - 1) * ST_BYTES ? lds0 : lst + ST_BYTES;
+  };
+
+  // ---- LDS read addresses
+  int xa[OP == OP_DW ? RJ : 1], ya[OP == OP_DW ? CJ : 1];
+  if constexpr (OP == OP_DW) {
+    const int row = 8 * q + (r16 >> 2);
+#pragma unroll
+    for (int j = 0; j < RJ; ++j) xa[j] = row * BR * 2 + ((((wr * RJ + j) * 2) ^ swz_tr<BR>(row)) << 4) + (r16 & 3) * 8;
+#pragma unroll
+    for (int j = 0; j < CJ; ++j)
+      ya[j] = PX * X_BYTES + row * BC * 2 + ((((wc * CJ + j) * 2) ^ swz_tr<BC>(row)) << 4) + (r16 & 3) * 8;
+  } else {
+    xa[0] = (wr * RJ * 16 + r16) * 64 + ((q ^ ((r16 >> 2) & 3)) << 4);
+    ya[0] = PX * X_BYTES + (wc * CJ * 16 + r16) * 64 + ((q ^ ((r16 >> 2) & 3)) << 4);
+  }
+  auto frag = [&](const uint8_t* st, const int* at, int j, int row_bytes) {
+    if constexpr (OP == OP_DW) {
+      const u32x2 lo = lds_read_tr(st + at[j]), hi = lds_read_tr(st + at[j] + 4 * row_bytes);
+      return u32x4{lo[0], lo[1], hi[0], hi[1]};
+    } else {
+      return *(const u32x4*)(st + at[0] + j * 16 * 64);
+    }
+  };
+
+  floatx4 acc[CJ][RJ];
+#pragma unroll
+  for (int c = 0; c < CJ; ++c)
+#pragma unroll
+    for (int r = 0; r < RJ; ++r) acc[c][r] = floatx4{0.f, 0.f, 0.f, 0.f};
+
+  auto compute = [&](const uint8_t* st) {
+    u32x4 yf[PY][CJ];
+#pragma unroll
+    for (int p = 0; p < PY; ++p)
+#pragma unroll
+      for (int c = 0; c < CJ; ++c) yf[p][c] = frag(st + p * Y_BYTES, ya, c, BC * 2);
+#pragma unroll
+    for (int r = 0; r < RJ; ++r) {
+      const u32x4 hi = frag(st, xa, r, BR * 2), lo = frag(st + (PX - 1) * X_BYTES, xa, r, BR * 2);
+      if constexpr (OP == OP_DW) {
+        const u32x4 mid = frag(st + X_BYTES, xa, r, BR * 2);
+#pragma unroll
+        for (int c = 0; c < CJ; ++c) acc[c][r] = mfma16(yf[0][c], lo, acc[c][r]);
+#pragma unroll
+        for (int c = 0; c < CJ; ++c) acc[c][r] = mfma16(yf[0][c], mid, acc[c][r]);
+#pragma unroll
+        for (int c = 0; c < CJ; ++c) acc[c][r] = mfma16(yf[0][c], hi, acc[c][r]);
       } else {
-        const int64_t t = r0 + i / KS;
-        A[i % KS][i / KS] = t < rows ? a.dl[t * a.E + k0 + i % KS] : 0.f;
-        B[i / 64][i % 64] = a.w[(k0 + i / 64) * a.H + c0 + i % 64];
+#pragma unroll
+        for (int c = 0; c < CJ; ++c) acc[c][r] = mfma16_f16(yf[0][c], hi, acc[c][r]);
+#pragma unroll
+        for (int c = 0; c < CJ; ++c) acc[c][r] = mfma16_f16(yf[0][c], lo, acc[c][r]);
+#pragma unroll
+        for (int c = 0; c < CJ; ++c) acc[c][r] = mfma16_f16(yf[PY - 1][c], hi, acc[c][r]);
       }
     }
-    __syncthreads();
-    for (int k = 0; k < KS; ++k)
-      for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) acc[i][j] = __builtin_fmaf(A[k][tr * 4 + i], B[k][tc * 4 + j], acc[i][j]);
-    __syncthreads();
+  };
+
+  // ---- steps: wait for this stage's loads (those of later stages stay in flight), meet the other
+  // waves, refill the stage that all have left, multiply
+#pragma unroll
+  for (int j = 0; j < NST - 1; ++j)
+    if (j < nsteps) issue();
+  int stage = 0;
+  for (int s = 0; s < nsteps; ++s) {
+    if (nsteps - 1 - s >= NST - 2) wait_vmcnt<(NST - 2) * LN>();
+    else wait_vmcnt<0>();
+    lds_barrier();
+    if (s + NST - 1 < nsteps) issue();
+    compute(lds + stage);
+    stage = stage == (NST - 1) * ST_BYTES ? 0 : stage + ST_BYTES;
   }
-  for (int i = 0; i < 4; ++i) {
-    const int64_t r = r0 + tr * 4 + i;
-    if (r >= rows) continue;
-    for (int j = 0; j < 4; ++j) {
-      const int64_t at = r * a.H + c0 + tc * 4 + j;
-      if constexpr (DW) a.dw[at] = a.acc_w ? a.dw[at] + acc[i][j] : acc[i][j];
-      else if constexpr (F32) ((float*)a.dx)[at] = a.acc_x ? ((float*)a.dx)[at] + acc[i][j] : acc[i][j];
-      else ((uint16_t*)a.dx)[at] = (uint16_t)f32x2_to_bf16x2(acc[i][j], 0.f);
+
+  // ---- result: lane (r16, q) holds columns 16c + 4q .. +3 of row r16 of the fragments; four fragments
+  // turned within quads of lanes make 16 lanes hold one row's 64 columns (whole cache lines)
+  static_assert(CJ % 4 == 0 || CJ == 2, "column fragments");
+  constexpr bool TURN = CJ % 4 == 0;
+  const int rows = OP == OP_DW ? a.E : a.T;
+  float* const o32 = OP == OP_DX ? (float*)a.dx : a.nsplit > 1 ? a.part + (int64_t)split * a.E * a.H : a.dw;
+  const bool add = OP == OP_DX ? a.acc_x : a.acc_w && a.nsplit == 1;
+#pragma unroll
+  for (int cb = 0; cb < (TURN ? CJ / 4 : 1); ++cb) {
+    constexpr int CN = TURN ? 4 : CJ;
+    const int row0 = r0 + wr * RJ * 16 + (TURN ? r16 & 12 : r16);
+    const int col0 = c0 + (wc * CJ + cb * 4) * 16 + 4 * q + (TURN ? (r16 & 3) * 16 : 0);
+#pragma unroll
+    for (int r = 0; r < RJ; ++r) {
+      floatx4 v[CN];
+#pragma unroll
+      for (int j = 0; j < CN; ++j) v[j] = acc[cb * 4 + j][r];
+      if constexpr (TURN) quad_transpose(v);
+      floatx4 old[CN];
+#pragma unroll
+      for (int j = 0; j < CN; ++j) {
+        const int row = row0 + r * 16 + (TURN ? j : 0), col = col0 + (TURN ? 0 : j * 16);
+        const bool ok = row < rows && col < a.H;
+        if (F32 && add) old[j] = *(const floatx4*)(o32 + (ok ? (int64_t)row * a.H + col : 0));
+        if constexpr (OP == OP_DX) {  // (the exponents' arrays reach to the end of the last tile)
+          const int er = a.dexp[row];
+          const int4 ec = *(const int4*)(a.wexp + col);
+          v[j] = floatx4{__builtin_amdgcn_ldexpf(v[j][0], -(er + ec.x)), __builtin_amdgcn_ldexpf(v[j][1], -(er + ec.y)),
+                         __builtin_amdgcn_ldexpf(v[j][2], -(er + ec.z)), __builtin_amdgcn_ldexpf(v[j][3], -(er + ec.w))};
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < CN; ++j) {
+        const int row = row0 + r * 16 + (TURN ? j : 0), col = col0 + (TURN ? 0 : j * 16);
+        if (row >= rows || col >= a.H) continue;
+        const int64_t at = (int64_t)row * a.H + col;
+        if (F32 && add) v[j] += old[j];
+        if constexpr (F32) *(floatx4*)(o32 + at) = v[j];
+        else *(u32x2*)((uint16_t*)a.dx + at) = u32x2{f32x2_to_bf16x2(v[j][0], v[j][1]), f32x2_to_bf16x2(v[j][2], v[j][3])};
+      }
     }
   }
 }
 
+// d router_w = (d router_w +) the splits' parts in order
+__global__ __launch_bounds__(256) void router_join_kernel(RouterGradArgs a) {
+  const int64_t n = (int64_t)a.E * a.H, i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= n) return;
+  floatx4 v{0.f, 0.f, 0.f, 0.f};
+  if (a.acc_w) v = *(const floatx4*)(a.dw + i);
+  floatx4 s{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+  for (int p = 0; p < a.nsplit; ++p) s += *(const floatx4*)(a.part + p * n + i);
+  *(floatx4*)(a.dw + i) = v + s;
+}
+
+template <int OP, int BR, int BC, int WR, int WC, int NST, bool F32>
+void run_tiles(const RouterGradArgs& a, hipStream_t s) {
+  const int nct = (a.H + BC - 1) / BC, nrt = ((OP == OP_DW ? a.E : a.T) + BR - 1) / BR;
+  const int64_t total = (int64_t)nct * nrt * (OP == OP_DW ? a.nsplit : 1);
+  hipLaunchKernelGGL((router_tile_kernel<OP, BR, BC, WR, WC, NST, F32>), dim3((unsigned)((total + 7) / 8 * 8)), dim3(WR * WC * 64), 0, s, a);
+}
+
 }  // namespace
 
-hipError_t launch_router_grad(const RouterGradArgs& a, hipStream_t s) {
-  if (a.dw) hipLaunchKernelGGL((router_product_kernel<true, true>), dim3(a.H / 64, a.E / 64), dim3(256), 0, s, a);
+RouterGradPlan router_grad_plan(int64_t T, int E, int H) {
+  RouterGradPlan p{};
+  const int64_t steps = std::max<int64_t>((T + 31) / 32, 1);
+  p.dw_tile = T >= 4096 ? 256 : 64;
+  p.dx_tile = T >= 4096 ? 256 : 64;
+  const int64_t tiles = (int64_t)((E + p.dw_tile - 1) / p.dw_tile) * ((H + p.dw_tile - 1) / p.dw_tile);
+  int64_t split = std::max<int64_t>(std::min<int64_t>(256 / tiles, steps / 4), 1);
+  if (p.dw_tile == 256) split = std::min<int64_t>(8, steps);
+  p.split_steps = (int)((steps + split - 1) / split);
+  p.nsplit = (int)((steps + p.split_steps - 1) / p.split_steps);
+  return p;
+}
+
+hipError_t launch_router_grad(RouterGradArgs a, hipStream_t s) {
+  const RouterGradPlan p = router_grad_plan(a.T, a.E, a.H);
+  a.nsplit = p.nsplit;
+  a.split_steps = p.split_steps;
+  if (a.dw) {
+    if (p.dw_tile == 256) run_tiles<OP_DW, 256, 256, 2, 4, 2, true>(a, s);
+    else if (p.dw_tile == 128) run_tiles<OP_DW, 128, 128, 2, 2, 2, true>(a, s);
+    else run_tiles<OP_DW, 64, 64, 2, 2, 4, true>(a, s);
+    if (a.nsplit > 1) hipLaunchKernelGGL(router_join_kernel, dim3((unsigned)(((int64_t)a.E * a.H + 1023) / 1024)), dim3(256), 0, s, a);
+  }
   if (a.dx && a.T > 0) {
-    const dim3 grid(a.H / 64, (unsigned)((a.T + 63) / 64));
-    if (a.dx_f32) hipLaunchKernelGGL((router_product_kernel<false, true>), grid, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((router_product_kernel<false, false>), grid, dim3(256), 0, s, a);
+    if (a.dx_f32) {
+      if (p.dx_tile == 256) run_tiles<OP_DX, 256, 256, 2, 4, 2, true>(a, s);
+      else if (p.dx_tile == 128) run_tiles<OP_DX, 128, 128, 2, 2, 2, true>(a, s);
+      else run_tiles<OP_DX, 64, 64, 2, 2, 4, true>(a, s);
+    } else {
+      if (p.dx_tile == 256) run_tiles<OP_DX, 256, 256, 2, 4, 2, false>(a, s);
+      else if (p.dx_tile == 128) run_tiles<OP_DX, 128, 128, 2, 2, 2, false>(a, s);
+      else run_tiles<OP_DX, 64, 64, 2, 2, 4, false>(a, s);
+    }
   }
   return hipGetLastError();
 }
