@@ -171,9 +171,10 @@ __device__ __forceinline__ void bf16_pieces(float v, uint32_t (&p)[3]) {
 template <int EPL, int P>
 struct Pieces {
   uint32_t w[P][(EPL + 1) / 2];
-  __device__ __forceinline__ void store(uint16_t* row, int64_t plane, int lane) const {
+  __device__ __forceinline__ void store(uint16_t* row, int64_t plane, int lane, int planes = P) const {
 #pragma unroll
-    for (int p = 0; p < P; ++p)
+    for (int p = 0; p < P; ++p) {
+      if (p >= planes) break;
 #pragma unroll
       for (int j = 0; j < Row<EPL>::NJ; ++j) {
         uint16_t* const at = row + p * plane + Row<EPL>::at(lane, j);
@@ -181,6 +182,7 @@ struct Pieces {
         else if constexpr (EPL == 2) *(uint32_t*)at = w[p][0];
         else *(u32x2*)at = u32x2{w[p][2 * j], w[p][2 * j + 1]};
       }
+    }
   }
 };
 
@@ -215,7 +217,7 @@ __device__ __forceinline__ void split_weight(const DlogitsArgs& a, int block, ui
       lo[j] = y;
     }
     *(u32x2*)(out + i) = hi;
-    *(u32x2*)(out + (int64_t)a.H * E + i) = lo;
+    if (a.pair) *(u32x2*)(out + (int64_t)a.H * E + i) = lo;
   }
 }
 
@@ -340,7 +342,7 @@ __global__ __launch_bounds__(256) void dlogits_kernel(DlogitsArgs a) {
       Pieces<EPL, 2> p;
 #pragma unroll
       for (int i = 0; i < EPL; i += 2) half_pieces(d[i], i + 1 < EPL ? d[i + 1] : 0.f, ex, p.w[0][i / 2], p.w[1][i / 2]);
-      p.store(a.hf + t * E, plane, lane);
+      p.store(a.hf + t * E, plane, lane, 1 + a.pair);
       if (lane == 0) a.hexp[t] = ex;
     }
   }

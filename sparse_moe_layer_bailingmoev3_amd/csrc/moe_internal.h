@@ -291,21 +291,22 @@ struct DlogitsArgs {
   float* dlogits;          // fp32, or NULL
   // the pieces that the products read (each NULL if not wanted), planes one behind the other
   uint16_t* bf;            // bf16 [3, T, E]
-  uint16_t* hf;            // fp16 [2, T, E], row t times 2^hexp[t]
+  int pair;                // fp16: both pieces (for a result in fp32), or the first alone
+  uint16_t* hf;            // fp16 [1 + pair, T, E], row t times 2^hexp[t]
   int32_t* hexp;           // [T]
   const float* w; int H;   // router_w [E, H], taken apart by the same launch (hf given)
-  uint16_t* wt;            // fp16 [2, H, E], row h times 2^wexp[h]
+  uint16_t* wt;            // fp16 [1 + pair, H, E], row h times 2^wexp[h]
   int32_t* wexp;           // [H]
   int run, token_blocks;   // tokens of a wave, workgroups of the tokens (set by the launch)
 };
 hipError_t launch_dlogits(DlogitsArgs a, hipStream_t s);
 
-constexpr int ROUTER_TILE_MAX = 256;  // largest tile of the products: the exponents' arrays reach to its end
+constexpr int ROUTER_TILE_MAX = 128;  // largest tile of the products: the exponents' arrays reach to its end
 struct RouterGradPlan {
-  int dw_tile, dx_tile;      // square tiles
+  int tile;                  // square tiles
   int nsplit, split_steps;   // d router_w: parts of the reduction over tokens, steps of 32 in each
 };
-RouterGradPlan router_grad_plan(int64_t T, int E, int H);
+RouterGradPlan router_grad_plan(int64_t T, int E, int H, bool dw, bool dx, bool f32);
 struct RouterGradArgs {
   int T, E, H;
   const uint16_t* dl;        // bf16 [3, T, E]
@@ -313,8 +314,8 @@ struct RouterGradArgs {
   float* dw; int acc_w;      // or NULL
   float* part;               // [nsplit, E, H], with nsplit > 1
   int nsplit, split_steps;   // set by the launch
-  const uint16_t* dh; const int32_t* dexp;  // fp16 [2, T, E]
-  const uint16_t* wt; const int32_t* wexp;  // fp16 [2, H, E]
+  const uint16_t* dh; const int32_t* dexp;  // fp16 [1 or 2, T, E]
+  const uint16_t* wt; const int32_t* wexp;  // fp16 [1 or 2, H, E]
   void* dx; int dx_f32, acc_x;  // or NULL
 };
 hipError_t launch_router_grad(RouterGradArgs a, hipStream_t s);

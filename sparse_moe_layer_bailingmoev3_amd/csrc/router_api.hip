@@ -55,13 +55,18 @@ Layout layout(const moe_config_t* c, int64_t T, int n_seq) {
   L.balance = off;
   off = 0;
   const size_t H = c->hidden_size, end = moe::ROUTER_TILE_MAX;
-  const moe::RouterGradPlan p = moe::router_grad_plan(T, (int)E, (int)H);
+  int parts = 0;
+  for (const bool dx : {false, true})
+    for (const bool f32 : {false, true}) {
+      const int n = moe::router_grad_plan(T, (int)E, (int)H, true, dx, f32).nsplit;
+      parts = std::max(parts, n > 1 ? n : 0);
+    }
   L.bf = take((size_t)T * E * 6);
   L.hf = take((size_t)T * E * 4);
   L.wt = take(H * E * 4);
   L.hexp = take((T + end) * 4);
   L.wexp = take((H + end) * 4);
-  L.part = take(p.nsplit > 1 ? p.nsplit * E * H * 4 : 0);
+  L.part = take(parts * E * H * 4);
   L.backward = off;
   return L;
 }
@@ -219,6 +224,7 @@ moe_status_t moe_router_backward(const moe_config_t* cfg, int64_t T, const moe_s
   d.dlogits = g->dlogits;
   if (g->drouter_w) d.bf = (uint16_t*)(w + L.bf);
   if (g->dx) {
+    d.pair = g->dx_dtype == MOE_DTYPE_FP32;
     d.hf = (uint16_t*)(w + L.hf);
     d.hexp = (int32_t*)(w + L.hexp);
     d.w = g->router_w;

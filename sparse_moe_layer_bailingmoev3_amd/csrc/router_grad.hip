@@ -6,11 +6,16 @@
 // pieces, and products are formed piece by piece with fp32 accumulation:
 //   * d router_w: dl in three bf16 pieces (exactly: 8 bits each), x is bf16 itself.  Three products.
 //     (Two rounded pieces lose 2.4e-6 in the norm, twice what a product in fp32 throughout loses.)
-//   * dx: both operands in fp16 pieces (22 bits and more), each row of dl and each column of router_w
-//     scaled by a power of two that brings its largest value to 2^14..2^15, so that fp16's range
-//     covers 2^-38 of the largest; the result is scaled back.  hi hi + hi lo + lo hi: what is left out is 2^-22
-//     of the magnitudes.  Three products, against six with three bf16 pieces each.
+//   * dx: both operands in fp16, each row of dl and each column of router_w scaled by a power of two
+//     that brings its largest value to 2^14..2^15, so that fp16's range covers 2^-38 of the largest; the
+//     result is scaled back.  In fp32: two pieces each (22 bits), hi hi + hi lo + lo hi; what is left out
+//     is 2^-22 of the magnitudes.  Three products, against six with three bf16 pieces each.  In bf16:
+//     the first pieces alone, rounded to 11 bits (2^-11 each at most, 3e-4 in the norm, where the result's own
+//     rounding to 8 bits is 1.7e-3).  One product.
 // The pieces are written by the kernel that computes dl (balance.hip), router_w's transposed.
+//
+// Both products are tiles of one launch, the weight gradient's (longer ones) first: the tokens' tiles,
+// which end in reading and writing dx, then run beside them on the same compute units.
 //
 // One tile engine: BR rows by BC columns of the result, reduction steps of 32 values, both operands'
 // planes brought into a ring of NST LDS stages by direct loads.  dx's planes run along the reduction
@@ -26,14 +31,21 @@ namespace {
 
 constexpr int OP_DW = 0, OP_DX = 1;
 
+// what a tile of BR x BC takes from LDS
+template <int OP, int BR, int BC, bool F32>
+struct Stage {
+  static constexpr int KS = 32, PX = OP == OP_DW ? 3 : F32 ? 2 : 1, PY = OP == OP_DX && F32 ? 2 : 1;  // planes
+  static constexpr int X_BYTES = BR * KS * 2, Y_BYTES = BC * KS * 2, BYTES = PX * X_BYTES + PY * Y_BYTES;
+};
+
 template <int OP, int BR, int BC, int WR, int WC, int NST, bool F32>
-__global__ __launch_bounds__(WR* WC * 64, 2) void router_tile_kernel(RouterGradArgs a) {
-  constexpr int NW = WR * WC, PX = OP == OP_DX ? 2 : 3, PY = OP == OP_DX ? 2 : 1, KS = 32;
-  constexpr int X_BYTES = BR * KS * 2, Y_BYTES = BC * KS * 2, ST_BYTES = PX * X_BYTES + PY * Y_BYTES;
+__device__ __forceinline__ void router_tile(const RouterGradArgs& a, int block, int blocks, uint8_t* lds) {
+  typedef Stage<OP, BR, BC, F32> St;
+  constexpr int NW = WR * WC, KS = St::KS, PX = St::PX, PY = St::PY;
+  constexpr int X_BYTES = St::X_BYTES, Y_BYTES = St::Y_BYTES, ST_BYTES = St::BYTES;
   constexpr int XN = X_BYTES / (NW * 1024), YN = Y_BYTES / (NW * 1024), LN = PX * XN + PY * YN;  // loads per wave
   static_assert(XN * NW * 1024 == X_BYTES && YN * NW * 1024 == Y_BYTES, "a plane must split evenly over the waves");
   constexpr int RJ = BR / WR / 16, CJ = BC / WC / 16;
-  __shared__ __align__(16) uint8_t lds[NST * ST_BYTES];
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -44,9 +56,8 @@ __global__ __launch_bounds__(WR* WC * 64, 2) void router_tile_kernel(RouterGradA
   const int nct = (a.H + BC - 1) / BC;
   const int nrt = ((OP == OP_DW ? a.E : a.T) + BR - 1) / BR;
   const int tiles = nct * nrt, total = OP == OP_DW ? tiles * a.nsplit : tiles;
-  const int per = (total + 7) >> 3;
-  const int item = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
-  if ((int)(blockIdx.x >> 3) >= per || item >= total) return;
+  const int item = (block & 7) * (blocks >> 3) + (block >> 3);  // (blocks: total, rounded up to a multiple of 8)
+  if (item >= total) return;
   const int split = item / tiles, tile = item - split * tiles;
   const int rt = tile / nct, r0 = rt * BR, c0 = (tile - rt * nct) * BC;
   const int red0 = OP == OP_DW ? split * a.split_steps * KS : 0;
@@ -58,10 +69,8 @@ __global__ __launch_bounds__(WR* WC * 64, 2) void router_tile_kernel(RouterGradA
   uint32_t xo[XN], yo[YN], xstep, ystep;
   int xrow[XN], yrow[YN];  // reduction row of the loads (d router_w: masked in the last step)
   if constexpr (OP == OP_DX) {
-    xb[0] = (uint64_t)(a.dh + (int64_t)r0 * a.E);
-    xb[1] = xb[0] + (uint64_t)a.T * a.E * 2;
-    yb[0] = (uint64_t)(a.wt + (int64_t)c0 * a.E);
-    yb[1] = yb[0] + (uint64_t)a.H * a.E * 2;
+    each<PX>([&](auto p) { xb[p] = (uint64_t)(a.dh + ((int64_t)p * a.T + r0) * a.E); });
+    each<PY>([&](auto p) { yb[p] = (uint64_t)(a.wt + ((int64_t)p * a.H + c0) * a.E); });
     xstep = ystep = KS * 2;
     auto offset = [&](int load, int rows) {
       const int row = load * 16 + lane / 4;
@@ -144,23 +153,17 @@ __global__ __launch_bounds__(WR* WC * 64, 2) void router_tile_kernel(RouterGradA
       for (int c = 0; c < CJ; ++c) yf[p][c] = frag(st + p * Y_BYTES, ya, c, BC * 2);
 #pragma unroll
     for (int r = 0; r < RJ; ++r) {
-      const u32x4 hi = frag(st, xa, r, BR * 2), lo = frag(st + (PX - 1) * X_BYTES, xa, r, BR * 2);
-      if constexpr (OP == OP_DW) {
-        const u32x4 mid = frag(st + X_BYTES, xa, r, BR * 2);
+      u32x4 xf[PX];
 #pragma unroll
-        for (int c = 0; c < CJ; ++c) acc[c][r] = mfma16(yf[0][c], lo, acc[c][r]);
+      for (int p = 0; p < PX; ++p) xf[p] = frag(st + p * X_BYTES, xa, r, BR * 2);
+      // small terms first
 #pragma unroll
-        for (int c = 0; c < CJ; ++c) acc[c][r] = mfma16(yf[0][c], mid, acc[c][r]);
+      for (int p = PX + PY - 2; p >= 0; --p)
 #pragma unroll
-        for (int c = 0; c < CJ; ++c) acc[c][r] = mfma16(yf[0][c], hi, acc[c][r]);
-      } else {
-#pragma unroll
-        for (int c = 0; c < CJ; ++c) acc[c][r] = mfma16_f16(yf[0][c], hi, acc[c][r]);
-#pragma unroll
-        for (int c = 0; c < CJ; ++c) acc[c][r] = mfma16_f16(yf[0][c], lo, acc[c][r]);
-#pragma unroll
-        for (int c = 0; c < CJ; ++c) acc[c][r] = mfma16_f16(yf[PY - 1][c], hi, acc[c][r]);
-      }
+        for (int c = 0; c < CJ; ++c) {
+          if constexpr (OP == OP_DW) acc[c][r] = mfma16(yf[0][c], xf[p], acc[c][r]);
+          else acc[c][r] = mfma16_f16(yf[p == 2 ? PY - 1 : 0][c], xf[p == 2 ? 0 : p], acc[c][r]);
+        }
     }
   };
 
@@ -235,49 +238,68 @@ __global__ __launch_bounds__(256) void router_join_kernel(RouterGradArgs a) {
   *(floatx4*)(a.dw + i) = v + s;
 }
 
-template <int OP, int BR, int BC, int WR, int WC, int NST, bool F32>
-void run_tiles(const RouterGradArgs& a, hipStream_t s) {
-  const int nct = (a.H + BC - 1) / BC, nrt = ((OP == OP_DW ? a.E : a.T) + BR - 1) / BR;
-  const int64_t total = (int64_t)nct * nrt * (OP == OP_DW ? a.nsplit : 1);
-  hipLaunchKernelGGL((router_tile_kernel<OP, BR, BC, WR, WC, NST, F32>), dim3((unsigned)((total + 7) / 8 * 8)), dim3(WR * WC * 64), 0, s, a);
+template <int BR, int BC, int WR, int WC, int NST, bool F32>
+__global__ __launch_bounds__(WR* WC * 64, 2) void router_products_kernel(RouterGradArgs a, int dw_blocks) {
+  constexpr int DW = Stage<OP_DW, BR, BC, true>::BYTES, DX = Stage<OP_DX, BR, BC, F32>::BYTES;
+  __shared__ __align__(16) uint8_t lds[NST * (DW > DX ? DW : DX)];
+  const int block = blockIdx.x;
+  if (block < dw_blocks) router_tile<OP_DW, BR, BC, WR, WC, NST, true>(a, block, dw_blocks, lds);
+  else router_tile<OP_DX, BR, BC, WR, WC, NST, F32>(a, block - dw_blocks, (int)gridDim.x - dw_blocks, lds);
+}
+
+template <int B, int WR, int WC, int NST>
+void run_products(const RouterGradArgs& a, hipStream_t s) {
+  auto blocks = [&](int64_t rows, int n) { return (int)(((rows + B - 1) / B * ((a.H + B - 1) / B) * n + 7) / 8 * 8); };
+  const int dw = a.dw ? blocks(a.E, a.nsplit) : 0, dx = a.dx && a.T > 0 ? blocks(a.T, 1) : 0;
+  if (dw + dx == 0) return;
+  if (a.dx_f32)
+    hipLaunchKernelGGL((router_products_kernel<B, B, WR, WC, NST, true>), dim3((unsigned)(dw + dx)), dim3(WR * WC * 64), 0, s, a, dw);
+  else
+    hipLaunchKernelGGL((router_products_kernel<B, B, WR, WC, NST, false>), dim3((unsigned)(dw + dx)), dim3(WR * WC * 64), 0, s, a, dw);
 }
 
 }  // namespace
 
-RouterGradPlan router_grad_plan(int64_t T, int E, int H) {
-  RouterGradPlan p{};
+// Tile size and the parts of the weight gradient's reduction, by price: a step of one product of a tile
+// takes `step` us on a place (`wgs` workgroups a compute unit); the weight gradient's items are started
+// first, the others fill the places that they leave.
+RouterGradPlan router_grad_plan(int64_t T, int E, int H, bool dw, bool dx, bool f32) {
+  struct Shape {
+    int tile, wgs;
+    float step, end;
+  };
+  static const Shape shapes[2] = {{128, 2, .45f, 3.f}, {64, 2, .25f, 2.f}};
   const int64_t steps = std::max<int64_t>((T + 31) / 32, 1);
-  p.dw_tile = T >= 4096 ? 256 : 64;
-  p.dx_tile = T >= 4096 ? 256 : 64;
-  const int64_t tiles = (int64_t)((E + p.dw_tile - 1) / p.dw_tile) * ((H + p.dw_tile - 1) / p.dw_tile);
-  int64_t split = std::max<int64_t>(std::min<int64_t>(256 / tiles, steps / 4), 1);
-  if (p.dw_tile == 256) split = std::min<int64_t>(8, steps);
-  p.split_steps = (int)((steps + split - 1) / split);
-  p.nsplit = (int)((steps + p.split_steps - 1) / p.split_steps);
-  return p;
+  RouterGradPlan best{};
+  double cost = -1;
+  for (const Shape& v : shapes) {
+    const double places = 256.0 * v.wgs;
+    const int64_t ct = (H + v.tile - 1) / v.tile, dwt = dw ? (E + v.tile - 1) / v.tile * ct : 0, dxt = dx ? (T + v.tile - 1) / v.tile * ct : 0;
+    const double dx_len = (E / 32) * (f32 ? 3 : 1) * v.step + v.end;
+    for (int64_t n = 1; n <= (dw ? std::min<int64_t>(steps, 32) : 1); ++n) {
+      const int64_t per = (steps + n - 1) / n;
+      if ((steps + per - 1) / per != n) continue;
+      const double len = per * 3 * v.step + v.end, items = (double)dwt * n;
+      const double first = std::ceil(items / places) * len;
+      const double c = std::max(first, (items * len + dxt * dx_len) / places + (dxt ? .5 * dx_len : 0)) +
+                       (n > 1 ? 3 + n * (double)E * H * 8 / 5e6 : 0);
+      if (cost < 0 || c < cost) {
+        cost = c;
+        best = {v.tile, (int)n, (int)per};
+      }
+    }
+  }
+  return best;
 }
 
 hipError_t launch_router_grad(RouterGradArgs a, hipStream_t s) {
-  const RouterGradPlan p = router_grad_plan(a.T, a.E, a.H);
+  const RouterGradPlan p = router_grad_plan(a.T, a.E, a.H, a.dw, a.dx, a.dx_f32);
   a.nsplit = p.nsplit;
   a.split_steps = p.split_steps;
-  if (a.dw) {
-    if (p.dw_tile == 256) run_tiles<OP_DW, 256, 256, 2, 4, 2, true>(a, s);
-    else if (p.dw_tile == 128) run_tiles<OP_DW, 128, 128, 2, 2, 2, true>(a, s);
-    else run_tiles<OP_DW, 64, 64, 2, 2, 4, true>(a, s);
-    if (a.nsplit > 1) hipLaunchKernelGGL(router_join_kernel, dim3((unsigned)(((int64_t)a.E * a.H + 1023) / 1024)), dim3(256), 0, s, a);
-  }
-  if (a.dx && a.T > 0) {
-    if (a.dx_f32) {
-      if (p.dx_tile == 256) run_tiles<OP_DX, 256, 256, 2, 4, 2, true>(a, s);
-      else if (p.dx_tile == 128) run_tiles<OP_DX, 128, 128, 2, 2, 2, true>(a, s);
-      else run_tiles<OP_DX, 64, 64, 2, 2, 4, true>(a, s);
-    } else {
-      if (p.dx_tile == 256) run_tiles<OP_DX, 256, 256, 2, 4, 2, false>(a, s);
-      else if (p.dx_tile == 128) run_tiles<OP_DX, 128, 128, 2, 2, 2, false>(a, s);
-      else run_tiles<OP_DX, 64, 64, 2, 2, 4, false>(a, s);
-    }
-  }
+  if (p.tile == 128) run_products<128, 2, 2, 2>(a, s);
+  else run_products<64, 2, 2, 4>(a, s);
+  if (a.dw && a.nsplit > 1)
+    hipLaunchKernelGGL(router_join_kernel, dim3((unsigned)(((int64_t)a.E * a.H + 1023) / 1024)), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 

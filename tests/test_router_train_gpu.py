@@ -129,21 +129,23 @@ def check_dlogits(got, want):
 
 
 def check_products(want, tol, x, rw, dw=None, dx=None, dw0=None, dx0=None):
-    """The products' own roundings (the operands' pieces 2^-17 each and their product, sums in fp32) and
-    the logits' gradient's."""
+    """The products' own roundings (drouter_w: none, three exact pieces; dx: operands in two fp16 pieces,
+    2^-22 each, and what is left out as much again, or, for a result in bf16, in one, 2^-11 each at half a
+    step; sums in fp32) and the logits' gradient's."""
     xn, wn = np.abs(f64(x)), np.abs(f64(rw))
     d = np.abs(want.dlogits)
     T, E = d.shape
     if dw is not None:
         old = 0 if dw0 is None else f64(dw0)
         ref = want.dlogits.T @ f64(x) + old
-        lim = tol.T @ xn + (2.0 ** -17 + 2 * T * U32) * (d.T @ xn) + U32 * (np.abs(ref) + np.abs(old)) + 1e-37
+        lim = tol.T @ xn + 2 * 3 * T * U32 * (d.T @ xn) + U32 * (np.abs(ref) + np.abs(old)) + 1e-37
         err = np.abs(f64(dw) - ref)
         assert np.all(err <= lim), f"drouter_w: err/tol {np.max(err / lim):.2f}"
     if dx is not None:
         old = 0 if dx0 is None else f64(dx0)
         ref = want.dlogits @ f64(rw) + old
-        lim = tol @ wn + (2.0 ** -17 + 2 * E * U32) * (d @ wn) + (HALF_BF16 if dx.dtype is BF else U32) * np.abs(ref) + U32 * np.abs(old) + 1e-37
+        piece = 2.01 * 2.0 ** -11 if dx.dtype is BF else 3 * 2.0 ** -22
+        lim = tol @ wn + (piece + 2 * 3 * E * U32) * (d @ wn) + (HALF_BF16 if dx.dtype is BF else U32) * np.abs(ref) + U32 * np.abs(old) + 1e-37
         err = np.abs(f64(dx) - ref)
         assert np.all(err <= lim), f"dx: err/tol {np.max(err / lim):.2f}"
 
