@@ -701,6 +701,8 @@ def moe_adamw_dequantise(codes, scales, out, signed, stream=None):
 def _exact(t, name, dtype, shape, dev):
     """Address of a contiguous tensor of that type and shape."""
     try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
         wrong = t.dtype is not dtype or t.dim() != len(shape) or t.get_device() != dev
     except AttributeError:  # no tensor
         wrong = True
@@ -708,9 +710,7 @@ def _exact(t, name, dtype, shape, dev):
         _explain(t, name, dtype, len(shape), dev)
     if t.shape != shape:
         _refuse(f"{name} is {tuple(t.shape)}, {tuple(shape)} needed")
-    if not t.is_contiguous():
-        _refuse(f"{name} must be contiguous")
-    return t.data_ptr() or None
+    _refuse(f"{name} must be contiguous")
 
 
 def _workspace(ws, dev):
@@ -785,17 +785,22 @@ def moe_router_backward(cfg, T, logits, topk_idx, dtopk_w=None, counts=None, coe
     seqs, B = _sequences(seq_offsets, seq_lens, dev)
     if drouter_w is not None and x is None or dx is not None and router_w is None:
         _refuse("drouter_w needs x, and dx needs router_w")
-    opt = lambda t, name, dtype, shape: None if t is None else _exact(t, name, dtype, shape, dev)  # noqa: E731
     p, n = _workspace(ws, dev)
-    dx_at, dx_type = None, 0
+    dx_at, dx_type, I = None, 0, torch.int32
     if dx is not None:
         dx_type = _dtype_code(dx, "dx") if isinstance(dx, torch.Tensor) else 0
         dx_at = _exact(dx, "dx", F if dx_type else torch.bfloat16, (T, H), dev)
-    g = _RouterBackward(_exact(logits, "logits", F, (T, E), dev), opt(topk_idx, "topk_idx", torch.int32, (T, K)),
-                        opt(dtopk_w, "dtopk_w", F, (T, K)), opt(counts, "counts", torch.int32, (B, E)), coef,
-                        None if dloss is None else _scalar_at(dloss, "dloss", F, dev), opt(x, "x", torch.bfloat16, (T, H)),
-                        opt(router_w, "router_w", F, (E, H)), opt(dlogits, "dlogits", F, (T, E)),
-                        opt(drouter_w, "drouter_w", F, (E, H)), 1 if accumulate_w else 0, dx_at, dx_type, 1 if accumulate_x else 0)
+    g = _RouterBackward(
+        _exact(logits, "logits", F, (T, E), dev),
+        None if topk_idx is None else _exact(topk_idx, "topk_idx", I, (T, K), dev),
+        None if dtopk_w is None else _exact(dtopk_w, "dtopk_w", F, (T, K), dev),
+        None if counts is None else _exact(counts, "counts", I, (B, E), dev), coef,
+        None if dloss is None else _scalar_at(dloss, "dloss", F, dev),
+        None if x is None else _exact(x, "x", torch.bfloat16, (T, H), dev),
+        None if router_w is None else _exact(router_w, "router_w", F, (E, H), dev),
+        None if dlogits is None else _exact(dlogits, "dlogits", F, (T, E), dev),
+        None if drouter_w is None else _exact(drouter_w, "drouter_w", F, (E, H), dev), 1 if accumulate_w else 0,
+        dx_at, dx_type, 1 if accumulate_x else 0)
     _enqueue(load_library().moe_router_backward, dev, stream, cfg, T, seqs, g, p, n)
 
 

@@ -5,11 +5,11 @@
 //   loss = coef sum_b (n_b / N) sum_e f_be P_be  =  coef E / (K N) sum_be c_be P_be
 //
 // Two launches.  The first cuts the tokens into chunks; a workgroup walks the sequences that its
-// chunk touches, its waves taking a token each (a lane EPL experts of it), and leaves one row of
-// sums and counts per (chunk c, sequence b) in slot c + b of the workspace.  (Both grow along the
+// chunk touches, its waves taking four tokens at a time (a lane EPL experts of each), and leaves one
+// row of sums and counts per (chunk c, sequence b) in slot c + b of the workspace.  (Both grow along the
 // walk and one of them at every step, so no two pairs share a slot.)  The second adds a sequence's
-// slots, 64 experts a workgroup, and its last workgroup to finish adds the parts of the loss.
-// Every sum has a fixed order.
+// slots, 64 experts a workgroup, and its last workgroup to finish adds the parts of the loss.  A batch of
+// one chunk is done by one workgroup in one launch.  Every sum has a fixed order.
 //
 // Counts are integers: LDS atomics, whose order does not matter.
 #include "router_scores.h"
@@ -17,6 +17,45 @@
 namespace moe {
 
 namespace {
+
+// sums over the tokens [lo, hi) of one sequence and their counts, left in sums[0] and hist
+template <int EPL, int WAVES>
+__device__ __forceinline__ void balance_run(const BalanceArgs& a, int lo, int hi, float (*sums)[EPL * 64], int* hist) {
+  constexpr int E = EPL * 64, AHEAD = EPL > 8 ? 2 : 4;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  float acc[EPL] = {};
+  for (int t = lo + wave * AHEAD; t < hi; t += WAVES * AHEAD) {
+    float l[AHEAD][EPL];
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) Row<EPL>::load(a.logits + (int64_t)min(t + k, hi - 1) * E, lane, l[k]);
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      float total = 0.f;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        l[k][i] = score_of(l[k][i]).s;
+        total += l[k][i];
+      }
+      total = wave_sum(total);
+      const float inv = total == 0.f || t + k >= hi ? 0.f : 1.0f / total;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) acc[i] = t + k < hi ? __builtin_fmaf(l[k][i], inv, acc[i]) : acc[i];
+    }
+  }
+  const int64_t p1 = (int64_t)hi * a.K;
+  for (int64_t p = (int64_t)lo * a.K + threadIdx.x; p < p1; p += WAVES * 64) {
+    const int e = a.topk_idx[p];
+    if ((unsigned)e < (unsigned)E) atomicAdd(&hist[e], 1);
+  }
+  Row<EPL>::store(sums[wave], lane, acc);
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += WAVES * 64) {
+    float v = sums[0][e];
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) v += sums[w][e];
+    sums[0][e] = v;
+  }
+}
 
 constexpr int BAL_WAVES = 8;
 
@@ -26,7 +65,6 @@ __global__ __launch_bounds__(BAL_WAVES * 64) void balance_partial_kernel(Balance
   __shared__ __align__(16) float sums[BAL_WAVES][E];
   __shared__ int hist[E];
   __shared__ int first;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.done = 0;
   const int t0 = blockIdx.x * a.chunk, t1 = (int)min((int64_t)t0 + a.chunk, (int64_t)a.seq.T);
   for (int i = threadIdx.x; i < E; i += BAL_WAVES * 64) hist[i] = 0;
@@ -37,39 +75,53 @@ __global__ __launch_bounds__(BAL_WAVES * 64) void balance_partial_kernel(Balance
     if (q.begin >= t1) break;
     const int lo = max(q.begin, t0), hi = min(q.end, t1);
     if (lo < hi) {
-      float acc[EPL] = {};
-      for (int t = lo + wave; t < hi; t += BAL_WAVES) {
-        float l[EPL], s[EPL], total = 0.f;
-        Row<EPL>::load(a.logits + (int64_t)t * E, lane, l);
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-          s[i] = score_of(l[i]).s;
-          total += s[i];
-        }
-        total = wave_sum(total);
-        const float inv = total == 0.f ? 0.f : 1.0f / total;
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) acc[i] += s[i] * inv;
-      }
-      const int64_t p1 = (int64_t)hi * a.K;
-      for (int64_t p = (int64_t)lo * a.K + threadIdx.x; p < p1; p += BAL_WAVES * 64) {
-        const int e = a.topk_idx[p];
-        if ((unsigned)e < (unsigned)E) atomicAdd(&hist[e], 1);
-      }
-      Row<EPL>::store(sums[wave], lane, acc);
-      __syncthreads();
+      balance_run<EPL, BAL_WAVES>(a, lo, hi, sums, hist);
       const int64_t slot = (int64_t)blockIdx.x + b;
       for (int e = threadIdx.x; e < E; e += BAL_WAVES * 64) {
-        float v = 0.f;
-#pragma unroll
-        for (int w = 0; w < BAL_WAVES; ++w) v += sums[w][e];
-        a.psum[slot * E + e] = v;
+        a.psum[slot * E + e] = sums[0][e];
         a.pcnt[slot * E + e] = hist[e];
         hist[e] = 0;
       }
       __syncthreads();
     }
     if (q.next >= t1) break;
+  }
+}
+
+// one chunk of tokens: all of it
+template <int EPL>
+__global__ __launch_bounds__(1024) void balance_small_kernel(BalanceArgs a) {
+  constexpr int E = EPL * 64, WAVES = 16;
+  __shared__ __align__(16) float sums[WAVES][E];
+  __shared__ int hist[E];
+  __shared__ double parts[WAVES];
+  __shared__ int tokens;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  for (int i = threadIdx.x; i < E; i += 1024) hist[i] = 0;
+  const int N = seq_tokens(a.seq, &tokens);
+  __syncthreads();
+  double part = 0;
+  for (int b = 0; b < a.seq.n; ++b) {
+    const Seq q = seq_at(a.seq, b);
+    const int n = q.end - q.begin;
+    if (n > 0) balance_run<EPL, WAVES>(a, q.begin, q.end, sums, hist);
+    for (int e = threadIdx.x; e < E; e += 1024) {
+      const double mean = n > 0 ? (double)sums[0][e] / n : 0.0;
+      a.probs[(int64_t)b * E + e] = (float)mean;
+      a.counts[(int64_t)b * E + e] = hist[e];
+      part += hist[e] * mean;
+      hist[e] = 0;
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int m = 32; m >= 1; m >>= 1) part += __shfl_xor(part, m, WAVE);
+  if (lane == 0) parts[wave] = part;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    part = 0;
+    for (int w = 0; w < WAVES; ++w) part += parts[w];
+    *a.loss = N > 0 ? (float)((double)a.coef * E * part / ((double)a.K * N)) : 0.f;
   }
 }
 
@@ -85,11 +137,21 @@ __global__ __launch_bounds__(1024) void balance_finish_kernel(BalanceArgs a) {
   int cnt = 0;
   if (q.begin < q.end) {
     const int c1 = (q.end - 1) / a.chunk;
-#pragma unroll 4
-    for (int c = q.begin / a.chunk + wave; c <= c1; c += 16) {
-      const int64_t at = ((int64_t)c + b) * a.E + e;
-      sum += a.psum[at];
-      cnt += a.pcnt[at];
+    for (int c = q.begin / a.chunk + wave; c <= c1; c += 16 * 16) {
+      float v[16];  // sixteen slots' loads at once
+      int n[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const int64_t at = ((int64_t)min(c + 16 * k, c1) + b) * a.E + e;
+        v[k] = a.psum[at];
+        n[k] = a.pcnt[at];
+      }
+#pragma unroll
+      for (int k = 0; k < 16; ++k)
+        if (c + 16 * k <= c1) {
+          sum += v[k];
+          cnt += n[k];
+        }
     }
   }
   sums[wave][lane] = sum;
@@ -187,14 +249,16 @@ struct Pieces {
 };
 
 // 16 columns of router_w, transposed, in scaled fp16 pieces: a thread takes 4 EPL consecutive experts of
-// a column.  `lds`: 256 words.
+// a column; a plane is laid out in LDS and written in whole rows.
+template <int EPL>
+constexpr int SPLIT_WORDS = 16 * (EPL * 32 + 4);  // 16 rows of E / 2 words, 16 bytes apart
 template <int EPL>
 __device__ __forceinline__ void split_weight(const DlogitsArgs& a, int block, uint32_t* lds) {
-  constexpr int E = EPL * 64, N = 4 * EPL;
-  const int col = threadIdx.x & 15, grp = threadIdx.x >> 4, h = block * 16 + col;
+  constexpr int E = EPL * 64, N = 4 * EPL, LD = E / 2 + 4;
+  const int col = threadIdx.x & 15, grp = threadIdx.x >> 4, h0 = block * 16;
   float v[N];
   uint32_t top = 0;
-  const float* src = a.w + (int64_t)grp * N * a.H + h;
+  const float* src = a.w + (int64_t)grp * N * a.H + h0 + col;
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = src[(int64_t)i * a.H];
 #pragma unroll
@@ -204,20 +268,21 @@ __device__ __forceinline__ void split_weight(const DlogitsArgs& a, int block, ui
 #pragma unroll
   for (int g = 0; g < 16; ++g) top = max(top, lds[g * 16 + col]);
   const int ex = half_exponent(top);
-  if (grp == 0) a.wexp[h] = ex;
-  uint16_t* const out = a.wt + (int64_t)h * E + grp * N;
+  if (grp == 0) a.wexp[h0 + col] = ex;
+  uint32_t w[2][N / 2];
 #pragma unroll
-  for (int i = 0; i < N; i += 4) {
-    u32x2 hi, lo;
+  for (int i = 0; i < N / 2; ++i) half_pieces(v[2 * i], v[2 * i + 1], ex, w[0][i], w[1][i]);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      uint32_t x, y;
-      half_pieces(v[i + 2 * j], v[i + 2 * j + 1], ex, x, y);
-      hi[j] = x;
-      lo[j] = y;
+  for (int p = 0; p < 2; ++p) {
+    if (p > a.pair) break;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N / 2; i += 2) *(u32x2*)(lds + col * LD + grp * (N / 2) + i) = u32x2{w[p][i], w[p][i + 1]};
+    __syncthreads();
+    for (int c = threadIdx.x; c < 16 * (E / 8); c += 256) {
+      const int row = c / (E / 8), at = c % (E / 8);
+      *(u32x4*)(a.wt + ((int64_t)p * a.H + h0 + row) * E + at * 8) = *(const u32x4*)(lds + row * LD + at * 4);
     }
-    *(u32x2*)(out + i) = hi;
-    if (a.pair) *(u32x2*)(out + (int64_t)a.H * E + i) = lo;
   }
 }
 
@@ -231,14 +296,16 @@ __device__ __forceinline__ void split_weight(const DlogitsArgs& a, int block, ui
 template <int EPL>
 __global__ __launch_bounds__(256) void dlogits_kernel(DlogitsArgs a) {
   constexpr int E = EPL * 64;
-  __shared__ __align__(16) float rows[4][E];
+  __shared__ __align__(16) uint32_t lds[SPLIT_WORDS<EPL>];
   __shared__ int first, tokens;
-  if ((int)blockIdx.x >= a.token_blocks) {
-    split_weight<EPL>(a, (int)blockIdx.x - a.token_blocks, (uint32_t*)&rows[0][0]);
+  if ((int)blockIdx.x < a.weight_blocks) {  // (first: they take longest)
+    split_weight<EPL>(a, blockIdx.x, lds);
     return;
   }
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t base = (int64_t)blockIdx.x * 4 * a.run;
+  static_assert(SPLIT_WORDS<EPL> >= 4 * E, "a row of every wave");
+  float(*const rows)[E] = (float(*)[E])lds;
+  const int64_t base = (int64_t)((int)blockIdx.x - a.weight_blocks) * 4 * a.run;
   int b = 0;
   float g0 = 0.f;
   if (a.counts) {
@@ -251,9 +318,26 @@ __global__ __launch_bounds__(256) void dlogits_kernel(DlogitsArgs a) {
   float f[EPL] = {};
   bool have = false;
   const int64_t t0 = base + (int64_t)wave * a.run, t1 = min(t0 + a.run, (int64_t)a.seq.T);
+  // the next token's loads are under way while one is computed
+  float ahead[EPL] = {};
+  int e_ahead = -1;
+  float g_ahead = 0.f;
+  auto fetch = [&](int64_t t) {
+    if (t >= t1) return;
+    Row<EPL>::load(a.logits + t * E, lane, ahead);
+    if (a.dtopk_w && lane < a.K) {
+      e_ahead = a.topk_idx[t * a.K + lane];
+      g_ahead = a.dtopk_w[t * a.K + lane];
+    }
+  };
+  fetch(t0);
   for (int64_t t = t0; t < t1; ++t) {
     float l[EPL], d[EPL];
-    Row<EPL>::load(a.logits + t * E, lane, l);
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) l[i] = ahead[i];
+    const int e = (unsigned)e_ahead < (unsigned)E ? e_ahead : -1;
+    const float dw = g_ahead;
+    fetch(t + 1);
     Score s[EPL];
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
@@ -289,20 +373,19 @@ __global__ __launch_bounds__(256) void dlogits_kernel(DlogitsArgs a) {
       }
     }
     if (a.dtopk_w) {
-      const float zero[EPL] = {};
-      Row<EPL>::store(rows[wave], lane, zero);
-      float v = 0.f;
-      int e = -1;
-      if (lane < a.K) {
-        e = a.topk_idx[t * a.K + lane];
-        if ((unsigned)e >= (unsigned)E) e = -1;
-      }
+      // the chosen experts' logits to their lanes, their gradients back, through the wave's row in LDS (a wave's
+      // LDS accesses run in order; the compiler, which sees one lane, must keep them so)
+      Row<EPL>::store(rows[wave], lane, l);
+      asm volatile("" ::: "memory");
       Score k{0.f, 0.f};
-      float g = 0.f;
+      float g = 0.f, v = 0.f;
       if (e >= 0) {
-        k = score_of(a.logits[t * E + e]);
-        g = a.dtopk_w[t * a.K + lane] * a.scale;
+        k = score_of(rows[wave][e]);
+        g = dw * a.scale;
       }
+      const float zero[EPL] = {};
+      asm volatile("" ::: "memory");
+      Row<EPL>::store(rows[wave], lane, zero);
       if (a.norm) {
         const float total = lane_of(row_sum(k.s), 0);  // (K <= 16: one row of lanes)
         const float share = total == 0.f ? 0.f : k.s / total;
@@ -311,7 +394,6 @@ __global__ __launch_bounds__(256) void dlogits_kernel(DlogitsArgs a) {
       } else {
         v = g * k.s * k.r;
       }
-      // (a wave's LDS accesses run in order; the compiler, which sees one lane, must keep them so)
       asm volatile("" ::: "memory");
       if (e >= 0) atomicAdd(&rows[wave][e], v);
       asm volatile("" ::: "memory");
@@ -350,6 +432,9 @@ __global__ __launch_bounds__(256) void dlogits_kernel(DlogitsArgs a) {
 
 }  // namespace
 
+// Up to this many logits one workgroup does it all.
+constexpr int64_t BALANCE_SMALL = 32768;
+
 int balance_chunk(int64_t T) {
   int c = 32;
   while (c < 256 && T > (int64_t)c * 1024) c *= 2;
@@ -367,8 +452,14 @@ int balance_chunk(int64_t T) {
   }
 
 hipError_t launch_balance(const BalanceArgs& a, hipStream_t s) {
-  const unsigned chunks = (unsigned)std::max<int64_t>(((int64_t)a.seq.T + a.chunk - 1) / a.chunk, 1);
-#define MOE_BAL(N) hipLaunchKernelGGL(balance_partial_kernel<N>, dim3(chunks), dim3(BAL_WAVES * 64), 0, s, a)
+  if ((int64_t)a.seq.T * a.E <= BALANCE_SMALL && a.seq.n <= std::max(a.seq.T, 16)) {
+#define MOE_BAL(N) hipLaunchKernelGGL(balance_small_kernel<N>, dim3(1), dim3(1024), 0, s, a)
+    MOE_EPL(a.E, MOE_BAL)
+#undef MOE_BAL
+    return hipGetLastError();
+  }
+  const unsigned chunks = (unsigned)(((int64_t)a.seq.T + a.chunk - 1) / a.chunk);
+#define MOE_BAL(N) hipLaunchKernelGGL(balance_partial_kernel<N>, dim3(std::max(chunks, 1u)), dim3(BAL_WAVES * 64), 0, s, a)
   MOE_EPL(a.E, MOE_BAL)
 #undef MOE_BAL
   const hipError_t e = hipGetLastError();
@@ -380,8 +471,8 @@ hipError_t launch_balance(const BalanceArgs& a, hipStream_t s) {
 hipError_t launch_dlogits(DlogitsArgs a, hipStream_t s) {
   if (a.seq.T == 0) return hipSuccess;
   a.run = (int)std::min<int64_t>(std::max<int64_t>(a.seq.T / 4096, 1), 8);
-  a.token_blocks = (int)(((int64_t)a.seq.T + 4 * a.run - 1) / (4 * a.run));
-  const unsigned grid = (unsigned)(a.token_blocks + (a.hf ? a.H / 16 : 0));
+  a.weight_blocks = a.hf ? a.H / 16 : 0;
+  const unsigned grid = (unsigned)(a.weight_blocks + ((int64_t)a.seq.T + 4 * a.run - 1) / (4 * a.run));
 #define MOE_DL(N) hipLaunchKernelGGL(dlogits_kernel<N>, dim3(grid), dim3(256), 0, s, a)
   MOE_EPL(a.E, MOE_DL)
 #undef MOE_DL

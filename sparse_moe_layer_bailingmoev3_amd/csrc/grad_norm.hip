@@ -6,9 +6,11 @@
 // The gradients are read once, in chunks of GRAD_CHUNK values that a table lists; the workgroups are
 // as many as fit the card and take every grid-th chunk, each leaving one sum in 64 bits; a second
 // launch of one workgroup adds them in order.  Squares are summed in fp32 within a lane's share of a
-// chunk (at most 64 values), in 64 bits from there on.  A chunk whose sum leaves 2^-60 .. 2^120 is
-// read again with squares in 64 bits: gradients whose squares overflow or vanish in fp32 have a
-// norm too.
+// chunk (64 values), in 64 bits from there on.  A share whose sum leaves 2^-60 .. 2^120 (all zeros
+// apart) is read again with squares in 64 bits: gradients whose squares overflow or vanish in fp32 have
+// a norm too.
+#include <type_traits>
+
 #include "moe_common.h"
 #include "moe_internal.h"
 
@@ -59,41 +61,53 @@ __device__ __forceinline__ void store8(void* p, int64_t i, int64_t n, const floa
   }
 }
 
-struct Table {
-  const GradTensor* tensors;
-  const GradChunk* chunks;
-};
-__device__ __forceinline__ bool open_table(const uint8_t* image, int64_t n_tensors, int64_t n_chunks, Table& t) {
-  const GradHeader* hd = (const GradHeader*)image;
-  // what is no image, or one of other sizes, is not followed
-  if (hd->magic != GRAD_MAGIC || hd->n_tensors != n_tensors || hd->n_chunks != n_chunks) return false;
-  t.tensors = (const GradTensor*)(hd + 1);
-  t.chunks = (const GradChunk*)(t.tensors + n_tensors);
-  return true;
-}
-
-// a lane's share of the chunk from value `base` on
-template <bool F32>
-__device__ __forceinline__ double chunk_sum(const void* p, int64_t base, int64_t n) {
-  float s[2] = {0.f, 0.f};
+// A lane's share of a chunk of n values, squared in fp32, or (WIDE) in 64 bits.  `any`: the bits of its
+// values, or-ed, signs apart.
+template <bool F32, bool WIDE>
+__device__ __forceinline__ double chunk_sum(const void* p, int n, uint32_t& any) {
+  typedef std::conditional_t<WIDE, double, float> sum_t;
+  sum_t s[2] = {0, 0};
+  any = 0;
+  auto add = [&](float v, int j) {
+    if constexpr (WIDE) s[j] += (double)v * (double)v;
+    else s[j] = __builtin_fmaf(v, v, s[j]);
+  };
+  if (n == GRAD_CHUNK) {
+    constexpr int W = GRAD_CHUNK / 2048 * (F32 ? 2 : 1);
+    u32x4 w[W];  // all loads at once
 #pragma unroll
-  for (int it = 0; it < GRAD_CHUNK / 2048; ++it) {
-    float v[8];
-    load8<F32>(p, base + it * 2048 + threadIdx.x * 8, n, v);
+    for (int i = 0; i < W; ++i) w[i] = ((const u32x4*)p)[i * 256 + threadIdx.x];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) s[j & 1] = __builtin_fmaf(v[j], v[j], s[j & 1]);
+    for (int i = 0; i < W; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        any |= w[i][j] & (F32 ? 0x7FFFFFFFu : 0x7FFF7FFFu);
+        if constexpr (F32) {
+          add(__uint_as_float(w[i][j]), j & 1);
+        } else {
+          add(__uint_as_float(w[i][j] << 16), 0);
+          add(__uint_as_float(w[i][j] & 0xFFFF0000u), 1);
+        }
+      }
+  } else {
+    for (int i = threadIdx.x * 8; i < n; i += 2048) {
+      float v[8];
+      load8<F32>(p, i, n, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        any |= __float_as_uint(v[j]) & 0x7FFFFFFFu;
+        add(v[j], j & 1);
+      }
+    }
   }
   return (double)s[0] + (double)s[1];
 }
 template <bool F32>
-__device__ double chunk_sum_wide(const void* p, int64_t base, int64_t n) {
-  double s = 0;
-  for (int it = 0; it < GRAD_CHUNK / 2048; ++it) {
-    float v[8];
-    load8<F32>(p, base + it * 2048 + threadIdx.x * 8, n, v);
-    for (int j = 0; j < 8; ++j) s += (double)v[j] * (double)v[j];
-  }
-  return s;
+__device__ __forceinline__ double chunk_sum(const void* p, int n) {
+  uint32_t any;
+  const double s = chunk_sum<F32, false>(p, n, any);
+  if (s < 0x1p120 && (s > 0x1p-60 || any == 0)) return s;
+  return chunk_sum<F32, true>(p, n, any);
 }
 
 __device__ __forceinline__ double wave_sum_f64(double v) {
@@ -102,19 +116,23 @@ __device__ __forceinline__ double wave_sum_f64(double v) {
   return v;
 }
 
+// what is no image, or one of other sizes, is not followed
+__device__ __forceinline__ bool is_image(const GradArgs& a) {
+  const GradHeader* hd = (const GradHeader*)a.image;
+  return hd->magic == GRAD_MAGIC && hd->n_tensors == a.n_tensors && hd->n_chunks == a.n_chunks;
+}
+__device__ __forceinline__ const GradChunk* chunks_of(const GradArgs& a) { return (const GradChunk*)(a.image + sizeof(GradHeader)); }
+
 __global__ __launch_bounds__(256) void grad_norm_kernel(GradArgs a) {
   __shared__ double sums[4];
-  Table tb;
   double total = 0;
-  if (open_table(a.image, a.n_tensors, a.n_chunks, tb)) {
-    for (int64_t c = blockIdx.x; c < a.n_chunks; c += gridDim.x) {
-      const GradChunk ck = tb.chunks[c];
-      const GradTensor t = tb.tensors[ck.tensor];
-      const int64_t base = (int64_t)ck.chunk * GRAD_CHUNK;
-      double s = t.flags & GRAD_IN_F32 ? chunk_sum<true>(t.in, base, t.numel) : chunk_sum<false>(t.in, base, t.numel);
-      // (a lane alone decides for its share; zeros need no second look, but come cheap)
-      if (!(s > 0x1p-60 && s < 0x1p120)) s = t.flags & GRAD_IN_F32 ? chunk_sum_wide<true>(t.in, base, t.numel) : chunk_sum_wide<false>(t.in, base, t.numel);
-      total += s;
+  if (is_image(a)) {
+    GradChunk next = chunks_of(a)[blockIdx.x];
+    for (int64_t c = blockIdx.x; c < a.n_chunks;) {
+      const GradChunk ck = next;
+      c += gridDim.x;
+      if (c < a.n_chunks) next = chunks_of(a)[c];
+      total += ck.flags & GRAD_IN_F32 ? chunk_sum<true>(ck.in, ck.n) : chunk_sum<false>(ck.in, ck.n);
     }
   }
   total = wave_sum_f64(total);
@@ -125,10 +143,13 @@ __global__ __launch_bounds__(256) void grad_norm_kernel(GradArgs a) {
 
 __global__ __launch_bounds__(1024) void grad_norm_finish_kernel(GradArgs a, int n) {
   __shared__ double sums[16];
-  const GradHeader* hd = (const GradHeader*)a.image;
-  if (a.n_chunks && (hd->magic != GRAD_MAGIC || hd->n_tensors != a.n_tensors || hd->n_chunks != a.n_chunks)) return;
+  if (a.n_chunks && !is_image(a)) return;
   double s = 0;
-  for (int i = threadIdx.x; i < n; i += 1024) s += a.partial[i];
+#pragma unroll
+  for (int i = 0; i < GRAD_MAX_PARTIALS / 1024; ++i) {
+    const int at = i * 1024 + threadIdx.x;
+    if (at < n) s += a.partial[at];
+  }
   s = wave_sum_f64(s);
   if ((threadIdx.x & 63) == 0) sums[threadIdx.x >> 6] = s;
   __syncthreads();
@@ -143,32 +164,49 @@ __global__ __launch_bounds__(1024) void grad_norm_finish_kernel(GradArgs a, int 
 }
 
 template <bool IF32, bool OF32>
-__device__ __forceinline__ void clip_chunk(const GradTensor& t, int64_t base, float c) {
+__device__ __forceinline__ void clip_chunk(const GradChunk& ck, float c) {
+  if (ck.n == GRAD_CHUNK) {  // the loads of half a chunk at once
 #pragma unroll
-  for (int it = 0; it < GRAD_CHUNK / 2048; ++it) {
-    const int64_t i = base + it * 2048 + threadIdx.x * 8;
-    if (i >= t.numel) break;
-    float v[8];
-    load8<IF32>(t.in, i, t.numel, v);
+    for (int h = 0; h < 2; ++h) {
+      constexpr int N = GRAD_CHUNK / 4096;
+      u32x4 w[N][IF32 ? 2 : 1];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] *= c;
-    store8<OF32>(t.out, i, t.numel, v);
+      for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int k = 0; k < (IF32 ? 2 : 1); ++k)
+          w[i][k] = ((const u32x4*)ck.in)[((h * N + i) * 256 + threadIdx.x) * (IF32 ? 2 : 1) + k];
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if constexpr (IF32) v[j] = __uint_as_float(w[i][j / 4][j & 3]) * c;
+          else v[j] = __uint_as_float(j & 1 ? w[i][0][j / 2] & 0xFFFF0000u : w[i][0][j / 2] << 16) * c;
+        }
+        store8<OF32>(ck.out, ((int64_t)(h * N + i) * 256 + threadIdx.x) * 8, GRAD_CHUNK, v);
+      }
+    }
+  } else {
+    for (int i = threadIdx.x * 8; i < ck.n; i += 2048) {
+      float v[8];
+      load8<IF32>(ck.in, i, ck.n, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] *= c;
+      store8<OF32>(ck.out, i, ck.n, v);
+    }
   }
 }
 
 __global__ __launch_bounds__(256) void grad_clip_kernel(GradArgs a) {
-  Table tb;
-  if (!open_table(a.image, a.n_tensors, a.n_chunks, tb)) return;
   const float c = *a.coef;
-  const GradChunk ck = tb.chunks[blockIdx.x];
-  const GradTensor t = tb.tensors[ck.tensor];
-  if (t.in == t.out && c == 1.f) return;  // in place: nothing changes
-  const int64_t base = (int64_t)ck.chunk * GRAD_CHUNK;
-  switch (t.flags & (GRAD_IN_F32 | GRAD_OUT_F32)) {
-    case 0: clip_chunk<false, false>(t, base, c); break;
-    case GRAD_IN_F32: clip_chunk<true, false>(t, base, c); break;
-    case GRAD_OUT_F32: clip_chunk<false, true>(t, base, c); break;
-    default: clip_chunk<true, true>(t, base, c);
+  if (!is_image(a)) return;
+  const GradChunk ck = chunks_of(a)[blockIdx.x];
+  if (ck.in == ck.out && c == 1.f) return;  // in place: nothing changes
+  switch (ck.flags & (GRAD_IN_F32 | GRAD_OUT_F32)) {
+    case 0: clip_chunk<false, false>(ck, c); break;
+    case GRAD_IN_F32: clip_chunk<true, false>(ck, c); break;
+    case GRAD_OUT_F32: clip_chunk<false, true>(ck, c); break;
+    default: clip_chunk<true, true>(ck, c);
   }
 }
 

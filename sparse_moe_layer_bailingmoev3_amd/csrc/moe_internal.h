@@ -297,13 +297,13 @@ struct DlogitsArgs {
   const float* w; int H;   // router_w [E, H], taken apart by the same launch (hf given)
   uint16_t* wt;            // fp16 [1 + pair, H, E], row h times 2^wexp[h]
   int32_t* wexp;           // [H]
-  int run, token_blocks;   // tokens of a wave, workgroups of the tokens (set by the launch)
+  int run, weight_blocks;  // tokens of a wave, workgroups that take router_w apart (set by the launch)
 };
 hipError_t launch_dlogits(DlogitsArgs a, hipStream_t s);
 
 constexpr int ROUTER_TILE_MAX = 128;  // largest tile of the products: the exponents' arrays reach to its end
 struct RouterGradPlan {
-  int tile;                  // square tiles
+  int tile;                  // square tiles: 128 or 64
   int nsplit, split_steps;   // d router_w: parts of the reduction over tokens, steps of 32 in each
 };
 RouterGradPlan router_grad_plan(int64_t T, int E, int H, bool dw, bool dx, bool f32);
@@ -323,12 +323,11 @@ hipError_t launch_router_grad(RouterGradArgs a, hipStream_t s);
 hipError_t launch_sum_logits(const float* partial, int nsplit, int64_t n, float* out, hipStream_t s);
 
 // ---- norm over many gradients, clipping (grad_norm.hip) --------------------------------
-constexpr int GRAD_CHUNK = 16384;        // values of one table entry
+constexpr int GRAD_CHUNK = 8192;        // values of one table entry
 constexpr int GRAD_MAX_PARTIALS = 4096;  // workgroups of the norm: one sum each in the workspace
 constexpr uint64_t GRAD_MAGIC = 0x314e44415247454dull;
-struct GradHeader { uint64_t magic; int64_t n_tensors, n_chunks, pad; };  // plan image: header, tensors, chunks
-struct GradTensor { const void* in; void* out; int64_t numel; int64_t flags; };
-struct GradChunk { int32_t tensor, chunk; };
+struct GradHeader { uint64_t magic; int64_t n_tensors, n_chunks, pad; };  // plan image: header, chunks
+struct GradChunk { const void* in; void* out; int32_t n, flags; };  // what a workgroup needs, in one load
 enum { GRAD_IN_F32 = 1, GRAD_OUT_F32 = 2 };
 struct GradArgs {
   const uint8_t* image;

@@ -281,7 +281,7 @@ moe_status_t moe_grad_plan(int64_t n_tensors, const moe_grad_tensor_t* tensors, 
   plan->n_tensors = n_tensors;
   plan->n_chunks = chunks;
   plan->workspace_bytes = moe::GRAD_MAX_PARTIALS * sizeof(double);
-  plan->image_bytes = sizeof(moe::GradHeader) + (size_t)n_tensors * sizeof(moe::GradTensor) + (size_t)chunks * sizeof(moe::GradChunk);
+  plan->image_bytes = sizeof(moe::GradHeader) + (size_t)chunks * sizeof(moe::GradChunk);
   if (!image) return MOE_OK;
   if (image_bytes < plan->image_bytes)
     return fail(MOE_ERR_WORKSPACE, "plan image has %zu bytes, %zu needed", image_bytes, plan->image_bytes);
@@ -315,17 +315,14 @@ moe_status_t moe_grad_plan(int64_t n_tensors, const moe_grad_tensor_t* tensors, 
   at += sizeof(hd);
   for (int64_t i = 0; i < n_tensors; ++i) {
     const moe_grad_tensor_t& t = tensors[i];
-    const moe::GradTensor d{t.grad, t.out ? t.out : t.grad, t.numel,
-                            (t.grad_dtype == MOE_DTYPE_FP32 ? moe::GRAD_IN_F32 : 0) | (t.out_dtype == MOE_DTYPE_FP32 ? moe::GRAD_OUT_F32 : 0)};
-    memcpy(at, &d, sizeof(d));
-    at += sizeof(d);
-  }
-  for (int64_t i = 0; i < n_tensors; ++i)
-    for (int64_t c = 0; c * moe::GRAD_CHUNK < tensors[i].numel; ++c) {
-      const moe::GradChunk k{(int32_t)i, (int32_t)c};
+    const int32_t flags = (t.grad_dtype == MOE_DTYPE_FP32 ? moe::GRAD_IN_F32 : 0) | (t.out_dtype == MOE_DTYPE_FP32 ? moe::GRAD_OUT_F32 : 0);
+    for (int64_t c = 0; c < t.numel; c += moe::GRAD_CHUNK) {
+      const moe::GradChunk k{(const char*)t.grad + c * dsize(t.grad_dtype), (char*)(t.out ? t.out : t.grad) + c * dsize(t.out_dtype),
+                             (int32_t)std::min<int64_t>(t.numel - c, moe::GRAD_CHUNK), flags};
       memcpy(at, &k, sizeof(k));
       at += sizeof(k);
     }
+  }
   return MOE_OK;
 }
 

@@ -17,10 +17,11 @@
 // Both products are tiles of one launch, the weight gradient's (longer ones) first: the tokens' tiles,
 // which end in reading and writing dx, then run beside them on the same compute units.
 //
-// One tile engine: BR rows by BC columns of the result, reduction steps of 32 values, both operands'
-// planes brought into a ring of NST LDS stages by direct loads.  dx's planes run along the reduction
-// and are read as they lie; d router_w's run across it and are read through the transposing LDS load.
-// Rows past the end are offsets past a buffer descriptor's end: zeros.
+// One tile engine: BR rows by BC columns of the result, reduction steps of KS values, both operands'
+// planes brought into a ring of NST LDS stages by direct loads, products on the 32 x 32 x 16 matrix
+// instruction.  dx's planes run along the reduction and are read as they lie; d router_w's run across it
+// and are read through the transposing LDS load.  Rows past the end are offsets past a buffer
+// descriptor's end: zeros.
 #include "moe_common.h"
 #include "moe_internal.h"
 #include "tile_ops.h"
@@ -31,25 +32,48 @@ namespace {
 
 constexpr int OP_DW = 0, OP_DX = 1;
 
+typedef float floatx16 __attribute__((ext_vector_type(16)));
+
+// 32 x 32 x 16 products.  Operands: lane l holds row l % 32, reduction values 8 (l / 32) .. +7.  Result:
+// lane l holds column l % 32 (of b), rows 8g + 4 (l / 32) .. +3 (of a) in elements 4g .. 4g+3.
+template <int OP>
+__device__ __forceinline__ floatx16 mfma32(const u32x4& a, const u32x4& b, floatx16 c) {
+  if constexpr (OP == OP_DW)
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+
 // what a tile of BR x BC takes from LDS
-template <int OP, int BR, int BC, bool F32>
+template <int OP, int BR, int BC, int KS_, bool F32>
 struct Stage {
-  static constexpr int KS = 32, PX = OP == OP_DW ? 3 : F32 ? 2 : 1, PY = OP == OP_DX && F32 ? 2 : 1;  // planes
+  static constexpr int KS = KS_, PX = OP == OP_DW ? 3 : F32 ? 2 : 1, PY = OP == OP_DX && F32 ? 2 : 1;  // planes
   static constexpr int X_BYTES = BR * KS * 2, Y_BYTES = BC * KS * 2, BYTES = PX * X_BYTES + PY * Y_BYTES;
 };
 
-template <int OP, int BR, int BC, int WR, int WC, int NST, bool F32>
+// 16-byte chunk swizzles.  Rows of KS reduction values (2 or 4 chunks): the 16-byte LDS read serves lanes
+// 0-3, 12-15, 20-23, 24-27 of each half wave together, then the others.
+template <int KS>
+__device__ __forceinline__ int swz_row(int row) { return KS == 16 ? (row >> 4) & 1 : (row >> 2) & 3; }
+// Rows of W output values under the transposing read, which touches rows r..r+3 and two blocks of 32 bytes
+// in each half wave.
+template <int W>
+__device__ __forceinline__ int swz_cols(int row) { return W >= 128 ? (row & 3) << 2 : (row & 2) << 1; }
+
+template <int OP, int BR, int BC, int WR, int WC, int KS, int NST, bool F32>
 __device__ __forceinline__ void router_tile(const RouterGradArgs& a, int block, int blocks, uint8_t* lds) {
-  typedef Stage<OP, BR, BC, F32> St;
-  constexpr int NW = WR * WC, KS = St::KS, PX = St::PX, PY = St::PY;
+  typedef Stage<OP, BR, BC, KS, F32> St;
+  constexpr int NW = WR * WC, PX = St::PX, PY = St::PY;
   constexpr int X_BYTES = St::X_BYTES, Y_BYTES = St::Y_BYTES, ST_BYTES = St::BYTES;
   constexpr int XN = X_BYTES / (NW * 1024), YN = Y_BYTES / (NW * 1024), LN = PX * XN + PY * YN;  // loads per wave
   static_assert(XN * NW * 1024 == X_BYTES && YN * NW * 1024 == Y_BYTES, "a plane must split evenly over the waves");
-  constexpr int RJ = BR / WR / 16, CJ = BC / WC / 16;
+  constexpr int RJ = BR / WR / 32, CJ = BC / WC / 32;
+  constexpr int KC = KS / 8;                 // chunks of a row of reduction values
+  constexpr int NA = RJ * CJ == 1 ? 2 : 1;   // sums that take turns (one alone would wait for itself)
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int r16 = lane & 15, q = lane >> 4;
+  const int r32 = lane & 31, half = lane >> 5;
   const int wr = wave / WC, wc = wave % WC;
 
   // ---- which tile: consecutive ones (the column tiles of a row tile, the tiles of a split) on one XCD
@@ -60,8 +84,8 @@ __device__ __forceinline__ void router_tile(const RouterGradArgs& a, int block, 
   if (item >= total) return;
   const int split = item / tiles, tile = item - split * tiles;
   const int rt = tile / nct, r0 = rt * BR, c0 = (tile - rt * nct) * BC;
-  const int red0 = OP == OP_DW ? split * a.split_steps * KS : 0;
-  const int red = OP == OP_DW ? max(min(a.T - red0, a.split_steps * KS), 0) : a.E;
+  const int red0 = OP == OP_DW ? split * a.split_steps * 32 : 0;
+  const int red = OP == OP_DW ? max(min(a.T - red0, a.split_steps * 32), 0) : a.E;
   const int nsteps = (red + KS - 1) / KS;
 
   // ---- loads
@@ -73,8 +97,8 @@ __device__ __forceinline__ void router_tile(const RouterGradArgs& a, int block, 
     each<PY>([&](auto p) { yb[p] = (uint64_t)(a.wt + ((int64_t)p * a.H + c0) * a.E); });
     xstep = ystep = KS * 2;
     auto offset = [&](int load, int rows) {
-      const int row = load * 16 + lane / 4;
-      return row < rows ? (uint32_t)(row * a.E * 2 + (((lane & 3) ^ ((row >> 2) & 3)) << 4)) : BUF_OUT;
+      const int row = load * (64 / KC) + lane / KC;
+      return row < rows ? (uint32_t)(row * a.E * 2 + (((lane % KC) ^ swz_row<KS>(row)) << 4)) : BUF_OUT;
     };
     each<XN>([&](auto i) { xo[i] = offset(wave * XN + i, a.T - r0); });
     each<YN>([&](auto i) { yo[i] = offset(wave * YN + i, a.H - c0); });
@@ -85,11 +109,11 @@ __device__ __forceinline__ void router_tile(const RouterGradArgs& a, int block, 
     xstep = KS * a.E * 2;
     ystep = KS * a.H * 2;
     each<XN>([&](auto i) {
-      const int row = xrow[i] = (wave * XN + i) * (64 / XL) + lane / XL, ch = (lane % XL) ^ swz_tr<BR>(row);
+      const int row = xrow[i] = (wave * XN + i) * (64 / XL) + lane / XL, ch = (lane % XL) ^ swz_cols<BR>(row);
       xo[i] = r0 + ch * 8 < a.E ? (uint32_t)(row * a.E * 2 + ch * 16) : BUF_OUT;
     });
     each<YN>([&](auto i) {
-      const int row = yrow[i] = (wave * YN + i) * (64 / YL) + lane / YL, ch = (lane % YL) ^ swz_tr<BC>(row);
+      const int row = yrow[i] = (wave * YN + i) * (64 / YL) + lane / YL, ch = (lane % YL) ^ swz_cols<BC>(row);
       yo[i] = c0 + ch * 8 < a.H ? (uint32_t)(row * a.H * 2 + ch * 16) : BUF_OUT;
     });
   }
@@ -117,53 +141,66 @@ __device__ __forceinline__ void router_tile(const RouterGradArgs& a, int block, 
     lst = lst == lds0 + (NST - 1) * ST_BYTES ? lds0 : lst + ST_BYTES;
   };
 
-  // ---- LDS read addresses
-  int xa[OP == OP_DW ? RJ : 1], ya[OP == OP_DW ? CJ : 1];
+  // ---- LDS read addresses.  Transposed: lanes 16g .. 16g+15 read rows 8 (g/2) .. of column block g%2.
+  int xa[OP == OP_DW ? RJ : KS / 16], ya[OP == OP_DW ? CJ : KS / 16];
   if constexpr (OP == OP_DW) {
-    const int row = 8 * q + (r16 >> 2);
+    const int row = 8 * half + ((lane & 15) >> 2), block16 = (lane >> 4) & 1, in = (lane & 3) * 8;
 #pragma unroll
-    for (int j = 0; j < RJ; ++j) xa[j] = row * BR * 2 + ((((wr * RJ + j) * 2) ^ swz_tr<BR>(row)) << 4) + (r16 & 3) * 8;
+    for (int j = 0; j < RJ; ++j)
+      xa[j] = row * BR * 2 + ((((wr * RJ + j) * 4 + block16 * 2) ^ swz_cols<BR>(row)) << 4) + in;
 #pragma unroll
     for (int j = 0; j < CJ; ++j)
-      ya[j] = PX * X_BYTES + row * BC * 2 + ((((wc * CJ + j) * 2) ^ swz_tr<BC>(row)) << 4) + (r16 & 3) * 8;
+      ya[j] = PX * X_BYTES + row * BC * 2 + ((((wc * CJ + j) * 4 + block16 * 2) ^ swz_cols<BC>(row)) << 4) + in;
   } else {
-    xa[0] = (wr * RJ * 16 + r16) * 64 + ((q ^ ((r16 >> 2) & 3)) << 4);
-    ya[0] = PX * X_BYTES + (wc * CJ * 16 + r16) * 64 + ((q ^ ((r16 >> 2) & 3)) << 4);
+#pragma unroll
+    for (int u = 0; u < KS / 16; ++u) {
+      xa[u] = (wr * RJ * 32 + r32) * KS * 2 + (((2 * u + half) ^ swz_row<KS>(r32)) << 4);
+      ya[u] = PX * X_BYTES + (wc * CJ * 32 + r32) * KS * 2 + (((2 * u + half) ^ swz_row<KS>(r32)) << 4);
+    }
   }
-  auto frag = [&](const uint8_t* st, const int* at, int j, int row_bytes) {
+  auto frag = [&](const uint8_t* st, const int* at, int j, int u, int row_bytes) {
     if constexpr (OP == OP_DW) {
-      const u32x2 lo = lds_read_tr(st + at[j]), hi = lds_read_tr(st + at[j] + 4 * row_bytes);
+      const uint8_t* const p = st + at[j] + u * 16 * row_bytes;
+      const u32x2 lo = lds_read_tr(p), hi = lds_read_tr(p + 4 * row_bytes);
       return u32x4{lo[0], lo[1], hi[0], hi[1]};
     } else {
-      return *(const u32x4*)(st + at[0] + j * 16 * 64);
+      return *(const u32x4*)(st + at[u] + j * 32 * KS * 2);
     }
   };
 
-  floatx4 acc[CJ][RJ];
+  floatx16 acc[NA][CJ][RJ];
 #pragma unroll
-  for (int c = 0; c < CJ; ++c)
+  for (int n = 0; n < NA; ++n)
 #pragma unroll
-    for (int r = 0; r < RJ; ++r) acc[c][r] = floatx4{0.f, 0.f, 0.f, 0.f};
+    for (int c = 0; c < CJ; ++c)
+#pragma unroll
+      for (int r = 0; r < RJ; ++r)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[n][c][r][i] = 0.f;
 
   auto compute = [&](const uint8_t* st) {
-    u32x4 yf[PY][CJ];
 #pragma unroll
-    for (int p = 0; p < PY; ++p)
+    for (int u = 0; u < KS / 16; ++u) {
+      u32x4 yf[PY][CJ];
 #pragma unroll
-      for (int c = 0; c < CJ; ++c) yf[p][c] = frag(st + p * Y_BYTES, ya, c, BC * 2);
+      for (int p = 0; p < PY; ++p)
 #pragma unroll
-    for (int r = 0; r < RJ; ++r) {
-      u32x4 xf[PX];
+        for (int c = 0; c < CJ; ++c) yf[p][c] = frag(st + p * Y_BYTES, ya, c, u, BC * 2);
 #pragma unroll
-      for (int p = 0; p < PX; ++p) xf[p] = frag(st + p * X_BYTES, xa, r, BR * 2);
-      // small terms first
+      for (int r = 0; r < RJ; ++r) {
+        u32x4 xf[PX];
 #pragma unroll
-      for (int p = PX + PY - 2; p >= 0; --p)
+        for (int p = 0; p < PX; ++p) xf[p] = frag(st + p * X_BYTES, xa, r, u, BR * 2);
+        // small terms first
 #pragma unroll
-        for (int c = 0; c < CJ; ++c) {
-          if constexpr (OP == OP_DW) acc[c][r] = mfma16(yf[0][c], xf[p], acc[c][r]);
-          else acc[c][r] = mfma16_f16(yf[p == 2 ? PY - 1 : 0][c], xf[p == 2 ? 0 : p], acc[c][r]);
-        }
+        for (int p = PX + PY - 2; p >= 0; --p)
+#pragma unroll
+          for (int c = 0; c < CJ; ++c) {
+            floatx16& s = acc[(u * (PX + PY - 1) + p) % NA][c][r];
+            if constexpr (OP == OP_DW) s = mfma32<OP>(yf[0][c], xf[p], s);
+            else s = mfma32<OP>(yf[p == 2 ? PY - 1 : 0][c], xf[p == 2 ? 0 : p], s);
+          }
+      }
     }
   };
 
@@ -182,40 +219,43 @@ __device__ __forceinline__ void router_tile(const RouterGradArgs& a, int block, 
     stage = stage == (NST - 1) * ST_BYTES ? 0 : stage + ST_BYTES;
   }
 
-  // ---- result: lane (r16, q) holds columns 16c + 4q .. +3 of row r16 of the fragments; four fragments
-  // turned within quads of lanes make 16 lanes hold one row's 64 columns (whole cache lines)
-  static_assert(CJ % 4 == 0 || CJ == 2, "column fragments");
-  constexpr bool TURN = CJ % 4 == 0;
+  // ---- result: four pieces of four columns a lane, turned within quads of lanes: 4 lanes of both half
+  // waves then hold 32 columns of one row side by side (whole cache lines)
   const int rows = OP == OP_DW ? a.E : a.T;
   float* const o32 = OP == OP_DX ? (float*)a.dx : a.nsplit > 1 ? a.part + (int64_t)split * a.E * a.H : a.dw;
   const bool add = OP == OP_DX ? a.acc_x : a.acc_w && a.nsplit == 1;
+  const int row0 = r0 + wr * RJ * 32 + (r32 & 28);
 #pragma unroll
-  for (int cb = 0; cb < (TURN ? CJ / 4 : 1); ++cb) {
-    constexpr int CN = TURN ? 4 : CJ;
-    const int row0 = r0 + wr * RJ * 16 + (TURN ? r16 & 12 : r16);
-    const int col0 = c0 + (wc * CJ + cb * 4) * 16 + 4 * q + (TURN ? (r16 & 3) * 16 : 0);
+  for (int c = 0; c < CJ; ++c) {
+    const int col = c0 + (wc * CJ + c) * 32 + 8 * (r32 & 3) + 4 * half;
+    int4 ec{0, 0, 0, 0};
+    if constexpr (OP == OP_DX) ec = *(const int4*)(a.wexp + col);  // (the exponents' arrays reach to the end of the last tile)
 #pragma unroll
     for (int r = 0; r < RJ; ++r) {
-      floatx4 v[CN];
+      floatx4 v[4], old[4];
 #pragma unroll
-      for (int j = 0; j < CN; ++j) v[j] = acc[cb * 4 + j][r];
-      if constexpr (TURN) quad_transpose(v);
-      floatx4 old[CN];
+      for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int j = 0; j < CN; ++j) {
-        const int row = row0 + r * 16 + (TURN ? j : 0), col = col0 + (TURN ? 0 : j * 16);
-        const bool ok = row < rows && col < a.H;
-        if (F32 && add) old[j] = *(const floatx4*)(o32 + (ok ? (int64_t)row * a.H + col : 0));
-        if constexpr (OP == OP_DX) {  // (the exponents' arrays reach to the end of the last tile)
-          const int er = a.dexp[row];
-          const int4 ec = *(const int4*)(a.wexp + col);
-          v[j] = floatx4{__builtin_amdgcn_ldexpf(v[j][0], -(er + ec.x)), __builtin_amdgcn_ldexpf(v[j][1], -(er + ec.y)),
-                         __builtin_amdgcn_ldexpf(v[j][2], -(er + ec.z)), __builtin_amdgcn_ldexpf(v[j][3], -(er + ec.w))};
+        for (int i = 0; i < 4; ++i) {
+          v[j][i] = acc[0][c][r][4 * j + i];
+          if constexpr (NA == 2) v[j][i] += acc[NA - 1][c][r][4 * j + i];
+        }
+      quad_transpose(v);
+      int4 er{0, 0, 0, 0};
+      if constexpr (OP == OP_DX) er = *(const int4*)(a.dexp + row0 + r * 32);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int row = row0 + r * 32 + j;
+        if (F32 && add) old[j] = *(const floatx4*)(o32 + (row < rows && col < a.H ? (int64_t)row * a.H + col : 0));
+        if constexpr (OP == OP_DX) {
+          const int e = j == 0 ? er.x : j == 1 ? er.y : j == 2 ? er.z : er.w;
+          v[j] = floatx4{__builtin_amdgcn_ldexpf(v[j][0], -(e + ec.x)), __builtin_amdgcn_ldexpf(v[j][1], -(e + ec.y)),
+                         __builtin_amdgcn_ldexpf(v[j][2], -(e + ec.z)), __builtin_amdgcn_ldexpf(v[j][3], -(e + ec.w))};
         }
       }
 #pragma unroll
-      for (int j = 0; j < CN; ++j) {
-        const int row = row0 + r * 16 + (TURN ? j : 0), col = col0 + (TURN ? 0 : j * 16);
+      for (int j = 0; j < 4; ++j) {
+        const int row = row0 + r * 32 + j;
         if (row >= rows || col >= a.H) continue;
         const int64_t at = (int64_t)row * a.H + col;
         if (F32 && add) v[j] += old[j];
@@ -238,51 +278,55 @@ __global__ __launch_bounds__(256) void router_join_kernel(RouterGradArgs a) {
   *(floatx4*)(a.dw + i) = v + s;
 }
 
-template <int BR, int BC, int WR, int WC, int NST, bool F32>
+template <int BR, int BC, int WR, int WC, int KS, int NW, int NX, bool F32>
 __global__ __launch_bounds__(WR* WC * 64, 2) void router_products_kernel(RouterGradArgs a, int dw_blocks) {
-  constexpr int DW = Stage<OP_DW, BR, BC, true>::BYTES, DX = Stage<OP_DX, BR, BC, F32>::BYTES;
-  __shared__ __align__(16) uint8_t lds[NST * (DW > DX ? DW : DX)];
+  constexpr int DW = NW * Stage<OP_DW, BR, BC, KS, true>::BYTES, DX = NX * Stage<OP_DX, BR, BC, KS, F32>::BYTES;
+  __shared__ __align__(16) uint8_t lds[DW > DX ? DW : DX];
   const int block = blockIdx.x;
-  if (block < dw_blocks) router_tile<OP_DW, BR, BC, WR, WC, NST, true>(a, block, dw_blocks, lds);
-  else router_tile<OP_DX, BR, BC, WR, WC, NST, F32>(a, block - dw_blocks, (int)gridDim.x - dw_blocks, lds);
+  if (block < dw_blocks) router_tile<OP_DW, BR, BC, WR, WC, KS, NW, true>(a, block, dw_blocks, lds);
+  else router_tile<OP_DX, BR, BC, WR, WC, KS, NX, F32>(a, block - dw_blocks, (int)gridDim.x - dw_blocks, lds);
 }
 
-template <int B, int WR, int WC, int NST>
+template <int BR, int BC, int WR, int WC, int KS, int NW, int NX>
 void run_products(const RouterGradArgs& a, hipStream_t s) {
-  auto blocks = [&](int64_t rows, int n) { return (int)(((rows + B - 1) / B * ((a.H + B - 1) / B) * n + 7) / 8 * 8); };
+  auto blocks = [&](int64_t rows, int n) { return (int)(((rows + BR - 1) / BR * ((a.H + BC - 1) / BC) * n + 7) / 8 * 8); };
   const int dw = a.dw ? blocks(a.E, a.nsplit) : 0, dx = a.dx && a.T > 0 ? blocks(a.T, 1) : 0;
   if (dw + dx == 0) return;
   if (a.dx_f32)
-    hipLaunchKernelGGL((router_products_kernel<B, B, WR, WC, NST, true>), dim3((unsigned)(dw + dx)), dim3(WR * WC * 64), 0, s, a, dw);
+    hipLaunchKernelGGL((router_products_kernel<BR, BC, WR, WC, KS, NW, NX, true>), dim3((unsigned)(dw + dx)), dim3(WR * WC * 64), 0, s, a, dw);
   else
-    hipLaunchKernelGGL((router_products_kernel<B, B, WR, WC, NST, false>), dim3((unsigned)(dw + dx)), dim3(WR * WC * 64), 0, s, a, dw);
+    hipLaunchKernelGGL((router_products_kernel<BR, BC, WR, WC, KS, NW, NX, false>), dim3((unsigned)(dw + dx)), dim3(WR * WC * 64), 0, s, a, dw);
 }
 
 }  // namespace
 
 // Tile size and the parts of the weight gradient's reduction, by price: a step of one product of a tile
-// takes `step` us on a place (`wgs` workgroups a compute unit); the weight gradient's items are started
-// first, the others fill the places that they leave.
+// takes `full` us on a place with all `wgs` places of its compute unit taken, `alone` at least; `end` is a tile's
+// beginning and end, 5 us what a third launch costs, besides the parts' bytes.  The weight gradient's items
+// are started first, the others fill the places that they leave.  Fitted to sweeps over 16 to 8192 tokens at
+// 64 x 512 to 1024 x 2560.  Sides measured (us a call, 512 x 2560, fp32 dx):
+//   512 tokens:  128 28.2, 64 29.1     2048: 128 in 2 parts 49.3, 4 56.0; 64 59.0     8192: 128 141, 64 205
+//   1024 tokens of 128 x 640: 64 in one part 18.4, 8 18.4; 4096: 64 in 8 parts 22.3, 128 25.2
 RouterGradPlan router_grad_plan(int64_t T, int E, int H, bool dw, bool dx, bool f32) {
   struct Shape {
     int tile, wgs;
-    float step, end;
+    float alone, full, end;
   };
-  static const Shape shapes[2] = {{128, 2, .45f, 3.f}, {64, 2, .25f, 2.f}};
+  static const Shape shapes[2] = {{128, 2, .25f, .45f, 4.f}, {64, 2, .05f, .17f, 2.5f}};
   const int64_t steps = std::max<int64_t>((T + 31) / 32, 1);
   RouterGradPlan best{};
   double cost = -1;
   for (const Shape& v : shapes) {
     const double places = 256.0 * v.wgs;
     const int64_t ct = (H + v.tile - 1) / v.tile, dwt = dw ? (E + v.tile - 1) / v.tile * ct : 0, dxt = dx ? (T + v.tile - 1) / v.tile * ct : 0;
-    const double dx_len = (E / 32) * (f32 ? 3 : 1) * v.step + v.end;
     for (int64_t n = 1; n <= (dw ? std::min<int64_t>(steps, 32) : 1); ++n) {
       const int64_t per = (steps + n - 1) / n;
       if ((steps + per - 1) / per != n) continue;
-      const double len = per * 3 * v.step + v.end, items = (double)dwt * n;
-      const double first = std::ceil(items / places) * len;
-      const double c = std::max(first, (items * len + dxt * dx_len) / places + (dxt ? .5 * dx_len : 0)) +
-                       (n > 1 ? 3 + n * (double)E * H * 8 / 5e6 : 0);
+      const double items = (double)dwt * n, load = std::min<double>(v.wgs, std::max(1.0, (items + dxt) / 256));
+      const double step = std::max<double>(v.alone, v.full * load / v.wgs);
+      const double len = per * 3 * step + v.end, dx_len = dxt ? (E / 32) * (f32 ? 3 : 1) * step + v.end : 0;
+      const double c = std::max(std::ceil(items / places) * len, (items * len + dxt * dx_len) / places + .5 * dx_len) +
+                       (n > 1 ? 5 + n * (double)E * H * 8 / 5e6 : 0);
       if (cost < 0 || c < cost) {
         cost = c;
         best = {v.tile, (int)n, (int)per};
@@ -296,8 +340,8 @@ hipError_t launch_router_grad(RouterGradArgs a, hipStream_t s) {
   const RouterGradPlan p = router_grad_plan(a.T, a.E, a.H, a.dw, a.dx, a.dx_f32);
   a.nsplit = p.nsplit;
   a.split_steps = p.split_steps;
-  if (p.tile == 128) run_products<128, 2, 2, 2>(a, s);
-  else run_products<64, 2, 2, 4>(a, s);
+  if (p.tile == 128) run_products<128, 128, 2, 2, 32, 2, 2>(a, s);
+  else run_products<64, 64, 2, 2, 32, 4, 4>(a, s);
   if (a.dw && a.nsplit > 1)
     hipLaunchKernelGGL(router_join_kernel, dim3((unsigned)(((int64_t)a.E * a.H + 1023) / 1024)), dim3(256), 0, s, a);
   return hipGetLastError();
