@@ -24,6 +24,8 @@ __device__ __forceinline__ void balance_run(const BalanceArgs& a, int lo, int hi
   constexpr int E = EPL * 64, AHEAD = EPL > 8 ? 2 : 4;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   float acc[EPL] = {};
+  const int64_t p0 = (int64_t)lo * a.K + threadIdx.x, p1 = (int64_t)hi * a.K;
+  const int e0 = p0 < p1 ? a.topk_idx[p0] : -1;  // (asked for before the scores, which take longer)
   for (int t = lo + wave * AHEAD; t < hi; t += WAVES * AHEAD) {
     float l[AHEAD][EPL];
 #pragma unroll
@@ -42,8 +44,8 @@ __device__ __forceinline__ void balance_run(const BalanceArgs& a, int lo, int hi
       for (int i = 0; i < EPL; ++i) acc[i] = t + k < hi ? __builtin_fmaf(l[k][i], inv, acc[i]) : acc[i];
     }
   }
-  const int64_t p1 = (int64_t)hi * a.K;
-  for (int64_t p = (int64_t)lo * a.K + threadIdx.x; p < p1; p += WAVES * 64) {
+  if ((unsigned)e0 < (unsigned)E) atomicAdd(&hist[e0], 1);
+  for (int64_t p = p0 + WAVES * 64; p < p1; p += WAVES * 64) {
     const int e = a.topk_idx[p];
     if ((unsigned)e < (unsigned)E) atomicAdd(&hist[e], 1);
   }
@@ -114,8 +116,7 @@ __global__ __launch_bounds__(1024) void balance_small_kernel(BalanceArgs a) {
     }
     __syncthreads();
   }
-#pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) part += __shfl_xor(part, m, WAVE);
+  part = wave_sum_f64(part);
   if (lane == 0) parts[wave] = part;
   __syncthreads();
   if (threadIdx.x == 0) {
@@ -133,6 +134,7 @@ __global__ __launch_bounds__(1024) void balance_finish_kernel(BalanceArgs a) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int b = blockIdx.x, e = blockIdx.y * 64 + lane;
   const Seq q = seq_at(a.seq, b);
+  const int N = seq_tokens(a.seq, &tokens);
   double sum = 0;
   int cnt = 0;
   if (q.begin < q.end) {
@@ -157,44 +159,48 @@ __global__ __launch_bounds__(1024) void balance_finish_kernel(BalanceArgs a) {
   sums[wave][lane] = sum;
   cnts[wave][lane] = cnt;
   __syncthreads();
+  const int64_t n = (int64_t)gridDim.x * gridDim.y;
+  const bool alone = n <= 1024;  // parts that one wave adds
   if (wave == 0) {
     for (int w = 1; w < 16; ++w) {
       sum += sums[w][lane];
       cnt += cnts[w][lane];
     }
-    const int n = q.end - q.begin;
-    const double mean = n > 0 ? sum / n : 0.0;
+    const int len = q.end - q.begin;
+    const double mean = len > 0 ? sum / len : 0.0;
     const int64_t at = (int64_t)b * a.E + e;
     a.counts[at] = cnt;
     a.probs[at] = (float)mean;
-    double part = cnt * mean;
-#pragma unroll
-    for (int m = 32; m >= 1; m >>= 1) part += __shfl_xor(part, m, WAVE);
+    const double part = wave_sum_f64(cnt * mean);
+    int is_last = 0;
     if (lane == 0) {
       a.part[(int64_t)b * gridDim.y + blockIdx.y] = part;
       __threadfence();
-      last = atomicAdd(a.done, 1) == (int)(gridDim.x * gridDim.y) - 1;
+      is_last = atomicAdd(a.done, 1) == (int)n - 1;
     }
+    is_last = __builtin_amdgcn_readfirstlane(is_last);
+    if (lane == 0) last = is_last;
+    if (alone && !is_last) return;
+  } else if (alone) {
+    return;
   }
-  __syncthreads();
-  if (!last) return;
+  if (!alone) {
+    __syncthreads();
+    if (!last) return;
+  }
   // the last workgroup: all parts in order, read past the caches that do not see other dies' stores
   __threadfence();
   double total = 0;
-  const int64_t n = (int64_t)gridDim.x * gridDim.y;
-  for (int64_t i = threadIdx.x; i < n; i += 1024)
+  for (int64_t i = threadIdx.x; i < n; i += alone ? 64 : 1024)
     total += __hip_atomic_load(a.part + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-#pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) total += __shfl_xor(total, m, WAVE);
-  const int N = seq_tokens(a.seq, &tokens);
-  __syncthreads();
-  if (lane == 0) sums[0][wave] = total;
-  __syncthreads();
-  if (threadIdx.x == 0) {
+  total = wave_sum_f64(total);
+  if (!alone) {
+    if (lane == 0) sums[0][wave] = total;
+    __syncthreads();
     total = 0;
     for (int w = 0; w < 16; ++w) total += sums[0][w];
-    *a.loss = N > 0 ? (float)((double)a.coef * a.E * total / ((double)a.K * N)) : 0.f;
   }
+  if (threadIdx.x == 0) *a.loss = N > 0 ? (float)((double)a.coef * a.E * total / ((double)a.K * N)) : 0.f;
 }
 
 // ---- fp32 values in 16-bit pieces -------------------------------------------------------------

@@ -110,12 +110,6 @@ __device__ __forceinline__ double chunk_sum(const void* p, int n) {
   return chunk_sum<F32, true>(p, n, any);
 }
 
-__device__ __forceinline__ double wave_sum_f64(double v) {
-#pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m, WAVE);
-  return v;
-}
-
 // what is no image, or one of other sizes, is not followed
 __device__ __forceinline__ bool is_image(const GradArgs& a) {
   const GradHeader* hd = (const GradHeader*)a.image;

@@ -76,6 +76,12 @@ __device__ __forceinline__ float wave_sum_f32(float v) {
   return v;
 }
 
+__device__ __forceinline__ double wave_sum_f64(double v) {
+#pragma unroll
+  for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m, WAVE);
+  return v;
+}
+
 // ---- MXFP8 (OCP MX v1.0, E4M3 elements, one e8m0 scale per 32 values) ----------------
 // Shared-scale byte of a block from its largest magnitude: X = floor(log2 amax) - 8 (8 = the
 // exponent of E4M3's largest normal, 448), clamped to [-127, 127], stored as X + 127; an

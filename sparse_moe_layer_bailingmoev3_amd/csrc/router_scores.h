@@ -94,10 +94,10 @@ __device__ __forceinline__ Seq seq_at(const SeqArgs& q, int b) {
   return r;
 }
 
-// The first sequence whose run ends behind token t (n if none): the ends up to t are counted by the
-// whole workgroup.  `count`: one int in LDS.
+// The first sequence whose run ends behind token t (n if none; 0 where there is but one): the ends up to t
+// are counted by the whole workgroup.  `count`: one int in LDS.
 __device__ __forceinline__ int seq_of(const SeqArgs& q, int t, int* count) {
-  if (!q.offsets) return 0;
+  if (!q.offsets || q.n == 1) return 0;
   if (threadIdx.x == 0) *count = 0;
   __syncthreads();
   int c = 0;
