@@ -239,13 +239,15 @@ __device__ __forceinline__ void bf16_pieces(float v, uint32_t (&p)[3]) {
 template <int EPL, int P>
 struct Pieces {
   uint32_t w[P][(EPL + 1) / 2];
-  __device__ __forceinline__ void store(uint16_t* row, int64_t plane, int lane, int planes = P) const {
+  // where(e): where expert e's value lies in the first plane
+  template <typename At>
+  __device__ __forceinline__ void store(uint16_t* base, int64_t plane, int lane, int planes, At where) const {
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       if (p >= planes) break;
 #pragma unroll
       for (int j = 0; j < Row<EPL>::NJ; ++j) {
-        uint16_t* const at = row + p * plane + Row<EPL>::at(lane, j);
+        uint16_t* const at = base + p * plane + where(Row<EPL>::at(lane, j));
         if constexpr (EPL == 1) *at = (uint16_t)w[p][0];
         else if constexpr (EPL == 2) *(uint32_t*)at = w[p][0];
         else *(u32x2*)at = u32x2{w[p][2 * j], w[p][2 * j + 1]};
@@ -286,8 +288,8 @@ __device__ __forceinline__ void split_weight(const DlogitsArgs& a, int block, ui
     for (int i = 0; i < N / 2; i += 2) *(u32x2*)(lds + col * LD + grp * (N / 2) + i) = u32x2{w[p][i], w[p][i + 1]};
     __syncthreads();
     for (int c = threadIdx.x; c < 16 * (E / 8); c += 256) {
-      const int row = c / (E / 8), at = c % (E / 8);
-      *(u32x4*)(a.wt + ((int64_t)p * a.H + h0 + row) * E + at * 8) = *(const u32x4*)(lds + row * LD + at * 4);
+      const int row = c / 4 % 16, at = c / 64 * 4 + c % 4;  // (in the planes' order: 64 lanes, one block)
+      *(u32x4*)(a.wt + p * plane_size(a.H, E) + plane_at(h0 + row, at * 8, E)) = *(const u32x4*)(lds + row * LD + at * 4);
     }
   }
 }
@@ -409,7 +411,6 @@ __global__ __launch_bounds__(256) void dlogits_kernel(DlogitsArgs a) {
       for (int i = 0; i < EPL; ++i) d[i] += add[i];
     }
     if (a.dlogits) Row<EPL>::store(a.dlogits + t * E, lane, d);
-    const int64_t plane = (int64_t)a.seq.T * E;
     if (a.bf) {
       Pieces<EPL, 3> p;
 #pragma unroll
@@ -420,7 +421,7 @@ __global__ __launch_bounds__(256) void dlogits_kernel(DlogitsArgs a) {
 #pragma unroll
         for (int k = 0; k < 3; ++k) p.w[k][i / 2] = x[k] >> 16 | y[k];
       }
-      p.store(a.bf + t * E, plane, lane);
+      p.store(a.bf, (int64_t)a.seq.T * E, lane, 3, [&](int e) { return t * E + e; });
     }
     if (a.hf) {
       uint32_t top = 0;
@@ -430,7 +431,7 @@ __global__ __launch_bounds__(256) void dlogits_kernel(DlogitsArgs a) {
       Pieces<EPL, 2> p;
 #pragma unroll
       for (int i = 0; i < EPL; i += 2) half_pieces(d[i], i + 1 < EPL ? d[i + 1] : 0.f, ex, p.w[0][i / 2], p.w[1][i / 2]);
-      p.store(a.hf + t * E, plane, lane, 1 + a.pair);
+      p.store(a.hf, plane_size(a.seq.T, E), lane, 1 + a.pair, [&](int e) { return plane_at(t, e, E); });
       if (lane == 0) a.hexp[t] = ex;
     }
   }

@@ -280,6 +280,11 @@ struct BalanceArgs {
 int balance_chunk(int64_t T);
 hipError_t launch_balance(const BalanceArgs& a, hipStream_t s);
 
+// The fp16 planes of dx's operands lie in blocks of 16 rows by 32 experts, 1 KB each, the blocks of 16 rows
+// one behind the other: where row r's value e is, and the values of a plane (rows up to a multiple of 16).
+constexpr int64_t plane_at(int64_t r, int e, int E) { return r / 16 * 16 * E + e / 32 * 512 + r % 16 * 32 + e % 32; }
+constexpr int64_t plane_size(int64_t rows, int E) { return (rows + 15) / 16 * 16 * E; }
+
 struct DlogitsArgs {
   SeqArgs seq;
   int E, K, norm;
@@ -292,16 +297,16 @@ struct DlogitsArgs {
   // the pieces that the products read (each NULL if not wanted), planes one behind the other
   uint16_t* bf;            // bf16 [3, T, E]
   int pair;                // fp16: both pieces (for a result in fp32), or the first alone
-  uint16_t* hf;            // fp16 [1 + pair, T, E], row t times 2^hexp[t]
+  uint16_t* hf;            // fp16, 1 + pair planes of T rows (plane_at), row t times 2^hexp[t]
   int32_t* hexp;           // [T]
   const float* w; int H;   // router_w [E, H], taken apart by the same launch (hf given)
-  uint16_t* wt;            // fp16 [1 + pair, H, E], row h times 2^wexp[h]
+  uint16_t* wt;            // fp16, 1 + pair planes of H rows, row h times 2^wexp[h]
   int32_t* wexp;           // [H]
   int run, weight_blocks;  // tokens of a wave, workgroups that take router_w apart (set by the launch)
 };
 hipError_t launch_dlogits(DlogitsArgs a, hipStream_t s);
 
-constexpr int ROUTER_TILE_MAX = 128;  // largest tile of the products: the exponents' arrays reach to its end
+constexpr int ROUTER_TILE_MAX = 256;  // largest tile of the products: the exponents' arrays reach to its end
 struct RouterGradPlan {
   int tile;                  // square tiles: 128 or 64
   int nsplit, split_steps;   // d router_w: parts of the reduction over tokens, steps of 32 in each
@@ -314,8 +319,8 @@ struct RouterGradArgs {
   float* dw; int acc_w;      // or NULL
   float* part;               // [nsplit, E, H], with nsplit > 1
   int nsplit, split_steps;   // set by the launch
-  const uint16_t* dh; const int32_t* dexp;  // fp16 [1 or 2, T, E]
-  const uint16_t* wt; const int32_t* wexp;  // fp16 [1 or 2, H, E]
+  const uint16_t* dh; const int32_t* dexp;  // fp16, planes of T rows
+  const uint16_t* wt; const int32_t* wexp;  // fp16, planes of H rows
   void* dx; int dx_f32, acc_x;  // or NULL
 };
 hipError_t launch_router_grad(RouterGradArgs a, hipStream_t s);

@@ -62,8 +62,8 @@ Layout layout(const moe_config_t* c, int64_t T, int n_seq) {
       parts = std::max(parts, n > 1 ? n : 0);
     }
   L.bf = take((size_t)T * E * 6);
-  L.hf = take((size_t)T * E * 4);
-  L.wt = take(H * E * 4);
+  L.hf = take(2 * (size_t)moe::plane_size(T, (int)E) * 2);
+  L.wt = take(2 * (size_t)moe::plane_size(H, (int)E) * 2);
   L.hexp = take((T + end) * 4);
   L.wexp = take((H + end) * 4);
   L.part = take(parts * E * H * 4);

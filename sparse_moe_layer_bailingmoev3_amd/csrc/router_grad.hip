@@ -60,7 +60,7 @@ __device__ __forceinline__ int swz_row(int row) { return KS == 16 ? (row >> 4) &
 template <int W>
 __device__ __forceinline__ int swz_cols(int row) { return W >= 128 ? (row & 3) << 2 : (row & 2) << 1; }
 
-template <int OP, int BR, int BC, int WR, int WC, int KS, int NST, bool F32>
+template <int OP, int BR, int BC, int WR, int WC, int KS, int NST, bool F32, bool AHEAD>
 __device__ __forceinline__ void router_tile(const RouterGradArgs& a, int block, int blocks, uint8_t* lds) {
   typedef Stage<OP, BR, BC, KS, F32> St;
   constexpr int NW = WR * WC, PX = St::PX, PY = St::PY;
@@ -93,12 +93,14 @@ __device__ __forceinline__ void router_tile(const RouterGradArgs& a, int block, 
   uint32_t xo[XN], yo[YN], xstep, ystep;
   int xrow[XN], yrow[YN];  // reduction row of the loads (d router_w: masked in the last step)
   if constexpr (OP == OP_DX) {
-    each<PX>([&](auto p) { xb[p] = (uint64_t)(a.dh + ((int64_t)p * a.T + r0) * a.E); });
-    each<PY>([&](auto p) { yb[p] = (uint64_t)(a.wt + ((int64_t)p * a.H + c0) * a.E); });
-    xstep = ystep = KS * 2;
+    // planes in blocks of 16 rows by 32 values (plane_block): a load is one block
+    static_assert(KS == 32, "a step is one block");
+    each<PX>([&](auto p) { xb[p] = (uint64_t)(a.dh + p * plane_size(a.T, a.E) + (int64_t)r0 * a.E); });
+    each<PY>([&](auto p) { yb[p] = (uint64_t)(a.wt + p * plane_size(a.H, a.E) + (int64_t)c0 * a.E); });
+    xstep = ystep = 1024;
     auto offset = [&](int load, int rows) {
-      const int row = load * (64 / KC) + lane / KC;
-      return row < rows ? (uint32_t)(row * a.E * 2 + (((lane % KC) ^ swz_row<KS>(row)) << 4)) : BUF_OUT;
+      const int row = lane / 4;
+      return load * 16 + row < rows ? (uint32_t)(load * 16 * a.E * 2 + row * 64 + (((lane & 3) ^ swz_row<KS>(row)) << 4)) : BUF_OUT;
     };
     each<XN>([&](auto i) { xo[i] = offset(wave * XN + i, a.T - r0); });
     each<YN>([&](auto i) { yo[i] = offset(wave * YN + i, a.H - c0); });
@@ -120,25 +122,29 @@ __device__ __forceinline__ void router_tile(const RouterGradArgs& a, int block, 
   const uint32_t lds0 = lds_offset(lds);
   int left = red;  // reduction values from the next step to load on
   uint32_t lst = lds0;
-  auto issue = [&]() {
+  // load i of a step, into the stage at `lst`; past the end it brings zeros
+  auto load = [&](auto i) {
+    constexpr int I = decltype(i)::value;
     const uint32_t st = __builtin_amdgcn_readfirstlane(lst);
-    const bool whole = OP == OP_DX || left >= KS;
-    each<PX>([&](auto p) {
-      const u32x4 rs = buffer_at(xb[p]);
-      each<XN>([&](auto i) {
-        dma16(whole || xrow[i] < left ? xo[i] : BUF_OUT, rs, st + p * X_BYTES + (wave * XN + i) * 1024);
-      });
-      xb[p] += xstep;
-    });
-    each<PY>([&](auto p) {
-      const u32x4 rs = buffer_at(yb[p]);
-      each<YN>([&](auto i) {
-        dma16(whole || yrow[i] < left ? yo[i] : BUF_OUT, rs, st + PX * X_BYTES + p * Y_BYTES + (wave * YN + i) * 1024);
-      });
-      yb[p] += ystep;
-    });
+    if constexpr (I < PX * XN) {
+      constexpr int p = I / XN, k = I % XN;
+      const bool ok = OP == OP_DX ? left > 0 : xrow[k] < left;
+      dma16(ok ? xo[k] : BUF_OUT, buffer_at(xb[p]), st + p * X_BYTES + (wave * XN + k) * 1024);
+    } else {
+      constexpr int p = (I - PX * XN) / YN, k = (I - PX * XN) % YN;
+      const bool ok = OP == OP_DX ? left > 0 : yrow[k] < left;
+      dma16(ok ? yo[k] : BUF_OUT, buffer_at(yb[p]), st + PX * X_BYTES + p * Y_BYTES + (wave * YN + k) * 1024);
+    }
+  };
+  auto next_load = [&]() {
+    each<PX>([&](auto p) { xb[p] += xstep; });
+    each<PY>([&](auto p) { yb[p] += ystep; });
     left -= KS;
     lst = lst == lds0 + (NST - 1) * ST_BYTES ? lds0 : lst + ST_BYTES;
+  };
+  auto issue = [&]() {
+    each<LN>(load);
+    next_load();
   };
 
   // ---- LDS read addresses.  Transposed: lanes 16g .. 16g+15 read rows 8 (g/2) .. of column block g%2.
@@ -178,45 +184,96 @@ __device__ __forceinline__ void router_tile(const RouterGradArgs& a, int block, 
 #pragma unroll
         for (int i = 0; i < 16; ++i) acc[n][c][r][i] = 0.f;
 
-  auto compute = [&](const uint8_t* st) {
-#pragma unroll
-    for (int u = 0; u < KS / 16; ++u) {
-      u32x4 yf[PY][CJ];
-#pragma unroll
-      for (int p = 0; p < PY; ++p)
-#pragma unroll
-        for (int c = 0; c < CJ; ++c) yf[p][c] = frag(st + p * Y_BYTES, ya, c, u, BC * 2);
-#pragma unroll
-      for (int r = 0; r < RJ; ++r) {
-        u32x4 xf[PX];
-#pragma unroll
-        for (int p = 0; p < PX; ++p) xf[p] = frag(st + p * X_BYTES, xa, r, u, BR * 2);
-        // small terms first
-#pragma unroll
-        for (int p = PX + PY - 2; p >= 0; --p)
-#pragma unroll
-          for (int c = 0; c < CJ; ++c) {
-            floatx16& s = acc[(u * (PX + PY - 1) + p) % NA][c][r];
-            if constexpr (OP == OP_DW) s = mfma32<OP>(yf[0][c], xf[p], s);
-            else s = mfma32<OP>(yf[p == 2 ? PY - 1 : 0][c], xf[p == 2 ? 0 : p], s);
-          }
-      }
-    }
+  // fragment i of a substep: the rows' planes first, then the columns'
+  constexpr int NF = PX * RJ + PY * CJ, NP = PX + PY - 1;  // fragments, products
+  auto read = [&](const uint8_t* st, int u, auto i) {
+    constexpr int I = decltype(i)::value;
+    if constexpr (I < PX * RJ) return frag(st + (I / RJ) * X_BYTES, xa, I % RJ, u, BR * 2);
+    else return frag(st + ((I - PX * RJ) / CJ) * Y_BYTES, ya, (I - PX * RJ) % CJ, u, BC * 2);
+  };
+  // product p of the tile (c, r): small terms are the higher ones
+  auto multiply = [&](const u32x4 (&f)[NF], int n, auto c, auto r, auto p) {
+    constexpr int P = decltype(p)::value, R = decltype(r)::value, C = decltype(c)::value;
+    constexpr int x = OP == OP_DW ? P : P == 2 ? 0 : P, y = OP == OP_DX && P == 2 ? 1 : 0;
+    floatx16& s = acc[(n * NP + P) % NA][C][R];
+    s = mfma32<OP>(f[PX * RJ + y * CJ + C], f[x * RJ + R], s);
   };
 
-  // ---- steps: wait for this stage's loads (those of later stages stay in flight), meet the other
-  // waves, refill the stage that all have left, multiply
+  if constexpr (AHEAD) {
+    // ---- one wave on each matrix unit: nothing but its own instructions can fill its waits, so the
+    // fragments of the next step are read, and the loads of a later one started, between the products
+    // of this one, one instruction in the shadow of a few products.  The stage whose fragments are in
+    // registers is the one to refill.
+    static_assert(KS == 16 && NA == 1, "one substep");
 #pragma unroll
-  for (int j = 0; j < NST - 1; ++j)
-    if (j < nsteps) issue();
-  int stage = 0;
-  for (int s = 0; s < nsteps; ++s) {
-    if (nsteps - 1 - s >= NST - 2) wait_vmcnt<(NST - 2) * LN>();
-    else wait_vmcnt<0>();
+    for (int j = 0; j < NST; ++j) issue();
+    wait_vmcnt<(NST - 1) * LN>();
     lds_barrier();
-    if (s + NST - 1 < nsteps) issue();
-    compute(lds + stage);
-    stage = stage == (NST - 1) * ST_BYTES ? 0 : stage + ST_BYTES;
+    u32x4 f0[NF], f1[NF];
+    each<NF>([&](auto i) { f0[i] = read(lds, 0, i); });
+    int stage = ST_BYTES;  // of the next step
+    auto step = [&](const u32x4 (&now)[NF], u32x4 (&then)[NF]) {
+      wait_vmcnt<(NST - 2) * LN>();
+      lds_barrier();
+      const uint8_t* const st = lds + stage;
+      constexpr int M = CJ * NP * RJ, SLOTS = (M + 2) / 3, EARLY = (NF + 1) / 2;
+      each<SLOTS>([&](auto slot) {
+        each<3>([&](auto k) {
+          constexpr int I = decltype(slot)::value * 3 + decltype(k)::value;
+          if constexpr (I < M) {
+            constexpr int c = I / (NP * RJ), p = NP - 1 - I / RJ % NP, r = I % RJ;
+            multiply(now, 0, std::integral_constant<int, c>{}, std::integral_constant<int, r>{}, std::integral_constant<int, p>{});
+          }
+        });
+        constexpr int S = decltype(slot)::value;
+        if constexpr (S < EARLY) {  // two fragments a slot, then the loads
+          then[2 * S] = read(st, 0, std::integral_constant<int, 2 * S>{});
+          if constexpr (2 * S + 1 < NF) then[2 * S + 1] = read(st, 0, std::integral_constant<int, 2 * S + 1>{});
+        } else {
+          constexpr int PER = (LN + SLOTS - EARLY - 1) / (SLOTS - EARLY), L0 = (S - EARLY) * PER;
+          each<PER>([&](auto k) {
+            if constexpr (L0 + decltype(k)::value < LN) load(std::integral_constant<int, L0 + decltype(k)::value>{});
+          });
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      });
+      next_load();
+      stage = stage == (NST - 1) * ST_BYTES ? 0 : stage + ST_BYTES;
+    };
+    int s = 0;
+    for (; s + 1 < nsteps; s += 2) {
+      step(f0, f1);
+      step(f1, f0);
+    }
+    if (s < nsteps) step(f0, f1);
+    wait_vmcnt<0>();  // no direct-to-LDS load may outlive the workgroup
+  } else {
+    auto compute = [&](const uint8_t* st) {
+#pragma unroll
+      for (int u = 0; u < KS / 16; ++u) {
+        u32x4 f[NF];
+        each<NF>([&](auto i) { f[i] = read(st, u, i); });
+        each<RJ>([&](auto r) {
+          each<NP>([&](auto k) {
+            each<CJ>([&](auto c) { multiply(f, u, c, r, std::integral_constant<int, NP - 1 - decltype(k)::value>{}); });
+          });
+        });
+      }
+    };
+    // ---- steps: wait for this stage's loads (those of later stages stay in flight), meet the other
+    // waves, refill the stage that all have left, multiply
+#pragma unroll
+    for (int j = 0; j < NST - 1; ++j)
+      if (j < nsteps) issue();
+    int stage = 0;
+    for (int s = 0; s < nsteps; ++s) {
+      if (nsteps - 1 - s >= NST - 2) wait_vmcnt<(NST - 2) * LN>();
+      else wait_vmcnt<0>();
+      lds_barrier();
+      if (s + NST - 1 < nsteps) issue();
+      compute(lds + stage);
+      stage = stage == (NST - 1) * ST_BYTES ? 0 : stage + ST_BYTES;
+    }
   }
 
   // ---- result: four pieces of four columns a lane, turned within quads of lanes: 4 lanes of both half
@@ -224,15 +281,38 @@ __device__ __forceinline__ void router_tile(const RouterGradArgs& a, int block, 
   const int rows = OP == OP_DW ? a.E : a.T;
   float* const o32 = OP == OP_DX ? (float*)a.dx : a.nsplit > 1 ? a.part + (int64_t)split * a.E * a.H : a.dw;
   const bool add = OP == OP_DX ? a.acc_x : a.acc_w && a.nsplit == 1;
-  const int row0 = r0 + wr * RJ * 32 + (r32 & 28);
-#pragma unroll
-  for (int c = 0; c < CJ; ++c) {
-    const int col = c0 + (wc * CJ + c) * 32 + 8 * (r32 & 3) + 4 * half;
-    int4 ec{0, 0, 0, 0};
-    if constexpr (OP == OP_DX) ec = *(const int4*)(a.wexp + col);  // (the exponents' arrays reach to the end of the last tile)
+  const int row0 = r0 + wr * RJ * 32 + (r32 & 28), col0 = c0 + wc * CJ * 32 + 8 * (r32 & 3) + 4 * half;
+  // everything that the tile's end reads is asked for at once, or, the old values, a column of fragments
+  // ahead of their use: one after another, each would wait for itself
+  int er[RJ][4] = {}, ec[CJ][4] = {};
+  if constexpr (OP == OP_DX) {  // (the exponents' arrays reach to the end of the last tile)
 #pragma unroll
     for (int r = 0; r < RJ; ++r) {
-      floatx4 v[4], old[4];
+      const int4 e = *(const int4*)(a.dexp + row0 + r * 32);
+      er[r][0] = e.x, er[r][1] = e.y, er[r][2] = e.z, er[r][3] = e.w;
+    }
+#pragma unroll
+    for (int c = 0; c < CJ; ++c) {
+      const int4 e = *(const int4*)(a.wexp + col0 + c * 32);
+      ec[c][0] = e.x, ec[c][1] = e.y, ec[c][2] = e.z, ec[c][3] = e.w;
+    }
+  }
+  auto load_old = [&](auto c, floatx4 (&old)[RJ][4]) {
+    if (!(F32 && add)) return;
+    const int col = col0 + c * 32;
+#pragma unroll
+    for (int r = 0; r < RJ; ++r)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int row = row0 + r * 32 + j;
+        old[r][j] = *(const floatx4*)(o32 + (row < rows && col < a.H ? (int64_t)row * a.H + col : 0));
+      }
+  };
+  auto finish = [&](auto c, const floatx4 (&old)[RJ][4]) {
+    const int col = col0 + c * 32;
+#pragma unroll
+    for (int r = 0; r < RJ; ++r) {
+      floatx4 v[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -241,29 +321,29 @@ __device__ __forceinline__ void router_tile(const RouterGradArgs& a, int block, 
           if constexpr (NA == 2) v[j][i] += acc[NA - 1][c][r][4 * j + i];
         }
       quad_transpose(v);
-      int4 er{0, 0, 0, 0};
-      if constexpr (OP == OP_DX) er = *(const int4*)(a.dexp + row0 + r * 32);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int row = row0 + r * 32 + j;
-        if (F32 && add) old[j] = *(const floatx4*)(o32 + (row < rows && col < a.H ? (int64_t)row * a.H + col : 0));
-        if constexpr (OP == OP_DX) {
-          const int e = j == 0 ? er.x : j == 1 ? er.y : j == 2 ? er.z : er.w;
-          v[j] = floatx4{__builtin_amdgcn_ldexpf(v[j][0], -(e + ec.x)), __builtin_amdgcn_ldexpf(v[j][1], -(e + ec.y)),
-                         __builtin_amdgcn_ldexpf(v[j][2], -(e + ec.z)), __builtin_amdgcn_ldexpf(v[j][3], -(e + ec.w))};
-        }
-      }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int row = row0 + r * 32 + j;
         if (row >= rows || col >= a.H) continue;
         const int64_t at = (int64_t)row * a.H + col;
-        if (F32 && add) v[j] += old[j];
+        if constexpr (OP == OP_DX) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[j][i] = __builtin_amdgcn_ldexpf(v[j][i], -(er[r][j] + ec[c][i]));
+        }
+        if (F32 && add) v[j] += old[r][j];
         if constexpr (F32) *(floatx4*)(o32 + at) = v[j];
         else *(u32x2*)((uint16_t*)a.dx + at) = u32x2{f32x2_to_bf16x2(v[j][0], v[j][1]), f32x2_to_bf16x2(v[j][2], v[j][3])};
       }
     }
-  }
+  };
+  floatx4 old0[RJ][4], old1[RJ][4];
+  load_old(std::integral_constant<int, 0>{}, old0);
+  each<CJ>([&](auto c) {
+    constexpr int C = decltype(c)::value;
+    auto& now = C % 2 ? old1 : old0;
+    if constexpr (C + 1 < CJ) load_old(std::integral_constant<int, C + 1>{}, C % 2 ? old0 : old1);
+    finish(c, now);
+  });
 }
 
 // d router_w = (d router_w +) the splits' parts in order
@@ -278,24 +358,24 @@ __global__ __launch_bounds__(256) void router_join_kernel(RouterGradArgs a) {
   *(floatx4*)(a.dw + i) = v + s;
 }
 
-template <int BR, int BC, int WR, int WC, int KS, int NW, int NX, bool F32>
-__global__ __launch_bounds__(WR* WC * 64, 2) void router_products_kernel(RouterGradArgs a, int dw_blocks) {
+template <int BR, int BC, int WR, int WC, int KS, int NW, int NX, bool F32, bool AHEAD>
+__global__ __launch_bounds__(WR* WC * 64, AHEAD ? 1 : 2) void router_products_kernel(RouterGradArgs a, int dw_blocks) {
   constexpr int DW = NW * Stage<OP_DW, BR, BC, KS, true>::BYTES, DX = NX * Stage<OP_DX, BR, BC, KS, F32>::BYTES;
   __shared__ __align__(16) uint8_t lds[DW > DX ? DW : DX];
   const int block = blockIdx.x;
-  if (block < dw_blocks) router_tile<OP_DW, BR, BC, WR, WC, KS, NW, true>(a, block, dw_blocks, lds);
-  else router_tile<OP_DX, BR, BC, WR, WC, KS, NX, F32>(a, block - dw_blocks, (int)gridDim.x - dw_blocks, lds);
+  if (block < dw_blocks) router_tile<OP_DW, BR, BC, WR, WC, KS, NW, true, AHEAD>(a, block, dw_blocks, lds);
+  else router_tile<OP_DX, BR, BC, WR, WC, KS, NX, F32, AHEAD>(a, block - dw_blocks, (int)gridDim.x - dw_blocks, lds);
 }
 
-template <int BR, int BC, int WR, int WC, int KS, int NW, int NX>
+template <int BR, int BC, int WR, int WC, int KS, int NW, int NX, bool AHEAD>
 void run_products(const RouterGradArgs& a, hipStream_t s) {
   auto blocks = [&](int64_t rows, int n) { return (int)(((rows + BR - 1) / BR * ((a.H + BC - 1) / BC) * n + 7) / 8 * 8); };
   const int dw = a.dw ? blocks(a.E, a.nsplit) : 0, dx = a.dx && a.T > 0 ? blocks(a.T, 1) : 0;
   if (dw + dx == 0) return;
   if (a.dx_f32)
-    hipLaunchKernelGGL((router_products_kernel<BR, BC, WR, WC, KS, NW, NX, true>), dim3((unsigned)(dw + dx)), dim3(WR * WC * 64), 0, s, a, dw);
+    hipLaunchKernelGGL((router_products_kernel<BR, BC, WR, WC, KS, NW, NX, true, AHEAD>), dim3((unsigned)(dw + dx)), dim3(WR * WC * 64), 0, s, a, dw);
   else
-    hipLaunchKernelGGL((router_products_kernel<BR, BC, WR, WC, KS, NW, NX, false>), dim3((unsigned)(dw + dx)), dim3(WR * WC * 64), 0, s, a, dw);
+    hipLaunchKernelGGL((router_products_kernel<BR, BC, WR, WC, KS, NW, NX, false, AHEAD>), dim3((unsigned)(dw + dx)), dim3(WR * WC * 64), 0, s, a, dw);
 }
 
 }  // namespace
@@ -340,8 +420,8 @@ hipError_t launch_router_grad(RouterGradArgs a, hipStream_t s) {
   const RouterGradPlan p = router_grad_plan(a.T, a.E, a.H, a.dw, a.dx, a.dx_f32);
   a.nsplit = p.nsplit;
   a.split_steps = p.split_steps;
-  if (p.tile == 128) run_products<128, 128, 2, 2, 32, 2, 2>(a, s);
-  else run_products<64, 64, 2, 2, 32, 4, 4>(a, s);
+  if (p.tile == 128) run_products<128, 128, 2, 2, 32, 2, 2, false>(a, s);
+  else run_products<64, 64, 2, 2, 32, 4, 4, false>(a, s);
   if (a.dw && a.nsplit > 1)
     hipLaunchKernelGGL(router_join_kernel, dim3((unsigned)(((int64_t)a.E * a.H + 1023) / 1024)), dim3(256), 0, s, a);
   return hipGetLastError();
