@@ -288,7 +288,7 @@ __device__ __forceinline__ void split_weight(const DlogitsArgs& a, int block, ui
     for (int i = 0; i < N / 2; i += 2) *(u32x2*)(lds + col * LD + grp * (N / 2) + i) = u32x2{w[p][i], w[p][i + 1]};
     __syncthreads();
     for (int c = threadIdx.x; c < 16 * (E / 8); c += 256) {
-      const int row = c / 4 % 16, at = c / 64 * 4 + c % 4;  // (in the planes' order: 64 lanes, one block)
+      const int row = c / 2 % 16, at = c / 32 * 2 + c % 2;  // (in the planes' order: 32 lanes, half a block)
       *(u32x4*)(a.wt + p * plane_size(a.H, E) + plane_at(h0 + row, at * 8, E)) = *(const u32x4*)(lds + row * LD + at * 4);
     }
   }

@@ -280,10 +280,10 @@ struct BalanceArgs {
 int balance_chunk(int64_t T);
 hipError_t launch_balance(const BalanceArgs& a, hipStream_t s);
 
-// The fp16 planes of dx's operands lie in blocks of 16 rows by 32 experts, 1 KB each, the blocks of 16 rows
-// one behind the other: where row r's value e is, and the values of a plane (rows up to a multiple of 16).
-constexpr int64_t plane_at(int64_t r, int e, int E) { return r / 16 * 16 * E + e / 32 * 512 + r % 16 * 32 + e % 32; }
-constexpr int64_t plane_size(int64_t rows, int E) { return (rows + 15) / 16 * 16 * E; }
+// The fp16 planes of dx's operands lie in blocks of 32 rows by 16 experts, 1 KB each, the blocks of 32 rows
+// one behind the other: where row r's value e is, and the values of a plane (rows up to a multiple of 32).
+constexpr int64_t plane_at(int64_t r, int e, int E) { return r / 32 * 32 * E + e / 16 * 512 + r % 32 * 16 + e % 16; }
+constexpr int64_t plane_size(int64_t rows, int E) { return (rows + 31) / 32 * 32 * E; }
 
 struct DlogitsArgs {
   SeqArgs seq;
@@ -306,7 +306,7 @@ struct DlogitsArgs {
 };
 hipError_t launch_dlogits(DlogitsArgs a, hipStream_t s);
 
-constexpr int ROUTER_TILE_MAX = 256;  // largest tile of the products: the exponents' arrays reach to its end
+constexpr int ROUTER_TILE_MAX = 128;  // largest tile of the products: the exponents' arrays reach to its end
 struct RouterGradPlan {
   int tile;                  // square tiles: 128 or 64
   int nsplit, split_steps;   // d router_w: parts of the reduction over tokens, steps of 32 in each

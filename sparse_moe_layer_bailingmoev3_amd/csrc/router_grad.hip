@@ -22,6 +22,18 @@
 // instruction.  dx's planes run along the reduction and are read as they lie; d router_w's run across it
 // and are read through the transposing LDS load.  Rows past the end are offsets past a buffer
 // descriptor's end: zeros.
+//
+// What bounds it, on one MI355X: 8192 tokens of 512 x 2560, dx added to in fp32, 121 us alone and up to 150
+// back to back (the card's power then holds its clock down): 129 GFLOP of products, 1.06 to 0.86 PFLOP/s (the
+// library's bf16 product reaches 1.31 in short runs), matrix units busy 48 % of the cycles; LDS reads of a
+// step (16 KB a wave for 24 products of 32 x 32 x 16) and what the loads write there take about as long as the
+// products, no bank conflicts.  d router_w alone 48 us (6400 tokens), dx alone 54 in fp32, 26 in bf16.
+// Measured and not kept: 256 x 256 tiles, as 16 waves of 64 x 64 or 4 waves of 128 x 128 that read the next
+// fragments between the products (1.5 PFLOP/s within a tile, but 480 long items on 256 places end unevenly:
+// 157 against 158 us a call), 256 x 128, steps of 16; dx's planes in rows of E values instead of blocks
+// (dx alone 90 against 54 us: a load of 16 or 32 rows touched as many cache lines by halves or quarters);
+// the tiles of both products mixed, or dx's first (+15 to +40 %); two rounded bf16 pieces of dl (-20 us, see
+// above).
 #include "moe_common.h"
 #include "moe_internal.h"
 #include "tile_ops.h"
@@ -51,16 +63,15 @@ struct Stage {
   static constexpr int X_BYTES = BR * KS * 2, Y_BYTES = BC * KS * 2, BYTES = PX * X_BYTES + PY * Y_BYTES;
 };
 
-// 16-byte chunk swizzles.  Rows of KS reduction values (2 or 4 chunks): the 16-byte LDS read serves lanes
-// 0-3, 12-15, 20-23, 24-27 of each half wave together, then the others.
-template <int KS>
-__device__ __forceinline__ int swz_row(int row) { return KS == 16 ? (row >> 4) & 1 : (row >> 2) & 3; }
+// 16-byte chunk swizzles.  Rows of 16 reduction values (2 chunks): the 16-byte LDS read serves lanes 0-3,
+// 12-15, 20-23, 24-27 of each half wave together, then the others.
+__device__ __forceinline__ int swz_row(int row) { return (row >> 4) & 1; }
 // Rows of W output values under the transposing read, which touches rows r..r+3 and two blocks of 32 bytes
 // in each half wave.
 template <int W>
 __device__ __forceinline__ int swz_cols(int row) { return W >= 128 ? (row & 3) << 2 : (row & 2) << 1; }
 
-template <int OP, int BR, int BC, int WR, int WC, int KS, int NST, bool F32, bool AHEAD>
+template <int OP, int BR, int BC, int WR, int WC, int KS, int NST, bool F32>
 __device__ __forceinline__ void router_tile(const RouterGradArgs& a, int block, int blocks, uint8_t* lds) {
   typedef Stage<OP, BR, BC, KS, F32> St;
   constexpr int NW = WR * WC, PX = St::PX, PY = St::PY;
@@ -68,8 +79,7 @@ __device__ __forceinline__ void router_tile(const RouterGradArgs& a, int block, 
   constexpr int XN = X_BYTES / (NW * 1024), YN = Y_BYTES / (NW * 1024), LN = PX * XN + PY * YN;  // loads per wave
   static_assert(XN * NW * 1024 == X_BYTES && YN * NW * 1024 == Y_BYTES, "a plane must split evenly over the waves");
   constexpr int RJ = BR / WR / 32, CJ = BC / WC / 32;
-  constexpr int KC = KS / 8;                 // chunks of a row of reduction values
-  constexpr int NA = RJ * CJ == 1 ? 2 : 1;   // sums that take turns (one alone would wait for itself)
+    constexpr int NA = RJ * CJ == 1 ? 2 : 1;   // sums that take turns (one alone would wait for itself)
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -93,17 +103,16 @@ __device__ __forceinline__ void router_tile(const RouterGradArgs& a, int block, 
   uint32_t xo[XN], yo[YN], xstep, ystep;
   int xrow[XN], yrow[YN];  // reduction row of the loads (d router_w: masked in the last step)
   if constexpr (OP == OP_DX) {
-    // planes in blocks of 16 rows by 32 values (plane_block): a load is one block
-    static_assert(KS == 32, "a step is one block");
+    // planes in blocks of 32 rows by 16 values (plane_at): a load is one block
     each<PX>([&](auto p) { xb[p] = (uint64_t)(a.dh + p * plane_size(a.T, a.E) + (int64_t)r0 * a.E); });
     each<PY>([&](auto p) { yb[p] = (uint64_t)(a.wt + p * plane_size(a.H, a.E) + (int64_t)c0 * a.E); });
-    xstep = ystep = 1024;
-    auto offset = [&](int load, int rows) {
-      const int row = lane / 4;
-      return load * 16 + row < rows ? (uint32_t)(load * 16 * a.E * 2 + row * 64 + (((lane & 3) ^ swz_row<KS>(row)) << 4)) : BUF_OUT;
+    xstep = ystep = KS * 64;
+    auto offset = [&](int load, int blocks, int rows) {
+      const int u = load / blocks, r = load % blocks * 32, row = lane / 2;
+      return r + row < rows ? (uint32_t)(r * a.E * 2 + u * 1024 + row * 32 + (((lane & 1) ^ swz_row(row)) << 4)) : BUF_OUT;
     };
-    each<XN>([&](auto i) { xo[i] = offset(wave * XN + i, a.T - r0); });
-    each<YN>([&](auto i) { yo[i] = offset(wave * YN + i, a.H - c0); });
+    each<XN>([&](auto i) { xo[i] = offset(wave * XN + i, BR / 32, a.T - r0); });
+    each<YN>([&](auto i) { yo[i] = offset(wave * YN + i, BC / 32, a.H - c0); });
   } else {
     constexpr int XL = BR / 8, YL = BC / 8;
     each<PX>([&](auto p) { xb[p] = (uint64_t)(a.dl + ((int64_t)p * a.T + red0) * a.E + r0); });
@@ -122,33 +131,29 @@ __device__ __forceinline__ void router_tile(const RouterGradArgs& a, int block, 
   const uint32_t lds0 = lds_offset(lds);
   int left = red;  // reduction values from the next step to load on
   uint32_t lst = lds0;
-  // load i of a step, into the stage at `lst`; past the end it brings zeros
-  auto load = [&](auto i) {
-    constexpr int I = decltype(i)::value;
+  auto issue = [&]() {
     const uint32_t st = __builtin_amdgcn_readfirstlane(lst);
-    if constexpr (I < PX * XN) {
-      constexpr int p = I / XN, k = I % XN;
-      const bool ok = OP == OP_DX ? left > 0 : xrow[k] < left;
-      dma16(ok ? xo[k] : BUF_OUT, buffer_at(xb[p]), st + p * X_BYTES + (wave * XN + k) * 1024);
-    } else {
-      constexpr int p = (I - PX * XN) / YN, k = (I - PX * XN) % YN;
-      const bool ok = OP == OP_DX ? left > 0 : yrow[k] < left;
-      dma16(ok ? yo[k] : BUF_OUT, buffer_at(yb[p]), st + PX * X_BYTES + p * Y_BYTES + (wave * YN + k) * 1024);
-    }
-  };
-  auto next_load = [&]() {
-    each<PX>([&](auto p) { xb[p] += xstep; });
-    each<PY>([&](auto p) { yb[p] += ystep; });
+    const bool whole = OP == OP_DX || left >= KS;
+    each<PX>([&](auto p) {
+      const u32x4 rs = buffer_at(xb[p]);
+      each<XN>([&](auto i) {
+        dma16(whole || xrow[i] < left ? xo[i] : BUF_OUT, rs, st + p * X_BYTES + (wave * XN + i) * 1024);
+      });
+      xb[p] += xstep;
+    });
+    each<PY>([&](auto p) {
+      const u32x4 rs = buffer_at(yb[p]);
+      each<YN>([&](auto i) {
+        dma16(whole || yrow[i] < left ? yo[i] : BUF_OUT, rs, st + PX * X_BYTES + p * Y_BYTES + (wave * YN + i) * 1024);
+      });
+      yb[p] += ystep;
+    });
     left -= KS;
     lst = lst == lds0 + (NST - 1) * ST_BYTES ? lds0 : lst + ST_BYTES;
   };
-  auto issue = [&]() {
-    each<LN>(load);
-    next_load();
-  };
 
   // ---- LDS read addresses.  Transposed: lanes 16g .. 16g+15 read rows 8 (g/2) .. of column block g%2.
-  int xa[OP == OP_DW ? RJ : KS / 16], ya[OP == OP_DW ? CJ : KS / 16];
+  int xa[OP == OP_DW ? RJ : 1], ya[OP == OP_DW ? CJ : 1];
   if constexpr (OP == OP_DW) {
     const int row = 8 * half + ((lane & 15) >> 2), block16 = (lane >> 4) & 1, in = (lane & 3) * 8;
 #pragma unroll
@@ -158,11 +163,9 @@ __device__ __forceinline__ void router_tile(const RouterGradArgs& a, int block, 
     for (int j = 0; j < CJ; ++j)
       ya[j] = PX * X_BYTES + row * BC * 2 + ((((wc * CJ + j) * 4 + block16 * 2) ^ swz_cols<BC>(row)) << 4) + in;
   } else {
-#pragma unroll
-    for (int u = 0; u < KS / 16; ++u) {
-      xa[u] = (wr * RJ * 32 + r32) * KS * 2 + (((2 * u + half) ^ swz_row<KS>(r32)) << 4);
-      ya[u] = PX * X_BYTES + (wc * CJ * 32 + r32) * KS * 2 + (((2 * u + half) ^ swz_row<KS>(r32)) << 4);
-    }
+    const int in = r32 * 32 + ((half ^ swz_row(r32)) << 4);
+    xa[0] = wr * RJ * 1024 + in;
+    ya[0] = PX * X_BYTES + wc * CJ * 1024 + in;
   }
   auto frag = [&](const uint8_t* st, const int* at, int j, int u, int row_bytes) {
     if constexpr (OP == OP_DW) {
@@ -170,7 +173,7 @@ __device__ __forceinline__ void router_tile(const RouterGradArgs& a, int block, 
       const u32x2 lo = lds_read_tr(p), hi = lds_read_tr(p + 4 * row_bytes);
       return u32x4{lo[0], lo[1], hi[0], hi[1]};
     } else {
-      return *(const u32x4*)(st + at[u] + j * 32 * KS * 2);
+      return *(const u32x4*)(st + at[0] + u * 16 * row_bytes + j * 1024);
     }
   };
 
@@ -184,96 +187,45 @@ __device__ __forceinline__ void router_tile(const RouterGradArgs& a, int block, 
 #pragma unroll
         for (int i = 0; i < 16; ++i) acc[n][c][r][i] = 0.f;
 
-  // fragment i of a substep: the rows' planes first, then the columns'
-  constexpr int NF = PX * RJ + PY * CJ, NP = PX + PY - 1;  // fragments, products
-  auto read = [&](const uint8_t* st, int u, auto i) {
-    constexpr int I = decltype(i)::value;
-    if constexpr (I < PX * RJ) return frag(st + (I / RJ) * X_BYTES, xa, I % RJ, u, BR * 2);
-    else return frag(st + ((I - PX * RJ) / CJ) * Y_BYTES, ya, (I - PX * RJ) % CJ, u, BC * 2);
-  };
-  // product p of the tile (c, r): small terms are the higher ones
-  auto multiply = [&](const u32x4 (&f)[NF], int n, auto c, auto r, auto p) {
-    constexpr int P = decltype(p)::value, R = decltype(r)::value, C = decltype(c)::value;
-    constexpr int x = OP == OP_DW ? P : P == 2 ? 0 : P, y = OP == OP_DX && P == 2 ? 1 : 0;
-    floatx16& s = acc[(n * NP + P) % NA][C][R];
-    s = mfma32<OP>(f[PX * RJ + y * CJ + C], f[x * RJ + R], s);
+  auto compute = [&](const uint8_t* st) {
+#pragma unroll
+    for (int u = 0; u < KS / 16; ++u) {
+      u32x4 yf[PY][CJ];
+#pragma unroll
+      for (int p = 0; p < PY; ++p)
+#pragma unroll
+        for (int c = 0; c < CJ; ++c) yf[p][c] = frag(st + p * Y_BYTES, ya, c, u, BC * 2);
+#pragma unroll
+      for (int r = 0; r < RJ; ++r) {
+        u32x4 xf[PX];
+#pragma unroll
+        for (int p = 0; p < PX; ++p) xf[p] = frag(st + p * X_BYTES, xa, r, u, BR * 2);
+        // small terms first
+#pragma unroll
+        for (int p = PX + PY - 2; p >= 0; --p)
+#pragma unroll
+          for (int c = 0; c < CJ; ++c) {
+            floatx16& s = acc[(u * (PX + PY - 1) + p) % NA][c][r];
+            if constexpr (OP == OP_DW) s = mfma32<OP>(yf[0][c], xf[p], s);
+            else s = mfma32<OP>(yf[p == 2 ? PY - 1 : 0][c], xf[p == 2 ? 0 : p], s);
+          }
+      }
+    }
   };
 
-  if constexpr (AHEAD) {
-    // ---- one wave on each matrix unit: nothing but its own instructions can fill its waits, so the
-    // fragments of the next step are read, and the loads of a later one started, between the products
-    // of this one, one instruction in the shadow of a few products.  The stage whose fragments are in
-    // registers is the one to refill.
-    static_assert(KS == 16 && NA == 1, "one substep");
+  // ---- steps: wait for this stage's loads (those of later stages stay in flight), meet the other
+  // waves, refill the stage that all have left, multiply
 #pragma unroll
-    for (int j = 0; j < NST; ++j) issue();
-    wait_vmcnt<(NST - 1) * LN>();
+  for (int j = 0; j < NST - 1; ++j)
+    if (j < nsteps) issue();
+  int stage = 0;
+  for (int s = 0; s < nsteps; ++s) {
+    if (nsteps - 1 - s >= NST - 2) wait_vmcnt<(NST - 2) * LN>();
+    else wait_vmcnt<0>();
     lds_barrier();
-    u32x4 f0[NF], f1[NF];
-    each<NF>([&](auto i) { f0[i] = read(lds, 0, i); });
-    int stage = ST_BYTES;  // of the next step
-    auto step = [&](const u32x4 (&now)[NF], u32x4 (&then)[NF]) {
-      wait_vmcnt<(NST - 2) * LN>();
-      lds_barrier();
-      const uint8_t* const st = lds + stage;
-      constexpr int M = CJ * NP * RJ, SLOTS = (M + 2) / 3, EARLY = (NF + 1) / 2;
-      each<SLOTS>([&](auto slot) {
-        each<3>([&](auto k) {
-          constexpr int I = decltype(slot)::value * 3 + decltype(k)::value;
-          if constexpr (I < M) {
-            constexpr int c = I / (NP * RJ), p = NP - 1 - I / RJ % NP, r = I % RJ;
-            multiply(now, 0, std::integral_constant<int, c>{}, std::integral_constant<int, r>{}, std::integral_constant<int, p>{});
-          }
-        });
-        constexpr int S = decltype(slot)::value;
-        if constexpr (S < EARLY) {  // two fragments a slot, then the loads
-          then[2 * S] = read(st, 0, std::integral_constant<int, 2 * S>{});
-          if constexpr (2 * S + 1 < NF) then[2 * S + 1] = read(st, 0, std::integral_constant<int, 2 * S + 1>{});
-        } else {
-          constexpr int PER = (LN + SLOTS - EARLY - 1) / (SLOTS - EARLY), L0 = (S - EARLY) * PER;
-          each<PER>([&](auto k) {
-            if constexpr (L0 + decltype(k)::value < LN) load(std::integral_constant<int, L0 + decltype(k)::value>{});
-          });
-        }
-        __builtin_amdgcn_sched_barrier(0);
-      });
-      next_load();
-      stage = stage == (NST - 1) * ST_BYTES ? 0 : stage + ST_BYTES;
-    };
-    int s = 0;
-    for (; s + 1 < nsteps; s += 2) {
-      step(f0, f1);
-      step(f1, f0);
-    }
-    if (s < nsteps) step(f0, f1);
-    wait_vmcnt<0>();  // no direct-to-LDS load may outlive the workgroup
-  } else {
-    auto compute = [&](const uint8_t* st) {
-#pragma unroll
-      for (int u = 0; u < KS / 16; ++u) {
-        u32x4 f[NF];
-        each<NF>([&](auto i) { f[i] = read(st, u, i); });
-        each<RJ>([&](auto r) {
-          each<NP>([&](auto k) {
-            each<CJ>([&](auto c) { multiply(f, u, c, r, std::integral_constant<int, NP - 1 - decltype(k)::value>{}); });
-          });
-        });
-      }
-    };
-    // ---- steps: wait for this stage's loads (those of later stages stay in flight), meet the other
-    // waves, refill the stage that all have left, multiply
-#pragma unroll
-    for (int j = 0; j < NST - 1; ++j)
-      if (j < nsteps) issue();
-    int stage = 0;
-    for (int s = 0; s < nsteps; ++s) {
-      if (nsteps - 1 - s >= NST - 2) wait_vmcnt<(NST - 2) * LN>();
-      else wait_vmcnt<0>();
-      lds_barrier();
-      if (s + NST - 1 < nsteps) issue();
-      compute(lds + stage);
-      stage = stage == (NST - 1) * ST_BYTES ? 0 : stage + ST_BYTES;
-    }
+    if (s + NST - 1 < nsteps) issue();
+    compute(lds + stage);
+    stage = stage == (NST - 1) * ST_BYTES ? 0 : stage + ST_BYTES;
   }
 
   // ---- result: four pieces of four columns a lane, turned within quads of lanes: 4 lanes of both half
@@ -358,24 +310,24 @@ __global__ __launch_bounds__(256) void router_join_kernel(RouterGradArgs a) {
   *(floatx4*)(a.dw + i) = v + s;
 }
 
-template <int BR, int BC, int WR, int WC, int KS, int NW, int NX, bool F32, bool AHEAD>
-__global__ __launch_bounds__(WR* WC * 64, AHEAD ? 1 : 2) void router_products_kernel(RouterGradArgs a, int dw_blocks) {
+template <int BR, int BC, int WR, int WC, int KS, int NW, int NX, bool F32>
+__global__ __launch_bounds__(WR* WC * 64, 2) void router_products_kernel(RouterGradArgs a, int dw_blocks) {
   constexpr int DW = NW * Stage<OP_DW, BR, BC, KS, true>::BYTES, DX = NX * Stage<OP_DX, BR, BC, KS, F32>::BYTES;
   __shared__ __align__(16) uint8_t lds[DW > DX ? DW : DX];
   const int block = blockIdx.x;
-  if (block < dw_blocks) router_tile<OP_DW, BR, BC, WR, WC, KS, NW, true, AHEAD>(a, block, dw_blocks, lds);
-  else router_tile<OP_DX, BR, BC, WR, WC, KS, NX, F32, AHEAD>(a, block - dw_blocks, (int)gridDim.x - dw_blocks, lds);
+  if (block < dw_blocks) router_tile<OP_DW, BR, BC, WR, WC, KS, NW, true>(a, block, dw_blocks, lds);
+  else router_tile<OP_DX, BR, BC, WR, WC, KS, NX, F32>(a, block - dw_blocks, (int)gridDim.x - dw_blocks, lds);
 }
 
-template <int BR, int BC, int WR, int WC, int KS, int NW, int NX, bool AHEAD>
+template <int BR, int BC, int WR, int WC, int KS, int NW, int NX>
 void run_products(const RouterGradArgs& a, hipStream_t s) {
   auto blocks = [&](int64_t rows, int n) { return (int)(((rows + BR - 1) / BR * ((a.H + BC - 1) / BC) * n + 7) / 8 * 8); };
   const int dw = a.dw ? blocks(a.E, a.nsplit) : 0, dx = a.dx && a.T > 0 ? blocks(a.T, 1) : 0;
   if (dw + dx == 0) return;
   if (a.dx_f32)
-    hipLaunchKernelGGL((router_products_kernel<BR, BC, WR, WC, KS, NW, NX, true, AHEAD>), dim3((unsigned)(dw + dx)), dim3(WR * WC * 64), 0, s, a, dw);
+    hipLaunchKernelGGL((router_products_kernel<BR, BC, WR, WC, KS, NW, NX, true>), dim3((unsigned)(dw + dx)), dim3(WR * WC * 64), 0, s, a, dw);
   else
-    hipLaunchKernelGGL((router_products_kernel<BR, BC, WR, WC, KS, NW, NX, false, AHEAD>), dim3((unsigned)(dw + dx)), dim3(WR * WC * 64), 0, s, a, dw);
+    hipLaunchKernelGGL((router_products_kernel<BR, BC, WR, WC, KS, NW, NX, false>), dim3((unsigned)(dw + dx)), dim3(WR * WC * 64), 0, s, a, dw);
 }
 
 }  // namespace
@@ -385,8 +337,8 @@ void run_products(const RouterGradArgs& a, hipStream_t s) {
 // beginning and end, 5 us what a third launch costs, besides the parts' bytes.  The weight gradient's items
 // are started first, the others fill the places that they leave.  Fitted to sweeps over 16 to 8192 tokens at
 // 64 x 512 to 1024 x 2560.  Sides measured (us a call, 512 x 2560, fp32 dx):
-//   512 tokens:  128 28.2, 64 29.1     2048: 128 in 2 parts 49.3, 4 56.0; 64 59.0     8192: 128 141, 64 205
-//   1024 tokens of 128 x 640: 64 in one part 18.4, 8 18.4; 4096: 64 in 8 parts 22.3, 128 25.2
+//   512 tokens:  128 26.4, 64 28.6     2048: 128 in 2 parts 50.5, 4 56.7; 64 62.4     8192: 128 148, 64 206
+//   512 tokens of 128 x 640: 64 in one part 14.5, 2 17.4; 4096: 64 in 8 parts 22.0, 128 24.6
 RouterGradPlan router_grad_plan(int64_t T, int E, int H, bool dw, bool dx, bool f32) {
   struct Shape {
     int tile, wgs;
@@ -420,8 +372,8 @@ hipError_t launch_router_grad(RouterGradArgs a, hipStream_t s) {
   const RouterGradPlan p = router_grad_plan(a.T, a.E, a.H, a.dw, a.dx, a.dx_f32);
   a.nsplit = p.nsplit;
   a.split_steps = p.split_steps;
-  if (p.tile == 128) run_products<128, 128, 2, 2, 32, 2, 2, false>(a, s);
-  else run_products<64, 64, 2, 2, 32, 4, 4, false>(a, s);
+  if (p.tile == 128) run_products<128, 128, 2, 2, 32, 2, 2>(a, s);
+  else run_products<64, 64, 2, 2, 32, 4, 4>(a, s);
   if (a.dw && a.nsplit > 1)
     hipLaunchKernelGGL(router_join_kernel, dim3((unsigned)(((int64_t)a.E * a.H + 1023) / 1024)), dim3(256), 0, s, a);
   return hipGetLastError();
