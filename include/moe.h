@@ -543,6 +543,8 @@ typedef struct {
  *   dlogits = dw/dl^T dtopk_w + dloss dloss/dl;   drouter_w = dlogits^T x;   dx = dlogits router_w
  * dtopk_w or counts must be given, and one of the outputs.  ws may be NULL if only dlogits is wanted.
  * An infinity or NaN in a token's logits or gradients makes that token's dlogits and dx, and drouter_w, not finite.
+ * Padding (a token of no sequence and without a chosen expert) has a zero gradient whatever its logits, dtopk_w
+ * and x hold; x is not read where a token's gradient is zero.
  * T = 0 writes zeros to drouter_w (or leaves it, accumulating).  Results have a fixed order of sums. */
 moe_status_t moe_router_backward(const moe_config_t* cfg, int64_t T, const moe_sequences_t* sequences,
                                  const moe_router_backward_t* grads, void* ws, size_t ws_bytes, void* stream);

@@ -769,7 +769,7 @@ def moe_balance_loss(cfg, T, logits, topk_idx, coef, counts, probs, loss, ws, se
     p, n = _workspace(ws, dev)
     _enqueue(load_library().moe_balance_loss, dev, stream, cfg, T, seqs, _exact(logits, "logits", torch.float32, (T, E), dev),
              _exact(topk_idx, "topk_idx", torch.int32, (T, K), dev), coef, _exact(counts, "counts", torch.int32, (B, E), dev),
-             _exact(probs, "probs", torch.float32, (B, E), dev), _exact(loss, "loss", torch.float32, (1,), dev), p, n)
+             _exact(probs, "probs", torch.float32, (B, E), dev), _scalar_at(loss, "loss", torch.float32, dev), p, n)
 
 
 def moe_router_backward(cfg, T, logits, topk_idx, dtopk_w=None, counts=None, coef=0.0, dloss=None, seq_offsets=None,

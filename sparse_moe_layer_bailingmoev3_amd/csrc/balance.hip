@@ -411,7 +411,14 @@ __global__ __launch_bounds__(256) void dlogits_kernel(DlogitsArgs a) {
       for (int i = 0; i < EPL; ++i) d[i] += add[i];
     }
     if (a.dlogits) Row<EPL>::store(a.dlogits + t * E, lane, d);
+    uint32_t top = 0;
+    if (a.bf || a.hf) {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) top = max(top, __float_as_uint(d[i]) & 0x7FFFFFFFu);
+      top = wave_max_u32(top);
+    }
     if (a.bf) {
+      if (lane == 0) a.live[t] = top != 0;
       Pieces<EPL, 3> p;
 #pragma unroll
       for (int i = 0; i < EPL; i += 2) {
@@ -424,10 +431,7 @@ __global__ __launch_bounds__(256) void dlogits_kernel(DlogitsArgs a) {
       p.store(a.bf, (int64_t)a.seq.T * E, lane, 3, [&](int e) { return t * E + e; });
     }
     if (a.hf) {
-      uint32_t top = 0;
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) top = max(top, __float_as_uint(d[i]) & 0x7FFFFFFFu);
-      const int ex = half_exponent(wave_max_u32(top));
+      const int ex = half_exponent(top);
       Pieces<EPL, 2> p;
 #pragma unroll
       for (int i = 0; i < EPL; i += 2) half_pieces(d[i], i + 1 < EPL ? d[i + 1] : 0.f, ex, p.w[0][i / 2], p.w[1][i / 2]);

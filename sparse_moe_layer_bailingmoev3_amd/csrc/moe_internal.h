@@ -296,6 +296,7 @@ struct DlogitsArgs {
   float* dlogits;          // fp32, or NULL
   // the pieces that the products read (each NULL if not wanted), planes one behind the other
   uint16_t* bf;            // bf16 [3, T, E]
+  uint8_t* live;           // with bf: [T], 1 where a token has a gradient, 0 where its row is zeros
   int pair;                // fp16: both pieces (for a result in fp32), or the first alone
   uint16_t* hf;            // fp16, 1 + pair planes of T rows (plane_at), row t times 2^hexp[t]
   int32_t* hexp;           // [T]
@@ -315,6 +316,7 @@ RouterGradPlan router_grad_plan(int64_t T, int E, int H, bool dw, bool dx, bool 
 struct RouterGradArgs {
   int T, E, H;
   const uint16_t* dl;        // bf16 [3, T, E]
+  const uint8_t* live;       // [T] and 32 bytes more
   const uint16_t* x;         // bf16 [T, H]
   float* dw; int acc_w;      // or NULL
   float* part;               // [nsplit, E, H], with nsplit > 1

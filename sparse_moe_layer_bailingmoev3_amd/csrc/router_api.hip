@@ -36,7 +36,7 @@ moe_status_t check_sequences(int64_t T, const moe_sequences_t* q, moe::SeqArgs* 
 
 struct Layout {
   size_t done, parts, psum, pcnt, balance;  // balance loss
-  size_t bf, hf, wt, hexp, wexp, part, backward;  // backward pass
+  size_t bf, live, hf, wt, hexp, wexp, part, backward;  // backward pass
 };
 Layout layout(const moe_config_t* c, int64_t T, int n_seq) {
   const size_t E = c->num_experts;
@@ -62,6 +62,7 @@ Layout layout(const moe_config_t* c, int64_t T, int n_seq) {
       parts = std::max(parts, n > 1 ? n : 0);
     }
   L.bf = take((size_t)T * E * 6);
+  L.live = take(T + 32);  // (read in words to the end of a step)
   L.hf = take(2 * (size_t)moe::plane_size(T, (int)E) * 2);
   L.wt = take(2 * (size_t)moe::plane_size(H, (int)E) * 2);
   L.hexp = take((T + end) * 4);
@@ -171,8 +172,9 @@ moe_status_t moe_router_backward(const moe_config_t* cfg, int64_t T, const moe_s
   if (!g) return fail(MOE_ERR_INVALID_ARG, "the gradients must not be NULL");
   moe::DlogitsArgs d{};
   MOE_TRY(check_sequences(T, sequences, &d.seq));
-  if (!g->dtopk_w && !g->counts) return fail(MOE_ERR_INVALID_ARG, "dtopk_w or counts must be given");
-  if (!g->dlogits && !g->drouter_w && !g->dx) return fail(MOE_ERR_INVALID_ARG, "dlogits, drouter_w or dx must be given");
+  // (without tokens an array may have no address)
+  if (T > 0 && !g->dtopk_w && !g->counts) return fail(MOE_ERR_INVALID_ARG, "dtopk_w or counts must be given");
+  if (T > 0 && !g->dlogits && !g->drouter_w && !g->dx) return fail(MOE_ERR_INVALID_ARG, "dlogits, drouter_w or dx must be given");
   if ((g->drouter_w || g->dx) && cfg->hidden_size > MAX_HIDDEN)
     return fail(MOE_ERR_UNSUPPORTED, "hidden_size %d is above %d", cfg->hidden_size, MAX_HIDDEN);
   if (!std::isfinite(g->balance_coef)) return fail(MOE_ERR_INVALID_ARG, "balance_coef is not finite");
@@ -222,7 +224,10 @@ moe_status_t moe_router_backward(const moe_config_t* cfg, int64_t T, const moe_s
   d.coef = g->balance_coef;
   d.dloss = g->dloss;
   d.dlogits = g->dlogits;
-  if (g->drouter_w) d.bf = (uint16_t*)(w + L.bf);
+  if (g->drouter_w) {
+    d.bf = (uint16_t*)(w + L.bf);
+    d.live = (uint8_t*)(w + L.live);
+  }
   if (g->dx) {
     d.pair = g->dx_dtype == MOE_DTYPE_FP32;
     d.hf = (uint16_t*)(w + L.hf);
@@ -239,6 +244,7 @@ moe_status_t moe_router_backward(const moe_config_t* cfg, int64_t T, const moe_s
   a.E = (int)E;
   a.H = (int)H;
   a.dl = d.bf;
+  a.live = d.live;
   a.x = (const uint16_t*)g->x;
   a.part = (float*)(w + L.part);
   a.dh = d.hf;

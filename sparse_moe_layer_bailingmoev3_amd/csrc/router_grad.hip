@@ -34,6 +34,8 @@
 // (dx alone 90 against 54 us: a load of 16 or 32 rows touched as many cache lines by halves or quarters);
 // the tiles of both products mixed, or dx's first (+15 to +40 %); two rounded bf16 pieces of dl (-20 us, see
 // above).
+#include <type_traits>
+
 #include "moe_common.h"
 #include "moe_internal.h"
 #include "tile_ops.h"
@@ -131,6 +133,23 @@ __device__ __forceinline__ void router_tile(const RouterGradArgs& a, int block, 
   const uint32_t lds0 = lds_offset(lds);
   int left = red;  // reduction values from the next step to load on
   uint32_t lst = lds0;
+  // Rows of x whose tokens have no gradient are not read (zeros instead): x may hold anything there, and 0
+  // times an infinity is no part of the sum.  One byte a token, read through the scalar cache a step ahead;
+  // a load's rows are 4 or 8 consecutive ones.
+  constexpr int YROWS = 64 * 8 / BC;  // rows of a load of x
+  typedef std::conditional_t<YROWS == 8, uint64_t, uint32_t> live_t;
+  static_assert(YROWS == 8 || YROWS == 4, "a load's bytes in one word");
+  typedef const __attribute__((address_space(4))) live_t* live_ptr;
+  const uint8_t* live_at = a.live + red0;
+  live_t live[YN] = {};
+  auto load_live = [&]() {
+    if constexpr (OP == OP_DW) {
+      if (left <= 0) return;
+      each<YN>([&](auto i) { live[i] = *(live_ptr)(uint64_t)(live_at + (wave * YN + i) * YROWS); });
+      live_at += KS;
+    }
+  };
+  load_live();
   auto issue = [&]() {
     const uint32_t st = __builtin_amdgcn_readfirstlane(lst);
     const bool whole = OP == OP_DX || left >= KS;
@@ -144,11 +163,14 @@ __device__ __forceinline__ void router_tile(const RouterGradArgs& a, int block, 
     each<PY>([&](auto p) {
       const u32x4 rs = buffer_at(yb[p]);
       each<YN>([&](auto i) {
-        dma16(whole || yrow[i] < left ? yo[i] : BUF_OUT, rs, st + PX * X_BYTES + p * Y_BYTES + (wave * YN + i) * 1024);
+        bool ok = whole || yrow[i] < left;
+        if constexpr (OP == OP_DW) ok = ok && (live[i] >> (lane / (BC / 8) * 8) & 1);
+        dma16(ok ? yo[i] : BUF_OUT, rs, st + PX * X_BYTES + p * Y_BYTES + (wave * YN + i) * 1024);
       });
       yb[p] += ystep;
     });
     left -= KS;
+    load_live();
     lst = lst == lds0 + (NST - 1) * ST_BYTES ? lds0 : lst + ST_BYTES;
   };
 
