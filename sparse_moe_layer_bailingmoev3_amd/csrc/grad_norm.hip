@@ -194,7 +194,8 @@ __device__ __forceinline__ void clip_chunk(const GradChunk& ck, float c) {
 __global__ __launch_bounds__(256) void grad_clip_kernel(GradArgs a) {
   const float c = *a.coef;
   if (!is_image(a)) return;
-  const GradChunk ck = chunks_of(a)[blockIdx.x];
+  // from the last chunk to the first: what the norm read last is still in the Infinity Cache
+  const GradChunk ck = chunks_of(a)[a.n_chunks - 1 - blockIdx.x];
   if (ck.in == ck.out && c == 1.f) return;  // in place: nothing changes
   switch (ck.flags & (GRAD_IN_F32 | GRAD_OUT_F32)) {
     case 0: clip_chunk<false, false>(ck, c); break;

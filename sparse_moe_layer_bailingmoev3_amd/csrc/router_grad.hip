@@ -33,7 +33,8 @@
 // 157 against 158 us a call), 256 x 128, steps of 16; dx's planes in rows of E values instead of blocks
 // (dx alone 90 against 54 us: a load of 16 or 32 rows touched as many cache lines by halves or quarters);
 // the tiles of both products mixed, or dx's first (+15 to +40 %); two rounded bf16 pieces of dl (-20 us, see
-// above).
+// above); the parts of d router_w added by the workgroup that finishes a tile last instead of a second launch
+// (its fences write back a whole L2: +50 us at 8192 tokens, +20 at 1333).
 #include <type_traits>
 
 #include "moe_common.h"
