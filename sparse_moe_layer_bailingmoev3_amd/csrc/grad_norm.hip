@@ -137,12 +137,13 @@ __global__ __launch_bounds__(256) void grad_norm_kernel(GradArgs a) {
 
 __global__ __launch_bounds__(1024) void grad_norm_finish_kernel(GradArgs a, int n) {
   __shared__ double sums[16];
-  if (a.n_chunks && !is_image(a)) return;
-  double s = 0;
+  double v[GRAD_MAX_PARTIALS / 1024], s = 0;
+  if (n > 0) {
 #pragma unroll
-  for (int i = 0; i < GRAD_MAX_PARTIALS / 1024; ++i) {
-    const int at = i * 1024 + threadIdx.x;
-    if (at < n) s += a.partial[at];
+    for (int i = 0; i < GRAD_MAX_PARTIALS / 1024; ++i) v[i] = a.partial[min(i * 1024 + (int)threadIdx.x, n - 1)];
+    if (!is_image(a)) return;
+#pragma unroll
+    for (int i = 0; i < GRAD_MAX_PARTIALS / 1024; ++i) s += i * 1024 + (int)threadIdx.x < n ? v[i] : 0.0;
   }
   s = wave_sum_f64(s);
   if ((threadIdx.x & 63) == 0) sums[threadIdx.x >> 6] = s;
