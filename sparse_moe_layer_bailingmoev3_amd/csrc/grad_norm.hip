@@ -9,6 +9,12 @@
 // chunk (64 values), in 64 bits from there on.  A share whose sum leaves 2^-60 .. 2^120 (all zeros
 // apart) is read again with squares in 64 bits: gradients whose squares overflow or vanish in fp32 have
 // a norm too.
+//
+// What bounds it, on one MI355X: HBM.  755 M bf16 values in 388 tensors 250 us a call, 6.05 TB/s (the reading
+// kernel 239-247, the adding one 4-5); 94.5 M fp32 values with clipping into bf16 175, of which the norm 70-74
+// and the clipping 87-90: 945 MB in all at 5.4 TB/s.  1.3 M values: three launches of 2.9, 2.0 and 3.4 us, and
+// as long on the host.  Chunks of 16,384 values were as fast (249 and 181 us); loads one after another instead of a
+// chunk's at once, and a table of tensors behind the chunks', took 286 and 6.6 us (small) for the norm.
 #include <type_traits>
 
 #include "moe_common.h"
@@ -211,6 +217,7 @@ __global__ __launch_bounds__(256) void grad_clip_kernel(GradArgs a) {
 hipError_t launch_grad_norm(const GradArgs& a, hipStream_t s) {
   const int cus = device_cu_count();
   if (cus <= 0) return hipErrorInvalidDevice;
+  // as many workgroups as the card holds: few sums to add, no second round
   const int grid = (int)std::min<int64_t>(std::min<int64_t>(a.n_chunks, (int64_t)cus * 8), GRAD_MAX_PARTIALS);
   if (grid > 0) hipLaunchKernelGGL(grad_norm_kernel, dim3((unsigned)grid), dim3(256), 0, s, a);
   const hipError_t e = hipGetLastError();

@@ -23,8 +23,8 @@
 // and are read through the transposing LDS load.  Rows past the end are offsets past a buffer
 // descriptor's end: zeros.
 //
-// What bounds it, on one MI355X: 8192 tokens of 512 x 2560, dx added to in fp32, 121 us alone and up to 150
-// back to back (the card's power then holds its clock down): 129 GFLOP of products, 1.06 to 0.86 PFLOP/s (the
+// What bounds it, on one MI355X: 8192 tokens of 512 x 2560, dx added to in fp32, 122 us at first and up to 167
+// back to back (the card's power then holds its clock down): 129 GFLOP of products, 1.06 to 0.77 PFLOP/s (the
 // library's bf16 product reaches 1.31 in short runs), matrix units busy 48 % of the cycles; LDS reads of a
 // step (16 KB a wave for 24 products of 32 x 32 x 16) and what the loads write there take about as long as the
 // products, no bank conflicts.  d router_w alone 48 us (6400 tokens), dx alone 54 in fp32, 26 in bf16.
