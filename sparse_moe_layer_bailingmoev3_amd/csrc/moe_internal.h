@@ -314,18 +314,18 @@ struct RouterGradPlan {
 };
 RouterGradPlan router_grad_plan(int64_t T, int E, int H, bool dw, bool dx, bool f32);
 struct RouterGradArgs {
+  RouterGradPlan plan;       // of these sizes and outputs
   int T, E, H;
   const uint16_t* dl;        // bf16 [3, T, E]
   const uint8_t* live;       // [T] and 32 bytes more
   const uint16_t* x;         // bf16 [T, H]
   float* dw; int acc_w;      // or NULL
   float* part;               // [nsplit, E, H], with nsplit > 1
-  int nsplit, split_steps;   // set by the launch
   const uint16_t* dh; const int32_t* dexp;  // fp16, planes of T rows
   const uint16_t* wt; const int32_t* wexp;  // fp16, planes of H rows
   void* dx; int dx_f32, acc_x;  // or NULL
 };
-hipError_t launch_router_grad(RouterGradArgs a, hipStream_t s);
+hipError_t launch_router_grad(const RouterGradArgs& a, hipStream_t s);
 // out[t,e] = the partial logits added in split order
 hipError_t launch_sum_logits(const float* partial, int nsplit, int64_t n, float* out, hipStream_t s);
 

@@ -38,7 +38,8 @@ struct Layout {
   size_t done, parts, psum, pcnt, balance;  // balance loss
   size_t bf, live, hf, wt, hexp, wexp, part, backward;  // backward pass
 };
-Layout layout(const moe_config_t* c, int64_t T, int n_seq) {
+// parts: of the weight gradient (0: not split)
+Layout layout(const moe_config_t* c, int64_t T, int n_seq, int parts) {
   const size_t E = c->num_experts;
   const size_t chunk = moe::balance_chunk(T), slots = std::max<size_t>((T + chunk - 1) / chunk, 1) + n_seq;
   Layout L{};
@@ -55,19 +56,13 @@ Layout layout(const moe_config_t* c, int64_t T, int n_seq) {
   L.balance = off;
   off = 0;
   const size_t H = c->hidden_size, end = moe::ROUTER_TILE_MAX;
-  int parts = 0;
-  for (const bool dx : {false, true})
-    for (const bool f32 : {false, true}) {
-      const int n = moe::router_grad_plan(T, (int)E, (int)H, true, dx, f32).nsplit;
-      parts = std::max(parts, n > 1 ? n : 0);
-    }
   L.bf = take((size_t)T * E * 6);
   L.live = take(T + 32);  // (read in words to the end of a step)
   L.hf = take(2 * (size_t)moe::plane_size(T, (int)E) * 2);
   L.wt = take(2 * (size_t)moe::plane_size(H, (int)E) * 2);
   L.hexp = take((T + end) * 4);
   L.wexp = take((H + end) * 4);
-  L.part = take(parts * E * H * 4);
+  L.part = take((parts > 1 ? parts : 0) * E * H * 4);
   L.backward = off;
   return L;
 }
@@ -116,7 +111,11 @@ moe_status_t moe_router_workspace_size(const moe_config_t* cfg, int64_t T, int32
   if (!bytes) return fail(MOE_ERR_INVALID_ARG, "bytes must not be NULL");
   if (n_seq < 1) return fail(MOE_ERR_INVALID_ARG, "n_seq %d must be >= 1", n_seq);
   if (n_seq > MAX_SEQ) return fail(MOE_ERR_UNSUPPORTED, "n_seq %d is above %d", n_seq, MAX_SEQ);
-  const Layout L = layout(cfg, T, n_seq);
+  int parts = 0;  // of any call
+  for (const bool dx : {false, true})
+    for (const bool f32 : {false, true})
+      parts = std::max(parts, moe::router_grad_plan(T, cfg->num_experts, cfg->hidden_size, true, dx, f32).nsplit);
+  const Layout L = layout(cfg, T, n_seq, parts);
   *bytes = std::max(L.balance, L.backward);
   return MOE_OK;
 }
@@ -137,7 +136,7 @@ moe_status_t moe_balance_loss(const moe_config_t* cfg, int64_t T, const moe_sequ
   MOE_TRY(need(probs, "probs"));
   MOE_TRY(need(loss, "loss", 4));
   const int64_t E = cfg->num_experts, K = cfg->num_experts_per_tok, B = a.seq.n;
-  const Layout L = layout(cfg, T, a.seq.n);
+  const Layout L = layout(cfg, T, a.seq.n, 0);
   MOE_TRY(check_ws(ws, ws_bytes, L.balance));
   Spans in, out;
   in.add(logits, T * E, 4, "logits");
@@ -195,8 +194,10 @@ moe_status_t moe_router_backward(const moe_config_t* cfg, int64_t T, const moe_s
   MOE_TRY(need_opt(g->drouter_w, "drouter_w", 16));
   MOE_TRY(need_opt(g->dx, "dx", 16));
   const int64_t E = cfg->num_experts, K = cfg->num_experts_per_tok, H = cfg->hidden_size;
-  const Layout L = layout(cfg, T, d.seq.n);
   const bool products = g->drouter_w || g->dx;
+  moe::RouterGradPlan plan{};
+  if (products) plan = moe::router_grad_plan(T, (int)E, (int)H, g->drouter_w, g->dx, g->dx_dtype == MOE_DTYPE_FP32);
+  const Layout L = layout(cfg, T, d.seq.n, plan.nsplit);
   if (products) MOE_TRY(check_ws(ws, ws_bytes, L.backward));
   Spans in, out;
   in.add(g->logits, T * E, 4, "logits");
@@ -240,6 +241,7 @@ moe_status_t moe_router_backward(const moe_config_t* cfg, int64_t T, const moe_s
   MOE_TRY(done(moe::launch_dlogits(d, (hipStream_t)stream), "router backward launch"));
   if (!products) return MOE_OK;
   moe::RouterGradArgs a{};
+  a.plan = plan;
   a.T = (int)T;
   a.E = (int)E;
   a.H = (int)H;

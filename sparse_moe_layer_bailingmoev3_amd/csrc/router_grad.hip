@@ -82,7 +82,7 @@ __device__ __forceinline__ void router_tile(const RouterGradArgs& a, int block, 
   constexpr int XN = X_BYTES / (NW * 1024), YN = Y_BYTES / (NW * 1024), LN = PX * XN + PY * YN;  // loads per wave
   static_assert(XN * NW * 1024 == X_BYTES && YN * NW * 1024 == Y_BYTES, "a plane must split evenly over the waves");
   constexpr int RJ = BR / WR / 32, CJ = BC / WC / 32;
-    constexpr int NA = RJ * CJ == 1 ? 2 : 1;   // sums that take turns (one alone would wait for itself)
+  constexpr int NA = RJ * CJ == 1 ? 2 : 1;   // sums that take turns (one alone would wait for itself)
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -92,13 +92,13 @@ __device__ __forceinline__ void router_tile(const RouterGradArgs& a, int block, 
   // ---- which tile: consecutive ones (the column tiles of a row tile, the tiles of a split) on one XCD
   const int nct = (a.H + BC - 1) / BC;
   const int nrt = ((OP == OP_DW ? a.E : a.T) + BR - 1) / BR;
-  const int tiles = nct * nrt, total = OP == OP_DW ? tiles * a.nsplit : tiles;
+  const int tiles = nct * nrt, total = OP == OP_DW ? tiles * a.plan.nsplit : tiles;
   const int item = (block & 7) * (blocks >> 3) + (block >> 3);  // (blocks: total, rounded up to a multiple of 8)
   if (item >= total) return;
   const int split = item / tiles, tile = item - split * tiles;
   const int rt = tile / nct, r0 = rt * BR, c0 = (tile - rt * nct) * BC;
-  const int red0 = OP == OP_DW ? split * a.split_steps * 32 : 0;
-  const int red = OP == OP_DW ? max(min(a.T - red0, a.split_steps * 32), 0) : a.E;
+  const int red0 = OP == OP_DW ? split * a.plan.split_steps * 32 : 0;
+  const int red = OP == OP_DW ? max(min(a.T - red0, a.plan.split_steps * 32), 0) : a.E;
   const int nsteps = (red + KS - 1) / KS;
 
   // ---- loads
@@ -254,8 +254,8 @@ __device__ __forceinline__ void router_tile(const RouterGradArgs& a, int block, 
   // ---- result: four pieces of four columns a lane, turned within quads of lanes: 4 lanes of both half
   // waves then hold 32 columns of one row side by side (whole cache lines)
   const int rows = OP == OP_DW ? a.E : a.T;
-  float* const o32 = OP == OP_DX ? (float*)a.dx : a.nsplit > 1 ? a.part + (int64_t)split * a.E * a.H : a.dw;
-  const bool add = OP == OP_DX ? a.acc_x : a.acc_w && a.nsplit == 1;
+  float* const o32 = OP == OP_DX ? (float*)a.dx : a.plan.nsplit > 1 ? a.part + (int64_t)split * a.E * a.H : a.dw;
+  const bool add = OP == OP_DX ? a.acc_x : a.acc_w && a.plan.nsplit == 1;
   const int row0 = r0 + wr * RJ * 32 + (r32 & 28), col0 = c0 + wc * CJ * 32 + 8 * (r32 & 3) + 4 * half;
   // everything that the tile's end reads is asked for at once, or, the old values, a column of fragments
   // ahead of their use: one after another, each would wait for itself
@@ -329,7 +329,7 @@ __global__ __launch_bounds__(256) void router_join_kernel(RouterGradArgs a) {
   if (a.acc_w) v = *(const floatx4*)(a.dw + i);
   floatx4 s{0.f, 0.f, 0.f, 0.f};
 #pragma unroll 8
-  for (int p = 0; p < a.nsplit; ++p) s += *(const floatx4*)(a.part + p * n + i);
+  for (int p = 0; p < a.plan.nsplit; ++p) s += *(const floatx4*)(a.part + p * n + i);
   *(floatx4*)(a.dw + i) = v + s;
 }
 
@@ -345,7 +345,7 @@ __global__ __launch_bounds__(WR* WC * 64, 2) void router_products_kernel(RouterG
 template <int BR, int BC, int WR, int WC, int KS, int NW, int NX>
 void run_products(const RouterGradArgs& a, hipStream_t s) {
   auto blocks = [&](int64_t rows, int n) { return (int)(((rows + BR - 1) / BR * ((a.H + BC - 1) / BC) * n + 7) / 8 * 8); };
-  const int dw = a.dw ? blocks(a.E, a.nsplit) : 0, dx = a.dx && a.T > 0 ? blocks(a.T, 1) : 0;
+  const int dw = a.dw ? blocks(a.E, a.plan.nsplit) : 0, dx = a.dx && a.T > 0 ? blocks(a.T, 1) : 0;
   if (dw + dx == 0) return;
   if (a.dx_f32)
     hipLaunchKernelGGL((router_products_kernel<BR, BC, WR, WC, KS, NW, NX, true>), dim3((unsigned)(dw + dx)), dim3(WR * WC * 64), 0, s, a, dw);
@@ -391,13 +391,10 @@ RouterGradPlan router_grad_plan(int64_t T, int E, int H, bool dw, bool dx, bool 
   return best;
 }
 
-hipError_t launch_router_grad(RouterGradArgs a, hipStream_t s) {
-  const RouterGradPlan p = router_grad_plan(a.T, a.E, a.H, a.dw, a.dx, a.dx_f32);
-  a.nsplit = p.nsplit;
-  a.split_steps = p.split_steps;
-  if (p.tile == 128) run_products<128, 128, 2, 2, 32, 2, 2>(a, s);
+hipError_t launch_router_grad(const RouterGradArgs& a, hipStream_t s) {
+  if (a.plan.tile == 128) run_products<128, 128, 2, 2, 32, 2, 2>(a, s);
   else run_products<64, 64, 2, 2, 32, 4, 4>(a, s);
-  if (a.dw && a.nsplit > 1)
+  if (a.dw && a.plan.nsplit > 1)
     hipLaunchKernelGGL(router_join_kernel, dim3((unsigned)(((int64_t)a.E * a.H + 1023) / 1024)), dim3(256), 0, s, a);
   return hipGetLastError();
 }
