@@ -75,10 +75,11 @@ __global__ __launch_bounds__(BAL_WAVES * 64) void balance_partial_kernel(Balance
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.done = 0;
   const int t0 = blockIdx.x * a.chunk, t1 = (int)min((int64_t)t0 + a.chunk, (int64_t)a.seq.T);
   for (int i = threadIdx.x; i < E; i += BAL_WAVES * 64) hist[i] = 0;
-  int b = seq_of(a.seq, t0, &first);
+  const Seqs seqs(a.seq);
+  int b = seqs.first(t0, &first);
   __syncthreads();
   for (; b < a.seq.n; ++b) {
-    const Seq q = seq_at(a.seq, b);
+    const Seq q = seqs.at(b);
     if (q.begin >= t1) break;
     const int lo = max(q.begin, t0), hi = min(q.end, t1);
     if (lo < hi) {
@@ -105,11 +106,12 @@ __global__ __launch_bounds__(1024) void balance_small_kernel(BalanceArgs a) {
   __shared__ int tokens;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   for (int i = threadIdx.x; i < E; i += 1024) hist[i] = 0;
-  const int N = seq_tokens(a.seq, &tokens);
+  const Seqs seqs(a.seq);
+  const int N = seqs.tokens(&tokens);
   __syncthreads();
   double part = 0;
   for (int b = 0; b < a.seq.n; ++b) {
-    const Seq q = seq_at(a.seq, b);
+    const Seq q = seqs.at(b);
     const int n = q.end - q.begin;
     if (n > 0) balance_run<EPL, WAVES>(a, q.begin, q.end, sums, hist);
     for (int e = threadIdx.x; e < E; e += 1024) {
@@ -138,18 +140,20 @@ __global__ __launch_bounds__(1024) void balance_finish_kernel(BalanceArgs a) {
   __shared__ int tokens, last;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int b = blockIdx.x, e = blockIdx.y * 64 + lane;
-  const Seq q = seq_at(a.seq, b);
-  const int N = seq_tokens(a.seq, &tokens);
+  const Seqs seqs(a.seq);
+  const Seq q = seqs.at(b);
+  const int N = seqs.tokens(&tokens);
   double sum = 0;
   int cnt = 0;
   if (q.begin < q.end) {
-    const int c1 = (q.end - 1) / a.chunk;
-    for (int c = q.begin / a.chunk + wave; c <= c1; c += 16 * 16) {
+    const int c1 = __builtin_amdgcn_readfirstlane((q.end - 1) / a.chunk);
+    for (int c = __builtin_amdgcn_readfirstlane(q.begin / a.chunk + wave); c <= c1; c += 16 * 16) {
       float v[16];  // sixteen slots' loads at once
       int n[16];
 #pragma unroll
       for (int k = 0; k < 16; ++k) {
-        const int64_t at = ((int64_t)min(c + 16 * k, c1) + b) * a.E + e;
+        if (c + 16 * k > c1) break;
+        const int64_t at = ((int64_t)(c + 16 * k) + b) * a.E + e;
         v[k] = a.psum[at];
         n[k] = a.pcnt[at];
       }
@@ -309,7 +313,7 @@ __device__ __forceinline__ void split_weight(const DlogitsArgs& a, int block, ui
 // asked for, and in the 16-bit pieces that the products take; other workgroups take router_w apart meanwhile.
 //
 // What bounds it, on one MI355X: 8192 tokens of 512 experts with both products' pieces 15.5-18 us, 28 MB read
-// and 50 written at the copy's rate; 16,384 tokens of 256 experts, fp32 alone, 12 us against 5 of traffic: latency
+// and 50 written at the copy's rate; 16,384 tokens of 256 experts, fp32 alone, 11.5 us against 5 of traffic: latency
 // and vector work of four tokens a wave.  router_w's part (512 x 2560) takes 8 alone, so it goes first.
 template <int EPL>
 __global__ __launch_bounds__(256) void dlogits_kernel(DlogitsArgs a) {
@@ -324,14 +328,6 @@ __global__ __launch_bounds__(256) void dlogits_kernel(DlogitsArgs a) {
   static_assert(SPLIT_WORDS<EPL> >= 4 * E, "a row of every wave");
   float(*const rows)[E] = (float(*)[E])lds;
   const int64_t base = (int64_t)((int)blockIdx.x - a.weight_blocks) * 4 * a.run;
-  int b = 0;
-  float g0 = 0.f;
-  if (a.counts) {
-    b = seq_of(a.seq, (int)base, &first);
-    const int N = seq_tokens(a.seq, &tokens);
-    g0 = N > 0 ? a.coef / (float)N : 0.f;
-    if (a.dloss) g0 *= *a.dloss;
-  }
   Seq q{0, 0, 0};
   float f[EPL] = {};
   bool have = false;
@@ -349,6 +345,15 @@ __global__ __launch_bounds__(256) void dlogits_kernel(DlogitsArgs a) {
     }
   };
   fetch(t0);
+  const Seqs seqs(a.seq, a.counts != nullptr);
+  int b = 0;
+  float g0 = 0.f;
+  if (a.counts) {
+    b = seqs.first((int)base, &first);
+    const int N = seqs.tokens(&tokens);
+    g0 = N > 0 ? a.coef / (float)N : 0.f;
+    if (a.dloss) g0 *= *a.dloss;
+  }
   for (int64_t t = t0; t < t1; ++t) {
     float l[EPL], d[EPL];
 #pragma unroll
@@ -366,7 +371,7 @@ __global__ __launch_bounds__(256) void dlogits_kernel(DlogitsArgs a) {
       while (b < a.seq.n && (!have || q.next <= t)) {  // on to the token's sequence
         if (have) ++b;
         if (b >= a.seq.n) break;
-        q = seq_at(a.seq, b);
+        q = seqs.at(b);
         have = true;
         if (q.next <= t) continue;
         int32_t c[EPL];
