@@ -415,6 +415,30 @@ def test_many_sequences(T, B):
     check_dlogits(dl, orc.router_backward(f64(logits), idx.numpy(), K, 1, 2.5, None, want.counts, 2.0, off))
 
 
+@pytest.mark.parametrize("B", [1, 2, 63, 64, 65])
+@pytest.mark.parametrize("T", [200, 3000, 20000])
+@pytest.mark.parametrize("padded", [False, True])
+def test_sequences_about_a_wave_of_them(T, B, padded):
+    g = gen(12)
+    E, K = 64, 2
+    cfg = config(E, K)
+    off = torch.sort(torch.randint(0, T + 1, (B + 1,), generator=g))[0].tolist()  # padding at both ends
+    lens = [int(torch.randint(0, b - a + 1, (1,), generator=g)) for a, b in zip(off, off[1:])] if padded else None
+    logits, idx, dw = torch.randn(T, E, generator=g), ids(g, T, E, K), torch.randn(T, K, generator=g)
+    counts, probs, loss = torch.empty(B, E, dtype=I32, device="cuda"), torch.empty(B, E, device="cuda"), torch.empty(1, device="cuda")
+    o, n = on_gpu(off, lens)
+    moe.moe_balance_loss(cfg, T, logits.cuda(), idx.cuda(), 2.0, counts, probs, loss, workspace(cfg, T, B), seq_offsets=o, seq_lens=n)
+    want = orc.balance_loss(f64(logits), idx.numpy(), K, 2.0, off, lens)
+    assert np.array_equal(counts.cpu().numpy(), want.counts)
+    rel = 2 * SCORE + (E / 64 + 8) * U32 + 264 * U32  # (as in test_balance_loss)
+    assert np.all(np.abs(f64(probs) - want.probs) <= rel * want.probs + 1e-37)
+    assert abs(loss.item() - want.loss) <= (rel + 4 * U32) * abs(want.loss)
+    dl = torch.empty(T, E, device="cuda")
+    moe.moe_router_backward(cfg, T, logits.cuda(), idx.cuda(), dtopk_w=dw.cuda(), counts=counts, coef=2.0, seq_offsets=o, seq_lens=n,
+                            dlogits=dl)
+    check_dlogits(dl, orc.router_backward(f64(logits), idx.numpy(), K, 1, 2.5, f64(dw), want.counts, 2.0, off, lens))
+
+
 @pytest.mark.parametrize("size", [1e-36, 1e-20, 1e-6, 1e6, 1e20, 1e30], ids=str)
 def test_gradients_of_any_size(size):
     """Scaled pieces: gradients, weights and columns of weights far from one, rows that span 2^30."""
