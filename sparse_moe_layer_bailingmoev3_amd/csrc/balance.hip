@@ -8,7 +8,7 @@
 // chunk touches, its waves taking four tokens at a time (a lane EPL experts of each), and leaves one
 // row of sums and counts per (chunk c, sequence b) in slot c + b of the workspace.  (Both grow along the
 // walk and one of them at every step, so no two pairs share a slot.)  The second adds a sequence's
-// slots, 64 experts a workgroup, and its last workgroup to finish adds the parts of the loss.  A small
+// slots, 64 experts a workgroup or wave, and its last workgroup to finish adds the parts of the loss.  A small
 // batch is done by one workgroup in one launch.  Every sum has a fixed order.
 //
 // Counts are integers: LDS atomics, whose order does not matter.
@@ -71,12 +71,11 @@ __global__ __launch_bounds__(BAL_WAVES * 64) void balance_partial_kernel(Balance
   constexpr int E = EPL * 64;
   __shared__ __align__(16) float sums[BAL_WAVES][E];
   __shared__ int hist[E];
-  __shared__ int first;
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.done = 0;
   const int t0 = blockIdx.x * a.chunk, t1 = (int)min((int64_t)t0 + a.chunk, (int64_t)a.seq.T);
   for (int i = threadIdx.x; i < E; i += BAL_WAVES * 64) hist[i] = 0;
   const Seqs seqs(a.seq);
-  int b = seqs.first(t0, &first);
+  int b = seqs.first(t0);
   __syncthreads();
   for (; b < a.seq.n; ++b) {
     const Seq q = seqs.at(b);
@@ -133,81 +132,103 @@ __global__ __launch_bounds__(1024) void balance_small_kernel(BalanceArgs a) {
   }
 }
 
-// Sequence blockIdx.x, experts 64 blockIdx.y ..; the waves take every 16th slot.
+// A pair is a sequence and 64 experts.  Few pairs: a workgroup each, whose waves take turns at the slots.
+// MANY: a wave each, 16 a workgroup, as launching and meeting at the counter cost each workgroup its turn.
+template <bool MANY>
 __global__ __launch_bounds__(1024) void balance_finish_kernel(BalanceArgs a) {
+  constexpr int WAVES = MANY ? 1 : 16;  // of a pair
   __shared__ double sums[16][64];
   __shared__ int cnts[16][64];
   __shared__ int tokens, last;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int b = blockIdx.x, e = blockIdx.y * 64 + lane;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, turn = MANY ? 0 : wave;
+  const int blocks = a.E / 64, pairs = a.seq.n * blocks;
+  const int pair = __builtin_amdgcn_readfirstlane(MANY ? blockIdx.x * 16 + wave : blockIdx.x);
+  const int b = pair / blocks, e = (pair - b * blocks) * 64 + lane;
   const Seqs seqs(a.seq);
-  const Seq q = seqs.at(b);
-  const int N = seqs.tokens(&tokens);
+  const bool late = a.seq.lens && !seqs.few;  // lens that the last workgroup adds
+  int N = late ? 0 : seqs.tokens(&tokens);
+  const Seq q = pair < pairs ? seqs.at(b) : Seq{0, 0, 0};
   double sum = 0;
   int cnt = 0;
   if (q.begin < q.end) {
     const int c1 = __builtin_amdgcn_readfirstlane((q.end - 1) / a.chunk);
-    for (int c = __builtin_amdgcn_readfirstlane(q.begin / a.chunk + wave); c <= c1; c += 16 * 16) {
+    for (int c = __builtin_amdgcn_readfirstlane(q.begin / a.chunk + turn); c <= c1; c += 16 * WAVES) {
       float v[16];  // sixteen slots' loads at once
       int n[16];
 #pragma unroll
       for (int k = 0; k < 16; ++k) {
-        if (c + 16 * k > c1) break;
-        const int64_t at = ((int64_t)(c + 16 * k) + b) * a.E + e;
+        if (c + WAVES * k > c1) break;
+        const int64_t at = ((int64_t)(c + WAVES * k) + b) * a.E + e;
         v[k] = a.psum[at];
         n[k] = a.pcnt[at];
       }
 #pragma unroll
       for (int k = 0; k < 16; ++k)
-        if (c + 16 * k <= c1) {
+        if (c + WAVES * k <= c1) {
           sum += v[k];
           cnt += n[k];
         }
     }
   }
-  sums[wave][lane] = sum;
-  cnts[wave][lane] = cnt;
-  __syncthreads();
-  const int64_t n = (int64_t)gridDim.x * gridDim.y;
-  const bool alone = n <= 1024;  // parts that one wave adds
-  if (wave == 0) {
-    for (int w = 1; w < 16; ++w) {
+  if constexpr (!MANY) {
+    sums[wave][lane] = sum;
+    cnts[wave][lane] = cnt;
+    __syncthreads();
+    if (wave > 0) return;
+    for (int w = 1; w < WAVES; ++w) {
       sum += sums[w][lane];
       cnt += cnts[w][lane];
     }
+  }
+  if (pair < pairs) {
     const int len = q.end - q.begin;
     const double mean = len > 0 ? sum / len : 0.0;
     const int64_t at = (int64_t)b * a.E + e;
     a.counts[at] = cnt;
     a.probs[at] = (float)mean;
     const double part = wave_sum_f64(cnt * mean);
-    int is_last = 0;
     if (lane == 0) {
-      a.part[(int64_t)b * gridDim.y + blockIdx.y] = part;
-      __threadfence();
-      is_last = atomicAdd(a.done, 1) == (int)n - 1;
+      // An exchange has taken place where all dies see it once its old value is here: no cache need be written
+      // back, as a fence would do for every pair (8192 pairs: 30 us a call, 172 with fences).
+      const unsigned long long old = __hip_atomic_exchange((unsigned long long*)(a.part + pair), __double_as_longlong(part),
+                                                           __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      asm volatile("" ::"v"(old) : "memory");
     }
-    is_last = __builtin_amdgcn_readfirstlane(is_last);
-    if (lane == 0) last = is_last;
-    if (alone && !is_last) return;
-  } else if (alone) {
-    return;
   }
-  if (!alone) {
+  int is_last = 0;
+  if constexpr (MANY) __syncthreads();
+  if (threadIdx.x == 0) is_last = atomicAdd(a.done, 1) == (int)gridDim.x - 1;
+  if constexpr (MANY) {
+    if (threadIdx.x == 0) last = is_last;
     __syncthreads();
-    if (!last) return;
+    is_last = last;
   }
+  if (!__builtin_amdgcn_readfirstlane(is_last)) return;
   // the last workgroup: all parts in order, read past the caches that do not see other dies' stores
   __threadfence();
+  constexpr int STEP = MANY ? 1024 : 64;
   double total = 0;
-  for (int64_t i = threadIdx.x; i < n; i += alone ? 64 : 1024)
-    total += __hip_atomic_load(a.part + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  for (int i = threadIdx.x; i < pairs; i += STEP) total += __hip_atomic_load(a.part + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   total = wave_sum_f64(total);
-  if (!alone) {
-    if (lane == 0) sums[0][wave] = total;
+  if (late) {
+    for (int i = threadIdx.x; i < a.seq.n; i += STEP) {
+      const Seq s = seq_at(a.seq, i);
+      N += s.end - s.begin;
+    }
+    N = wave_sum_i32(N);
+  }
+  if constexpr (MANY) {
+    if (lane == 0) {
+      sums[0][wave] = total;
+      cnts[0][wave] = N;
+    }
     __syncthreads();
     total = 0;
-    for (int w = 0; w < 16; ++w) total += sums[0][w];
+    if (late) N = 0;
+    for (int w = 0; w < 16; ++w) {
+      total += sums[0][w];
+      if (late) N += cnts[0][w];
+    }
   }
   if (threadIdx.x == 0) *a.loss = N > 0 ? (float)((double)a.coef * a.E * total / ((double)a.K * N)) : 0.f;
 }
@@ -319,7 +340,7 @@ template <int EPL>
 __global__ __launch_bounds__(256) void dlogits_kernel(DlogitsArgs a) {
   constexpr int E = EPL * 64;
   __shared__ __align__(16) uint32_t lds[SPLIT_WORDS<EPL>];
-  __shared__ int first, tokens;
+  __shared__ int tokens;
   if ((int)blockIdx.x < a.weight_blocks) {  // (first: they take longest)
     split_weight<EPL>(a, blockIdx.x, lds);
     return;
@@ -349,7 +370,7 @@ __global__ __launch_bounds__(256) void dlogits_kernel(DlogitsArgs a) {
   int b = 0;
   float g0 = 0.f;
   if (a.counts) {
-    b = seqs.first((int)base, &first);
+    b = seqs.first((int)base);
     const int N = seqs.tokens(&tokens);
     g0 = N > 0 ? a.coef / (float)N : 0.f;
     if (a.dloss) g0 *= *a.dloss;
@@ -458,17 +479,21 @@ __global__ __launch_bounds__(256) void dlogits_kernel(DlogitsArgs a) {
 
 }  // namespace
 
-// Up to so many tokens and logits one workgroup does it all.  Sides measured (us a call, one launch / two): 64
-// tokens of 512 experts 8.1 / 10.9, 128 11.9 / 10.9; 256 tokens of 64 experts 8.7 / 10.3, 512 14.2 / 10.8.
-constexpr int BALANCE_SMALL_T = 256;
-constexpr int64_t BALANCE_SMALL = 32768;
+// Up to so many tokens and logits one workgroup does it all, one sequence after another.  Sides measured (us a
+// call, one launch / two): 64 tokens of 512 experts 7.8 / 9.7, in 2 sequences 8.8 / 10.5, in 3 11.7 / 10.8; 128 tokens
+// 11.9 / 10.9; 256 tokens of 64 experts 8.7 / 9.9, in 4 sequences 9.7 / 10.1, in 6 11.7 / 9.8; 512 tokens 14.2 / 10.8.
+constexpr int BALANCE_SMALL_T = 256, BALANCE_SMALL_SEQ = 4;
+constexpr int64_t BALANCE_SMALL = 32768, BALANCE_SMALL_RUNS = 65536;
 
 // Tokens of a chunk: about one workgroup a compute unit, from 32 (four a wave, whose loads are under way at
 // once) to 256.  Sides measured (us a call, 512 experts): 8192 tokens 16 14.2, 32 12.8, 64 15.1; 16,384 32
-// 17.7, 64 15.2, 128 20.4; 32,768 64 23.8, 128 22.5, 256 32.3; 200,000 128 107, 256 105.
-int balance_chunk(int64_t T) {
+// 17.7, 64 15.2, 128 20.4; 32,768 64 23.8, 128 22.5, 256 32.3; 200,000 128 107, 256 105.  But no longer than a
+// sequence on average, down to 4, as a workgroup takes its sequences one after another: 65 tokens in 16
+// sequences 10.8, in chunks of 32 25.3; 257 tokens of 64 experts in 64 sequences 10.0, 14.6.
+int balance_chunk(int64_t T, int n_seq) {
   int c = 32;
   while (c < 256 && T > (int64_t)c * 256) c *= 2;
+  while (c > 4 && (int64_t)c * n_seq > T) c /= 2;
   return c;
 }
 
@@ -483,7 +508,8 @@ int balance_chunk(int64_t T) {
   }
 
 hipError_t launch_balance(const BalanceArgs& a, hipStream_t s) {
-  if (a.seq.T <= BALANCE_SMALL_T && a.seq.T * a.E <= BALANCE_SMALL && a.seq.n <= std::max(a.seq.T, 16)) {
+  if (a.seq.T <= BALANCE_SMALL_T && a.seq.T * a.E <= BALANCE_SMALL && a.seq.n <= BALANCE_SMALL_SEQ &&
+      a.seq.T * a.E * a.seq.n <= BALANCE_SMALL_RUNS) {
 #define MOE_BAL(N) hipLaunchKernelGGL(balance_small_kernel<N>, dim3(1), dim3(1024), 0, s, a)
     MOE_EPL(a.E, MOE_BAL)
 #undef MOE_BAL
@@ -495,7 +521,13 @@ hipError_t launch_balance(const BalanceArgs& a, hipStream_t s) {
 #undef MOE_BAL
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(balance_finish_kernel, dim3((unsigned)a.seq.n, (unsigned)(a.E / 64)), dim3(1024), 0, s, a);
+  // Sides measured (us a call, a workgroup each / a wave each): 128 pairs 13.1 / 15.5, 256 14.7 / 15.3, 512 18.3 /
+  // 15.2, 2048 47 / 21, 8192 145 / 30.
+  const int pairs = a.seq.n * (a.E / 64);
+  if (pairs <= 256)
+    hipLaunchKernelGGL(balance_finish_kernel<false>, dim3((unsigned)pairs), dim3(1024), 0, s, a);
+  else
+    hipLaunchKernelGGL(balance_finish_kernel<true>, dim3((unsigned)((pairs + 15) / 16)), dim3(1024), 0, s, a);
   return hipGetLastError();
 }
 

@@ -277,7 +277,7 @@ struct BalanceArgs {
   int* done;               // workgroups of the second launch that have finished
   int32_t* counts; float* probs; float* loss;
 };
-int balance_chunk(int64_t T);
+int balance_chunk(int64_t T, int n_seq);
 hipError_t launch_balance(const BalanceArgs& a, hipStream_t s);
 
 // The fp16 planes of dx's operands lie in blocks of 32 rows by 16 experts, 1 KB each, the blocks of 32 rows

@@ -41,7 +41,7 @@ struct Layout {
 // parts: of the weight gradient (0: not split)
 Layout layout(const moe_config_t* c, int64_t T, int n_seq, int parts) {
   const size_t E = c->num_experts;
-  const size_t chunk = moe::balance_chunk(T), slots = std::max<size_t>((T + chunk - 1) / chunk, 1) + n_seq;
+  const size_t chunk = moe::balance_chunk(T, n_seq), slots = std::max<size_t>((T + chunk - 1) / chunk, 1) + n_seq;
   Layout L{};
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -153,7 +153,7 @@ moe_status_t moe_balance_loss(const moe_config_t* cfg, int64_t T, const moe_sequ
   a.coef = coef;
   a.logits = logits;
   a.topk_idx = topk_idx;
-  a.chunk = moe::balance_chunk(T);
+  a.chunk = moe::balance_chunk(T, a.seq.n);
   a.done = (int*)(w + L.done);
   a.part = (double*)(w + L.parts);
   a.psum = (float*)(w + L.psum);

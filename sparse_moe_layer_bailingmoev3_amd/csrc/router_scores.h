@@ -122,20 +122,22 @@ struct Seqs {
     const int l = __builtin_amdgcn_readfirstlane(b);
     return {__builtin_amdgcn_readlane(mine.begin, l), __builtin_amdgcn_readlane(mine.end, l), __builtin_amdgcn_readlane(mine.next, l)};
   }
-  // The first sequence whose run ends behind token t (n if none; 0 where there is but one).  `count`: one int
-  // in LDS.
-  __device__ __forceinline__ int first(int t, int* count) const {
+  // The first sequence whose run ends behind token t (n if none; 0 where there is but one): up to 64, counted;
+  // more, sought in steps of 64 parts.
+  __device__ __forceinline__ int first(int t) const {
     if (!q.offsets || q.n == 1) return 0;
-    if (few) return __builtin_popcountll(__ballot((int)(threadIdx.x & 63) < q.n && mine.next <= t));
-    if (threadIdx.x == 0) *count = 0;
-    __syncthreads();
-    int c = 0;
-    for (int b = threadIdx.x; b < q.n; b += blockDim.x) c += q.offsets[b + 1] <= t;
-    if (c) atomicAdd(count, c);
-    __syncthreads();
-    return *count;
+    const int lane = threadIdx.x & 63;
+    if (few) return __builtin_popcountll(__ballot(lane < q.n && mine.next <= t));
+    int lo = 0;
+    for (int n = q.n; n > 0;) {  // lo .. lo + n holds the answer
+      const int part = (n + 63) / 64, at = (lane + 1) * part;  // each lane asks for the last of its part
+      const int k = __builtin_popcountll(__ballot(at <= n && q.offsets[lo + min(at, n)] <= t));
+      lo += k * part;
+      n = min(part - 1, n - k * part);
+    }
+    return lo;
   }
-  // Tokens of all sequences.  `count`: one int in LDS, not that of first().
+  // Tokens of all sequences.  `count`: one int in LDS.
   __device__ __forceinline__ int tokens(int* count) const {
     if (few) return wave_sum_i32(mine.end - mine.begin);
     if (!q.lens) return q.offsets ? max(min(q.offsets[q.n], q.T) - max(q.offsets[0], 0), 0) : q.T;

@@ -439,6 +439,30 @@ def test_sequences_about_a_wave_of_them(T, B, padded):
     check_dlogits(dl, orc.router_backward(f64(logits), idx.numpy(), K, 1, 2.5, f64(dw), want.counts, 2.0, off, lens))
 
 
+@pytest.mark.parametrize("E", [64, 512, 1024])
+@pytest.mark.parametrize("T,B", [(40, 4), (65, 16), (500, 33), (5000, 300), (20000, 66)])
+def test_short_and_long_sequences_together(T, B, E):
+    g = gen(13)
+    K = 4
+    cfg = config(E, K)
+    short = torch.arange(B) * (T // (3 * B))  # the last takes two thirds of the tokens
+    off = [*short.tolist(), T]
+    lens = [max(b - a - i % 3, 0) for i, (a, b) in enumerate(zip(off, off[1:]))]
+    logits, idx = torch.randn(T, E, generator=g), ids(g, T, E, K)
+    o, n = on_gpu(off, lens)
+    want = orc.balance_loss(f64(logits), idx.numpy(), K, 2.0, off, lens)
+    rel = 2 * SCORE + (E / 64 + 8) * U32 + 264 * U32  # (as in test_balance_loss)
+    losses = []
+    for _ in range(3):  # the parts, whichever workgroup ends last, in one order
+        counts, probs, loss = torch.empty(B, E, dtype=I32, device="cuda"), torch.empty(B, E, device="cuda"), torch.empty(1, device="cuda")
+        moe.moe_balance_loss(cfg, T, logits.cuda(), idx.cuda(), 2.0, counts, probs, loss, workspace(cfg, T, B), seq_offsets=o, seq_lens=n)
+        assert np.array_equal(counts.cpu().numpy(), want.counts)
+        assert np.all(np.abs(f64(probs) - want.probs) <= rel * want.probs + 1e-37)
+        assert abs(loss.item() - want.loss) <= (rel + 4 * U32) * abs(want.loss)
+        losses.append(loss.item())
+    assert losses[0] == losses[1] == losses[2]
+
+
 @pytest.mark.parametrize("size", [1e-36, 1e-20, 1e-6, 1e6, 1e20, 1e30], ids=str)
 def test_gradients_of_any_size(size):
     """Scaled pieces: gradients, weights and columns of weights far from one, rows that span 2^30."""
