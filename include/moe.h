@@ -545,7 +545,8 @@ typedef struct {
  * An infinity or NaN in a token's logits or gradients makes that token's dlogits and dx, and drouter_w, not finite.
  * Padding (a token of no sequence and without a chosen expert) has a zero gradient whatever its logits, dtopk_w
  * and x hold; x is not read where a token's gradient is zero.
- * T = 0 writes zeros to drouter_w (or leaves it, accumulating).  Results have a fixed order of sums. */
+ * T = 0 writes zeros to drouter_w (or leaves it, accumulating).  Results have a fixed order of sums, in fp32;
+ * a bf16 dx is the fp32 result rounded once. */
 moe_status_t moe_router_backward(const moe_config_t* cfg, int64_t T, const moe_sequences_t* sequences,
                                  const moe_router_backward_t* grads, void* ws, size_t ws_bytes, void* stream);
 

@@ -271,10 +271,9 @@ struct Pieces {
   uint32_t w[P][(EPL + 1) / 2];
   // where(e): where expert e's value lies in the first plane
   template <typename At>
-  __device__ __forceinline__ void store(uint16_t* base, int64_t plane, int lane, int planes, At where) const {
+  __device__ __forceinline__ void store(uint16_t* base, int64_t plane, int lane, At where) const {
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-      if (p >= planes) break;
 #pragma unroll
       for (int j = 0; j < Row<EPL>::NJ; ++j) {
         uint16_t* const at = base + p * plane + where(Row<EPL>::at(lane, j));
@@ -286,13 +285,12 @@ struct Pieces {
   }
 };
 
-// 16 columns of router_w, transposed, in scaled fp16 pieces: a thread takes 4 EPL consecutive experts of
-// a column; a plane is laid out in LDS and written in whole rows.
-template <int EPL>
-constexpr int SPLIT_WORDS = 16 * (EPL * 32 + 4);  // 16 rows of E / 2 words, 16 bytes apart
+// 16 columns of router_w, transposed, in scaled fp16 pieces: a thread takes N = 4 EPL consecutive experts of
+// a column, which lie side by side in the planes, 16 of them beside those of the next column.
 template <int EPL>
 __device__ __forceinline__ void split_weight(const DlogitsArgs& a, int block, uint32_t* lds) {
-  constexpr int E = EPL * 64, N = 4 * EPL, LD = E / 2 + 4;
+  constexpr int E = EPL * 64, N = 4 * EPL, V = N < 8 ? N / 2 : 4;  // words of a store
+  typedef uint32_t vec __attribute__((ext_vector_type(V)));
   const int col = threadIdx.x & 15, grp = threadIdx.x >> 4, h0 = block * 16;
   float v[N];
   uint32_t top = 0;
@@ -307,20 +305,18 @@ __device__ __forceinline__ void split_weight(const DlogitsArgs& a, int block, ui
   for (int g = 0; g < 16; ++g) top = max(top, lds[g * 16 + col]);
   const int ex = half_exponent(top);
   if (grp == 0) a.wexp[h0 + col] = ex;
-  uint32_t w[2][N / 2];
 #pragma unroll
-  for (int i = 0; i < N / 2; ++i) half_pieces(v[2 * i], v[2 * i + 1], ex, w[0][i], w[1][i]);
+  for (int i = 0; i < N; i += 2 * V) {
+    vec w[2];
 #pragma unroll
-  for (int p = 0; p < 2; ++p) {
-    if (p > a.pair) break;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < N / 2; i += 2) *(u32x2*)(lds + col * LD + grp * (N / 2) + i) = u32x2{w[p][i], w[p][i + 1]};
-    __syncthreads();
-    for (int c = threadIdx.x; c < 16 * (E / 8); c += 256) {
-      const int row = c / 2 % 16, at = c / 32 * 2 + c % 2;  // (in the planes' order: 32 lanes, half a block)
-      *(u32x4*)(a.wt + p * plane_size(a.H, E) + plane_at(h0 + row, at * 8, E)) = *(const u32x4*)(lds + row * LD + at * 4);
+    for (int j = 0; j < V; ++j) {
+      uint32_t hi, lo;
+      half_pieces(v[i + 2 * j], v[i + 2 * j + 1], ex, hi, lo);
+      w[0][j] = hi;
+      w[1][j] = lo;
     }
+#pragma unroll
+    for (int p = 0; p < 2; ++p) *(vec*)(a.wt + p * plane_size(a.H, E) + plane_at(h0 + col, grp * N + i, E)) = w[p];
   }
 }
 
@@ -339,14 +335,13 @@ __device__ __forceinline__ void split_weight(const DlogitsArgs& a, int block, ui
 template <int EPL>
 __global__ __launch_bounds__(256) void dlogits_kernel(DlogitsArgs a) {
   constexpr int E = EPL * 64;
-  __shared__ __align__(16) uint32_t lds[SPLIT_WORDS<EPL>];
+  __shared__ __align__(16) uint32_t lds[4 * E];  // a row of every wave, or a maximum of every thread
   __shared__ int tokens;
   if ((int)blockIdx.x < a.weight_blocks) {  // (first: they take longest)
     split_weight<EPL>(a, blockIdx.x, lds);
     return;
   }
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  static_assert(SPLIT_WORDS<EPL> >= 4 * E, "a row of every wave");
   float(*const rows)[E] = (float(*)[E])lds;
   const int64_t base = (int64_t)((int)blockIdx.x - a.weight_blocks) * 4 * a.run;
   Seq q{0, 0, 0};
@@ -464,14 +459,14 @@ __global__ __launch_bounds__(256) void dlogits_kernel(DlogitsArgs a) {
 #pragma unroll
         for (int k = 0; k < 3; ++k) p.w[k][i / 2] = x[k] >> 16 | y[k];
       }
-      p.store(a.bf, (int64_t)a.seq.T * E, lane, 3, [&](int e) { return t * E + e; });
+      p.store(a.bf, (int64_t)a.seq.T * E, lane, [&](int e) { return t * E + e; });
     }
     if (a.hf) {
       const int ex = half_exponent(top);
       Pieces<EPL, 2> p;
 #pragma unroll
       for (int i = 0; i < EPL; i += 2) half_pieces(d[i], i + 1 < EPL ? d[i + 1] : 0.f, ex, p.w[0][i / 2], p.w[1][i / 2]);
-      p.store(a.hf, plane_size(a.seq.T, E), lane, 1 + a.pair, [&](int e) { return plane_at(t, e, E); });
+      p.store(a.hf, plane_size(a.seq.T, E), lane, [&](int e) { return plane_at(t, e, E); });
       if (lane == 0) a.hexp[t] = ex;
     }
   }

@@ -297,11 +297,10 @@ struct DlogitsArgs {
   // the pieces that the products read (each NULL if not wanted), planes one behind the other
   uint16_t* bf;            // bf16 [3, T, E]
   uint8_t* live;           // with bf: [T], 1 where a token has a gradient, 0 where its row is zeros
-  int pair;                // fp16: both pieces (for a result in fp32), or the first alone
-  uint16_t* hf;            // fp16, 1 + pair planes of T rows (plane_at), row t times 2^hexp[t]
+  uint16_t* hf;            // fp16, two planes of T rows (plane_at), row t times 2^hexp[t]
   int32_t* hexp;           // [T]
   const float* w; int H;   // router_w [E, H], taken apart by the same launch (hf given)
-  uint16_t* wt;            // fp16, 1 + pair planes of H rows, row h times 2^wexp[h]
+  uint16_t* wt;            // fp16, two planes of H rows, row h times 2^wexp[h]
   int32_t* wexp;           // [H]
   int run, weight_blocks;  // tokens of a wave, workgroups that take router_w apart (set by the launch)
 };
@@ -312,7 +311,7 @@ struct RouterGradPlan {
   int tile;                  // square tiles: 128 or 64
   int nsplit, split_steps;   // d router_w: parts of the reduction over tokens, steps of 32 in each
 };
-RouterGradPlan router_grad_plan(int64_t T, int E, int H, bool dw, bool dx, bool f32);
+RouterGradPlan router_grad_plan(int64_t T, int E, int H, bool dw, bool dx);
 struct RouterGradArgs {
   RouterGradPlan plan;       // of these sizes and outputs
   int T, E, H;

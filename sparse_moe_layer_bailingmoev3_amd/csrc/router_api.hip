@@ -112,9 +112,7 @@ moe_status_t moe_router_workspace_size(const moe_config_t* cfg, int64_t T, int32
   if (n_seq < 1) return fail(MOE_ERR_INVALID_ARG, "n_seq %d must be >= 1", n_seq);
   if (n_seq > MAX_SEQ) return fail(MOE_ERR_UNSUPPORTED, "n_seq %d is above %d", n_seq, MAX_SEQ);
   int parts = 0;  // of any call
-  for (const bool dx : {false, true})
-    for (const bool f32 : {false, true})
-      parts = std::max(parts, moe::router_grad_plan(T, cfg->num_experts, cfg->hidden_size, true, dx, f32).nsplit);
+  for (const bool dx : {false, true}) parts = std::max(parts, moe::router_grad_plan(T, cfg->num_experts, cfg->hidden_size, true, dx).nsplit);
   const Layout L = layout(cfg, T, n_seq, parts);
   *bytes = std::max(L.balance, L.backward);
   return MOE_OK;
@@ -196,7 +194,7 @@ moe_status_t moe_router_backward(const moe_config_t* cfg, int64_t T, const moe_s
   const int64_t E = cfg->num_experts, K = cfg->num_experts_per_tok, H = cfg->hidden_size;
   const bool products = g->drouter_w || g->dx;
   moe::RouterGradPlan plan{};
-  if (products) plan = moe::router_grad_plan(T, (int)E, (int)H, g->drouter_w, g->dx, g->dx_dtype == MOE_DTYPE_FP32);
+  if (products) plan = moe::router_grad_plan(T, (int)E, (int)H, g->drouter_w, g->dx);
   const Layout L = layout(cfg, T, d.seq.n, plan.nsplit);
   if (products) MOE_TRY(check_ws(ws, ws_bytes, L.backward));
   Spans in, out;
@@ -230,7 +228,6 @@ moe_status_t moe_router_backward(const moe_config_t* cfg, int64_t T, const moe_s
     d.live = (uint8_t*)(w + L.live);
   }
   if (g->dx) {
-    d.pair = g->dx_dtype == MOE_DTYPE_FP32;
     d.hf = (uint16_t*)(w + L.hf);
     d.hexp = (int32_t*)(w + L.hexp);
     d.w = g->router_w;

@@ -8,10 +8,10 @@
 //     (Two rounded pieces lose 2.4e-6 in the norm, twice what a product in fp32 throughout loses.)
 //   * dx: both operands in fp16, each row of dl and each column of router_w scaled by a power of two
 //     that brings its largest value to 2^14..2^15, so that fp16's range covers 2^-38 of the largest; the
-//     result is scaled back.  In fp32: two pieces each (22 bits), hi hi + hi lo + lo hi; what is left out
-//     is 2^-22 of the magnitudes.  Three products, against six with three bf16 pieces each.  In bf16:
-//     the first pieces alone, rounded to 11 bits (2^-11 each at most, 3e-4 in the norm, where the result's own
-//     rounding to 8 bits is 1.7e-3).  One product.
+//     result is scaled back.  Two pieces each (22 bits), hi hi + hi lo + lo hi; what is left out is 2^-22 of
+//     the magnitudes.  Three products, against six with three bf16 pieces each.  A result in bf16 is the same
+//     sum rounded once.  (The first pieces alone, one product: 8192 tokens 115 instead of 144 us, 3e-4 in the norm,
+//     but a sum that cancels was off by any number of steps of bf16.)
 // The pieces are written by the kernel that computes dl (balance.hip), router_w's transposed.
 //
 // Both products are tiles of one launch, the weight gradient's (longer ones) first: the tokens' tiles,
@@ -60,9 +60,9 @@ __device__ __forceinline__ floatx16 mfma32(const u32x4& a, const u32x4& b, float
 }
 
 // what a tile of BR x BC takes from LDS
-template <int OP, int BR, int BC, int KS_, bool F32>
+template <int OP, int BR, int BC, int KS_>
 struct Stage {
-  static constexpr int KS = KS_, PX = OP == OP_DW ? 3 : F32 ? 2 : 1, PY = OP == OP_DX && F32 ? 2 : 1;  // planes
+  static constexpr int KS = KS_, PX = OP == OP_DW ? 3 : 2, PY = OP == OP_DW ? 1 : 2;  // planes
   static constexpr int X_BYTES = BR * KS * 2, Y_BYTES = BC * KS * 2, BYTES = PX * X_BYTES + PY * Y_BYTES;
 };
 
@@ -76,7 +76,7 @@ __device__ __forceinline__ int swz_cols(int row) { return W >= 128 ? (row & 3) <
 
 template <int OP, int BR, int BC, int WR, int WC, int KS, int NST, bool F32>
 __device__ __forceinline__ void router_tile(const RouterGradArgs& a, int block, int blocks, uint8_t* lds) {
-  typedef Stage<OP, BR, BC, KS, F32> St;
+  typedef Stage<OP, BR, BC, KS> St;
   constexpr int NW = WR * WC, PX = St::PX, PY = St::PY;
   constexpr int X_BYTES = St::X_BYTES, Y_BYTES = St::Y_BYTES, ST_BYTES = St::BYTES;
   constexpr int XN = X_BYTES / (NW * 1024), YN = Y_BYTES / (NW * 1024), LN = PX * XN + PY * YN;  // loads per wave
@@ -230,7 +230,7 @@ __device__ __forceinline__ void router_tile(const RouterGradArgs& a, int block, 
           for (int c = 0; c < CJ; ++c) {
             floatx16& s = acc[(u * (PX + PY - 1) + p) % NA][c][r];
             if constexpr (OP == OP_DW) s = mfma32<OP>(yf[0][c], xf[p], s);
-            else s = mfma32<OP>(yf[p == 2 ? PY - 1 : 0][c], xf[p == 2 ? 0 : p], s);
+            else s = mfma32<OP>(yf[p == 2][c], xf[p == 1], s);
           }
       }
     }
@@ -335,7 +335,7 @@ __global__ __launch_bounds__(256) void router_join_kernel(RouterGradArgs a) {
 
 template <int BR, int BC, int WR, int WC, int KS, int NW, int NX, bool F32>
 __global__ __launch_bounds__(WR* WC * 64, 2) void router_products_kernel(RouterGradArgs a, int dw_blocks) {
-  constexpr int DW = NW * Stage<OP_DW, BR, BC, KS, true>::BYTES, DX = NX * Stage<OP_DX, BR, BC, KS, F32>::BYTES;
+  constexpr int DW = NW * Stage<OP_DW, BR, BC, KS>::BYTES, DX = NX * Stage<OP_DX, BR, BC, KS>::BYTES;
   __shared__ __align__(16) uint8_t lds[DW > DX ? DW : DX];
   const int block = blockIdx.x;
   if (block < dw_blocks) router_tile<OP_DW, BR, BC, WR, WC, KS, NW, true>(a, block, dw_blocks, lds);
@@ -362,7 +362,7 @@ void run_products(const RouterGradArgs& a, hipStream_t s) {
 // 64 x 512 to 1024 x 2560.  Sides measured (us a call, 512 x 2560, fp32 dx):
 //   512 tokens:  128 26.4, 64 28.6     2048: 128 in 2 parts 50.5, 4 56.7; 64 62.4     8192: 128 148, 64 206
 //   512 tokens of 128 x 640: 64 in one part 14.5, 2 17.4; 4096: 64 in 8 parts 22.0, 128 24.6
-RouterGradPlan router_grad_plan(int64_t T, int E, int H, bool dw, bool dx, bool f32) {
+RouterGradPlan router_grad_plan(int64_t T, int E, int H, bool dw, bool dx) {
   struct Shape {
     int tile, wgs;
     float alone, full, end;
@@ -379,7 +379,7 @@ RouterGradPlan router_grad_plan(int64_t T, int E, int H, bool dw, bool dx, bool 
       if ((steps + per - 1) / per != n) continue;
       const double items = (double)dwt * n, load = std::min<double>(v.wgs, std::max(1.0, (items + dxt) / 256));
       const double step = std::max<double>(v.alone, v.full * load / v.wgs);
-      const double len = per * 3 * step + v.end, dx_len = dxt ? (E / 32) * (f32 ? 3 : 1) * step + v.end : 0;
+      const double len = per * 3 * step + v.end, dx_len = dxt ? (E / 32) * 3 * step + v.end : 0;
       const double c = std::max(std::ceil(items / places) * len, (items * len + dxt * dx_len) / places + .5 * dx_len) +
                        (n > 1 ? 5 + n * (double)E * H * 8 / 5e6 : 0);
       if (cost < 0 || c < cost) {

@@ -813,3 +813,25 @@ def test_gradient_table_outlives_a_plan_that_is_dropped():
     assert all(a.data_ptr() != address for a in again)
     torch.cuda.synchronize()
     assert abs(norm.item() - np.sqrt(300_000)) < 1e-2
+
+
+# ---- at the ends of the range ----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("T,E,H", [(1, 64, 128), (64, 512, 2560), (1333, 128, 640), (700, 1024, 256), (2500, 512, 640)], ids=str)
+def test_bf16_dx_is_rounded_once(T, E, H):
+    """dx in bf16 is the fp32 result rounded to bf16, also where a sum cancels: beside that rounding it may be off by
+    what dx in fp32 may be (operands in two fp16 pieces, sums in fp32), not by a share of the magnitudes summed."""
+    g = gen(30)
+    K, cfg = 8, config(E, 8, H)
+    x, rw, logits, idx, dw, counts, _, _, _ = backward_case(g, T, E, K, H, "one")
+    dl, dx, dx32 = torch.empty(T, E, device="cuda"), torch.empty(T, H, dtype=BF, device="cuda"), torch.empty(T, H, device="cuda")
+    for out in (dx, dx32):
+        moe.moe_router_backward(cfg, T, logits.cuda(), idx.cuda(), dtopk_w=dw.cuda(), counts=counts.cuda(), coef=3.0, dlogits=dl,
+                                router_w=rw.cuda(), dx=out, ws=workspace(cfg, T))
+    d, w = f64(dl), f64(rw)
+    want = d @ w
+    own = (3 * 2.0 ** -22 + 6 * E * U32) * (np.abs(d) @ np.abs(w))
+    lim = own + HALF_BF16 * (np.abs(want) + own) + 1e-37
+    err = np.abs(f64(dx) - want)
+    assert np.all(err <= lim), f"err/tol {np.max(err / lim):.1f}, {np.mean(err > lim):.2%} of the values"
+    assert torch.equal(dx, dx32.to(BF))
