@@ -341,6 +341,7 @@ moe_status_t moe_route_logits(const moe_config_t* cfg, int64_t T, const void* x,
   MOE_CHECK_PTR(logits, "logits");
   Layout L;
   if ((st = check_ws(cfg, T, ws, ws_bytes, &L)) != MOE_OK) return st;
+  if ((st = moe::check_route_apart(cfg, T, x, router_w, expert_bias, topk_idx, topk_w, logits, ws, L.total)) != MOE_OK) return st;
   const int E = cfg->num_experts;
   const moe::RouterPlan p = moe::router_plan(T, cfg->hidden_size, E);
   float* partial = p.nsplit > 1 ? (float*)at(ws, L.partial) : logits;

@@ -193,6 +193,11 @@ int device_cu_count();
 // the checks of a layer's configuration for T tokens; a refusal is recorded as the last error
 moe_status_t check_config(const moe_config_t* c, int64_t T);
 
+// whether what moe_route_logits writes (outputs, ws_bytes of workspace) is apart from its inputs and from each
+// other (router_api.hip)
+moe_status_t check_route_apart(const moe_config_t* c, int64_t T, const void* x, const float* router_w, const float* bias,
+                               const int32_t* topk_idx, const float* topk_w, const float* logits, const void* ws, size_t ws_bytes);
+
 // records `msg` as the calling thread's last error (moe_last_error) and returns nothing
 void set_last_error(const char* msg);
 

@@ -103,6 +103,22 @@ moe_status_t check_grad_plan(const moe_grad_plan_t* p, const void* image) {
 
 }  // namespace
 
+namespace moe {
+moe_status_t check_route_apart(const moe_config_t* c, int64_t T, const void* x, const float* router_w, const float* bias,
+                               const int32_t* topk_idx, const float* topk_w, const float* logits, const void* ws, size_t ws_bytes) {
+  const int64_t E = c->num_experts, K = c->num_experts_per_tok, H = c->hidden_size;
+  Spans in, out;
+  in.add(x, T * H, 2, "x");
+  in.add(router_w, E * H, 4, "router_w");
+  in.add(bias, E, 4, "expert_bias");
+  out.add(topk_idx, T * K, 4, "topk_idx");
+  out.add(topk_w, T * K, 4, "topk_w");
+  out.add(logits, T * E, 4, "logits");
+  out.add(ws, (int64_t)ws_bytes, 1, "workspace");
+  return all_apart(out, in);
+}
+}  // namespace moe
+
 extern "C" {
 
 moe_status_t moe_router_workspace_size(const moe_config_t* cfg, int64_t T, int32_t n_seq, size_t* bytes) {

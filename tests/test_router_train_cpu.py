@@ -117,6 +117,27 @@ def test_router_refusals(call, code, words):
     assert words in moe.load_library().moe_last_error()
 
 
+def route_logits(T=100, **kw):
+    d = dict(x=at(1), router_w=at(2), bias=at(7), idx=at(3), w=at(4), logits=at(5), ws=at(6))
+    d.update(kw)
+    return moe.load_library().moe_route_logits(ctypes.byref(config()), T, d["x"], d["router_w"], d["bias"], d["idx"], d["w"], d["logits"],
+                                               d["ws"], BIG, None)
+
+
+@needs_lib
+@pytest.mark.parametrize("given,words", [
+    (dict(logits=at(1)), b"logits overlaps x"), (dict(logits=at(2) + 64 * 128 * 4 - 16), b"logits overlaps router_w"),
+    (dict(bias=at(5) + 256), b"logits overlaps expert_bias"), (dict(idx=at(1) + 16), b"topk_idx overlaps x"),
+    (dict(w=at(2)), b"topk_w overlaps router_w"), (dict(w=at(3) + 16), b"topk_w overlaps topk_idx"),
+    (dict(logits=at(3)), b"logits overlaps topk_idx"), (dict(logits=at(4) + 1600 - 16), b"logits overlaps topk_w"),
+    (dict(ws=at(1)), b"workspace overlaps x"), (dict(logits=at(6)), b"workspace overlaps logits"),
+    (dict(idx=at(6) + 512), b"workspace overlaps topk_idx"), (dict(router_w=at(6) + 256), b"workspace overlaps router_w"),
+], ids=str)
+def test_route_logits_refuses_overlaps(given, words):
+    assert route_logits(**given) == INVALID
+    assert words in moe.load_library().moe_last_error()
+
+
 @needs_lib
 def test_workspace_size():
     cfg = config(E=512, K=8, H=2560)
