@@ -502,7 +502,7 @@ typedef struct {
 } moe_sequences_t;
 
 /* Bytes of device workspace (256-byte aligned) that moe_balance_loss and moe_router_backward need for T
- * tokens in n_seq sequences (host call).  It holds nothing between calls. */
+ * tokens in n_seq sequences, and for fewer tokens and sequences (host call).  It holds nothing between calls. */
 moe_status_t moe_router_workspace_size(const moe_config_t* cfg, int64_t T, int32_t n_seq, size_t* bytes);
 
 /* Balance loss: how evenly each sequence loads the experts.  With s = sigmoid(logits), sequence b of

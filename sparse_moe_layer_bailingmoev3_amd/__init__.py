@@ -753,7 +753,7 @@ def moe_route_logits(cfg, T, x, router_w, expert_bias, topk_idx, topk_w, logits,
 
 
 def moe_router_workspace_size(cfg, T, n_seq=1) -> int:
-    """Bytes of workspace that moe_balance_loss and moe_router_backward need."""
+    """Bytes of workspace that moe_balance_loss and moe_router_backward need for T tokens in n_seq sequences, or fewer."""
     n = ctypes.c_size_t()
     _check(load_library().moe_router_workspace_size(ctypes.byref(cfg), T, n_seq, ctypes.byref(n)))
     return n.value

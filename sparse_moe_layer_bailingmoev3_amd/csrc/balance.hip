@@ -492,6 +492,20 @@ int balance_chunk(int64_t T, int n_seq) {
   return c;
 }
 
+// Chunks do not grow with T where their size steps up: the most lie at the last T of each size.
+int64_t balance_chunks_bound(int64_t T, int n_seq) {
+  auto chunks = [&](int64_t t) {
+    const int c = balance_chunk(t, n_seq);
+    return (t + c - 1) / c;
+  };
+  int64_t most = std::max<int64_t>(chunks(T), 1);
+  for (int64_t c = 8; c <= 256; c *= 2) {  // the first T of chunks of c tokens
+    const int64_t from = std::max<int64_t>(c * n_seq, c > 32 ? c / 2 * 256 + 1 : 0);
+    if (from <= T) most = std::max(most, chunks(from - 1));
+  }
+  return most;
+}
+
 #define MOE_EPL(E, F)          \
   switch ((E) / WAVE) {        \
     case 1: F(1); break;       \

@@ -283,6 +283,7 @@ struct BalanceArgs {
   int32_t* counts; float* probs; float* loss;
 };
 int balance_chunk(int64_t T, int n_seq);
+int64_t balance_chunks_bound(int64_t T, int n_seq);  // chunks of any batch of T tokens or fewer
 hipError_t launch_balance(const BalanceArgs& a, hipStream_t s);
 
 // The fp16 planes of dx's operands lie in blocks of 32 rows by 16 experts, 1 KB each, the blocks of 32 rows
@@ -317,6 +318,7 @@ struct RouterGradPlan {
   int nsplit, split_steps;   // d router_w: parts of the reduction over tokens, steps of 32 in each
 };
 RouterGradPlan router_grad_plan(int64_t T, int E, int H, bool dw, bool dx);
+int router_grad_parts_bound(int64_t T, int E, int H);  // nsplit of any plan of T tokens or fewer
 struct RouterGradArgs {
   RouterGradPlan plan;       // of these sizes and outputs
   int T, E, H;

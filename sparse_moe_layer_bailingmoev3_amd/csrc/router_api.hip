@@ -38,10 +38,9 @@ struct Layout {
   size_t done, parts, psum, pcnt, balance;  // balance loss
   size_t bf, live, hf, wt, hexp, wexp, part, backward;  // backward pass
 };
-// parts: of the weight gradient (0: not split)
-Layout layout(const moe_config_t* c, int64_t T, int n_seq, int parts) {
-  const size_t E = c->num_experts;
-  const size_t chunk = moe::balance_chunk(T, n_seq), slots = std::max<size_t>((T + chunk - 1) / chunk, 1) + n_seq;
+// chunks: of the balance loss; parts: of the weight gradient (1: not split)
+Layout layout(const moe_config_t* c, int64_t T, int n_seq, int64_t chunks, int parts) {
+  const size_t E = c->num_experts, slots = (size_t)chunks + n_seq;
   Layout L{};
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -127,9 +126,9 @@ moe_status_t moe_router_workspace_size(const moe_config_t* cfg, int64_t T, int32
   if (!bytes) return fail(MOE_ERR_INVALID_ARG, "bytes must not be NULL");
   if (n_seq < 1) return fail(MOE_ERR_INVALID_ARG, "n_seq %d must be >= 1", n_seq);
   if (n_seq > MAX_SEQ) return fail(MOE_ERR_UNSUPPORTED, "n_seq %d is above %d", n_seq, MAX_SEQ);
-  int parts = 0;  // of any call
-  for (const bool dx : {false, true}) parts = std::max(parts, moe::router_grad_plan(T, cfg->num_experts, cfg->hidden_size, true, dx).nsplit);
-  const Layout L = layout(cfg, T, n_seq, parts);
+  // of any call, also for fewer tokens, of which some take more parts or chunks
+  const Layout L = layout(cfg, T, n_seq, moe::balance_chunks_bound(T, n_seq),
+                          moe::router_grad_parts_bound(T, cfg->num_experts, cfg->hidden_size));
   *bytes = std::max(L.balance, L.backward);
   return MOE_OK;
 }
@@ -150,7 +149,8 @@ moe_status_t moe_balance_loss(const moe_config_t* cfg, int64_t T, const moe_sequ
   MOE_TRY(need(probs, "probs"));
   MOE_TRY(need(loss, "loss", 4));
   const int64_t E = cfg->num_experts, K = cfg->num_experts_per_tok, B = a.seq.n;
-  const Layout L = layout(cfg, T, a.seq.n, 0);
+  a.chunk = moe::balance_chunk(T, a.seq.n);
+  const Layout L = layout(cfg, T, a.seq.n, std::max<int64_t>((T + a.chunk - 1) / a.chunk, 1), 1);
   MOE_TRY(check_ws(ws, ws_bytes, L.balance));
   Spans in, out;
   in.add(logits, T * E, 4, "logits");
@@ -167,7 +167,6 @@ moe_status_t moe_balance_loss(const moe_config_t* cfg, int64_t T, const moe_sequ
   a.coef = coef;
   a.logits = logits;
   a.topk_idx = topk_idx;
-  a.chunk = moe::balance_chunk(T, a.seq.n);
   a.done = (int*)(w + L.done);
   a.part = (double*)(w + L.parts);
   a.psum = (float*)(w + L.psum);
@@ -211,7 +210,7 @@ moe_status_t moe_router_backward(const moe_config_t* cfg, int64_t T, const moe_s
   const bool products = g->drouter_w || g->dx;
   moe::RouterGradPlan plan{};
   if (products) plan = moe::router_grad_plan(T, (int)E, (int)H, g->drouter_w, g->dx);
-  const Layout L = layout(cfg, T, d.seq.n, plan.nsplit);
+  const Layout L = layout(cfg, T, d.seq.n, 0, plan.nsplit);
   if (products) MOE_TRY(check_ws(ws, ws_bytes, L.backward));
   Spans in, out;
   in.add(g->logits, T * E, 4, "logits");

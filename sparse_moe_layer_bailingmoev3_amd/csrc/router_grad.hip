@@ -355,6 +355,18 @@ void run_products(const RouterGradArgs& a, hipStream_t s) {
 
 }  // namespace
 
+// Parts of d router_w's reduction over tokens that a plan takes at most: so many that its tiles are all under way
+// at once (two workgroups a compute unit), up to 32.  More would wait for places, and cost their bytes besides: no
+// plan of 64 x 128 to 1024 x 7168 and 1 to 300,000 tokens priced more as best.
+constexpr int PRODUCT_PLACES = 512, MAX_PARTS = 32;
+static int64_t most_parts(int64_t steps, int64_t tiles) {
+  return std::min<int64_t>(std::min<int64_t>(steps, MAX_PARTS), std::max<int64_t>(PRODUCT_PLACES / std::max<int64_t>(tiles, 1), 1));
+}
+static int64_t token_steps(int64_t T) { return std::max<int64_t>((T + 31) / 32, 1); }
+int router_grad_parts_bound(int64_t T, int E, int H) {
+  return (int)most_parts(token_steps(T), (int64_t)((E + 127) / 128) * ((H + 127) / 128));
+}
+
 // Tile size and the parts of the weight gradient's reduction, by price: a step of one product of a tile
 // takes `full` us on a place with all `wgs` places of its compute unit taken, `alone` at least; `end` is a tile's
 // beginning and end, 5 us what a third launch costs, besides the parts' bytes.  The weight gradient's items
@@ -368,13 +380,13 @@ RouterGradPlan router_grad_plan(int64_t T, int E, int H, bool dw, bool dx) {
     float alone, full, end;
   };
   static const Shape shapes[2] = {{128, 2, .25f, .45f, 4.f}, {64, 2, .05f, .17f, 2.5f}};
-  const int64_t steps = std::max<int64_t>((T + 31) / 32, 1);
+  const int64_t steps = token_steps(T);
   RouterGradPlan best{};
   double cost = -1;
   for (const Shape& v : shapes) {
-    const double places = 256.0 * v.wgs;
+    const double places = PRODUCT_PLACES;
     const int64_t ct = (H + v.tile - 1) / v.tile, dwt = dw ? (E + v.tile - 1) / v.tile * ct : 0, dxt = dx ? (T + v.tile - 1) / v.tile * ct : 0;
-    for (int64_t n = 1; n <= (dw ? std::min<int64_t>(steps, 32) : 1); ++n) {
+    for (int64_t n = 1; n <= (dw ? most_parts(steps, dwt) : 1); ++n) {
       const int64_t per = (steps + n - 1) / n;
       if ((steps + per - 1) / per != n) continue;
       const double items = (double)dwt * n, load = std::min<double>(v.wgs, std::max(1.0, (items + dxt) / 256));

@@ -150,6 +150,36 @@ def test_workspace_size():
             moe.moe_router_workspace_size(cfg, 64, bad)
 
 
+@needs_lib
+@pytest.mark.parametrize("E,H", [(64, 128), (64, 2560), (128, 640), (512, 2560), (1024, 128), (1024, 4096)])
+def test_workspace_size_never_falls(E, H):
+    cfg = config(E=E, H=H)
+    edges = [32 * i + d for i in range(300) for d in (0, 1)] + [c * n + d for c in (4, 8, 16, 32, 64, 128, 256) for n in (1, 7, 256, 1000)
+                                                               for d in (-1, 0, 1)]
+    Ts = sorted({*edges, *range(0, 70000, 997), 10**6, 10**7})
+    before = None
+    for n in (1, 2, 7, 64, 65, 1000, 65536):
+        sizes = [moe.moe_router_workspace_size(cfg, T, n) for T in Ts]
+        assert all(a <= b for a, b in zip(sizes, sizes[1:])), [t for t, a, b in zip(Ts[1:], sizes, sizes[1:]) if a > b][:3]
+        assert before is None or all(a <= b for a, b in zip(before, sizes))
+        before = sizes
+
+
+@needs_lib
+@pytest.mark.parametrize("E,H", [(64, 128), (128, 640), (512, 2560), (1024, 256)])
+def test_workspace_for_the_longest_batch_serves_every_shorter_one(E, H):
+    """A call that a workspace satisfies goes on to the next check: here, that an output lies on an input."""
+    cfg = config(E=E, H=H)
+    for T, n in ((2000, 3), (8200, 40), (33000, 1), (70000, 300)):
+        size = moe.moe_router_workspace_size(cfg, T, n)
+        for t in sorted({*range(1, T + 1, max(1, T // 400)), *(c * 256 for c in (32, 64, 128) if c * 256 <= T), T}):
+            q = seqs(n_seq=n) if n > 1 else None
+            # (addresses of one sequence and of n: apart from each other for every size here)
+            assert balance(cfg, t, q, probs=at(1), n=size) == INVALID
+            for kw in (dict(), dict(dx=None), dict(drouter_w=None), dict(dx_dtype=1)):
+                assert backward(cfg, t, q, dlogits=at(1), n=size, **kw) == INVALID
+
+
 # ---- norm ------------------------------------------------------------------------------------------
 
 def grad_plan(tensors, image=None, n=0, plan=True, count=None):
