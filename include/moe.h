@@ -576,7 +576,7 @@ moe_status_t moe_grad_plan(int64_t n_tensors, const moe_grad_tensor_t* tensors, 
  * scale max_norm / norm: what the gradients are multiplied with so that their norm is at most max_norm
  * (moe_adamw_step's grad_scale, or moe_grad_clip).  scale: of the gradients as they lie, 1 / micro-batches
  * for sums over micro-batches.  max_norm may be infinite.  Squares are added so that no finite gradient
- * overflows or vanishes; an infinite gradient makes norm infinite and coef 0, a NaN both NaN.
+ * overflows or vanishes; an infinite gradient makes norm infinite and coef 0 whatever max_norm, a NaN both NaN.
  *   norm, coef  device fp32 [1] (coef may be NULL)
  *   ws          device, 256-byte aligned, plan->workspace_bytes; holds nothing between calls
  * Memory that does not hold the plan's image is recognised as by moe_adamw_step: nothing is written. */

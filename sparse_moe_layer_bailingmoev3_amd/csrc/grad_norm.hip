@@ -159,8 +159,8 @@ __global__ __launch_bounds__(1024) void grad_norm_finish_kernel(GradArgs a, int 
     for (int w = 0; w < 16; ++w) s += sums[w];
     const double norm = fabs(a.scale) * sqrt(s);
     *a.norm = (float)norm;
-    // (a NaN norm gives a NaN coefficient, an infinite one zero)
-    if (a.coef_out) *a.coef_out = (float)(a.scale * (norm <= a.max_norm ? 1.0 : a.max_norm / norm));
+    // (a NaN norm gives a NaN coefficient, an infinite one zero, also where max_norm is infinite)
+    if (a.coef_out) *a.coef_out = (float)(a.scale * (isinf(norm) ? 0.0 : norm <= a.max_norm ? 1.0 : a.max_norm / norm));
   }
 }
 

@@ -835,3 +835,15 @@ def test_bf16_dx_is_rounded_once(T, E, H):
     err = np.abs(f64(dx) - want)
     assert np.all(err <= lim), f"err/tol {np.max(err / lim):.1f}, {np.mean(err > lim):.2%} of the values"
     assert torch.equal(dx, dx32.to(BF))
+
+
+@pytest.mark.parametrize("max_norm", [0.0, 1.0, float("inf")])
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf")], ids=str)
+def test_infinite_gradient_has_a_coefficient_of_zero(bad, max_norm):
+    grads = [torch.ones(100000, device="cuda"), torch.ones(9, dtype=BF, device="cuda")]
+    grads[1][3] = bad
+    plan = moe.MoEGradPlan(grads)
+    norm, coef = torch.empty(1, device="cuda"), torch.empty(1, device="cuda")
+    ws = torch.empty(plan.workspace_size, dtype=torch.uint8, device="cuda")
+    moe.moe_grad_norm(plan, max_norm, norm, coef, ws, scale=0.5)
+    assert np.isposinf(norm.item()) and coef.item() == 0
