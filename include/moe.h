@@ -511,7 +511,7 @@ moe_status_t moe_router_workspace_size(const moe_config_t* cfg, int64_t T, int32
  *   probs[b,e]  = mean over b's tokens of s_te / sum_j s_tj
  *   loss        = coef sum_b (n_b / N) sum_e f_be probs[b,e],   f_be = E counts[b,e] / (K n_b)
  * (coef for a perfectly even load).  An empty sequence has zeros and no part in the loss; without any
- * token the loss is 0.  A token whose scores are all zero counts as zeros.
+ * token the loss is 0.  A token whose scores are all zero (logits below -131) counts as zeros.
  *   sequences  host pointer, or NULL: one sequence of all tokens
  *   counts     device int32 [n_seq,E]; with one sequence the first E entries of moe_dispatch's
  *   probs      device fp32 [n_seq,E]      loss device fp32 [1]

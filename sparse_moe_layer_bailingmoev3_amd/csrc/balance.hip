@@ -35,16 +35,35 @@ __device__ __forceinline__ void balance_run(const BalanceArgs& a, int lo, int hi
     float l[AHEAD][EPL];
 #pragma unroll
     for (int k = 0; k < AHEAD; ++k) Row<EPL>::load(a.logits + (int64_t)min(t + k, hi - 1) * E, lane, l[k]);
+    float total[AHEAD], least = 1.f;
 #pragma unroll
     for (int k = 0; k < AHEAD; ++k) {
-      float total = 0.f;
+      total[k] = 0.f;
 #pragma unroll
       for (int i = 0; i < EPL; ++i) {
         l[k][i] = score_of(l[k][i]).s;
-        total += l[k][i];
+        total[k] += l[k][i];
       }
-      total = wave_sum(total);
-      const float inv = total == 0.f || t + k >= hi ? 0.f : 1.0f / total;
+      total[k] = wave_sum(total[k]);
+      least = fminf(least, total[k]);
+    }
+    if (least < SCORES_TINY) {
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k) {
+        if (!(total[k] < SCORES_TINY)) continue;
+        Row<EPL>::load(a.logits + (int64_t)min(t + k, hi - 1) * E, lane, l[k]);
+        total[k] = 0.f;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+          l[k][i] = tiny_score(l[k][i]);
+          total[k] += l[k][i];
+        }
+        total[k] = wave_sum(total[k]);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      const float inv = total[k] == 0.f || t + k >= hi ? 0.f : 1.0f / total[k];
 #pragma unroll
       for (int i = 0; i < EPL; ++i) acc[i] = t + k < hi ? __builtin_fmaf(l[k][i], inv, acc[i]) : acc[i];
     }
@@ -398,15 +417,29 @@ __global__ __launch_bounds__(256) void dlogits_kernel(DlogitsArgs a) {
       }
       if (b < a.seq.n && t >= q.begin && t < q.end) {
         float total = 0.f, load = 0.f;
+        auto add = [&]() {
+          total = load = 0.f;
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-          total += s[i].s;
-          load += f[i] * s[i].s;
+          for (int i = 0; i < EPL; ++i) {
+            total += s[i].s;
+            load += f[i] * s[i].s;
+          }
+          total = wave_sum(total);
+          load = wave_sum(load);
+        };
+        add();
+        if (total < SCORES_TINY) {
+#pragma unroll
+          for (int i = 0; i < EPL; ++i) s[i].s = tiny_score(l[i]);
+          add();
+          // shares in place of scores: a large gradient times this sum's reciprocal may leave fp32's range
+          const float part = total == 0.f ? 0.f : 1.0f / total;
+#pragma unroll
+          for (int i = 0; i < EPL; ++i) s[i].s *= part;
+          load *= part;
+          total = 1.f;
         }
-        total = wave_sum(total);
-        load = wave_sum(load);
-        const float inv = total == 0.f ? 0.f : 1.0f / total;
-        const float mean = load * inv, g = g0 * inv;
+        const float inv = 1.0f / total, mean = load * inv, g = g0 * inv;
 #pragma unroll
         for (int i = 0; i < EPL; ++i) d[i] = g * (f[i] - mean) * s[i].s * s[i].r;
       }
@@ -417,16 +450,21 @@ __global__ __launch_bounds__(256) void dlogits_kernel(DlogitsArgs a) {
       Row<EPL>::store(rows[wave], lane, l);
       asm volatile("" ::: "memory");
       Score k{0.f, 0.f};
-      float g = 0.f, v = 0.f;
+      float g = 0.f, v = 0.f, chosen = 0.f;
       if (e >= 0) {
-        k = score_of(rows[wave][e]);
+        chosen = rows[wave][e];
+        k = score_of(chosen);
         g = dw * a.scale;
       }
       const float zero[EPL] = {};
       asm volatile("" ::: "memory");
       Row<EPL>::store(rows[wave], lane, zero);
       if (a.norm) {
-        const float total = lane_of(row_sum(k.s), 0);  // (K <= 16: one row of lanes)
+        float total = lane_of(row_sum(k.s), 0);  // (K <= 16: one row of lanes)
+        if (total < SCORES_TINY) {
+          k.s = e >= 0 ? tiny_score(chosen) : 0.f;
+          total = lane_of(row_sum(k.s), 0);
+        }
         const float share = total == 0.f ? 0.f : k.s / total;
         const float mean = lane_of(row_sum(g * share), 0);
         v = (g - mean) * share * k.r;

@@ -6,23 +6,37 @@
 
 namespace moe {
 
-// sigmoid of a logit and its complement, both to a few ulp of themselves whatever their size: from
-// e = exp(-|l|) <= 1 the larger is 1 / (1 + e), the smaller e times that.  exp through the hardware's
-// power of two; the product |l| log2(e) is carried with its rounding (else its 2^-24 would be
-// multiplied by |l|).
+// exp(a) 2^up for a <= 0, through the hardware's power of two, which gives zero below fp32's normal range.  The
+// product a log2(e) is carried with its rounding (else its 2^-24 would be multiplied by a).
+__device__ __forceinline__ float exp_scaled(float a, float up) {
+  a = a < -200.f ? -200.f : a;  // (far below what any use can tell from zero; NaN stays)
+  const float t = a * 1.44269504f;
+  const float lo = __builtin_fmaf(a, 1.44269504f, -t) + a * 1.92596299e-8f;
+  float at;
+  {
+#pragma clang fp contract(off)
+    at = t + up;  // (exact; as one operation with the product it would leave nothing for `lo` to correct)
+  }
+  const float e = __builtin_amdgcn_exp2f(at);
+  return __builtin_fmaf(e, lo * 0.693147181f, e);
+}
+
+// sigmoid of a logit and its complement, both to a few ulp of themselves in fp32's normal range, zero below it
+// (from |l| = 87.3 on): from e = exp(-|l|) <= 1 the larger is 1 / (1 + e), the smaller e times that.
 struct Score {
   float s, r;  // sigmoid(l), 1 - sigmoid(l)
 };
 __device__ __forceinline__ Score score_of(float l) {
-  float a = -fabsf(l);
-  a = a < -200.f ? -200.f : a;  // e is zero from -104 on; NaN stays
-  const float t = a * 1.44269504f;
-  const float lo = __builtin_fmaf(a, 1.44269504f, -t) + a * 1.92596299e-8f;
-  float e = __builtin_amdgcn_exp2f(t);
-  e = __builtin_fmaf(e, lo * 0.693147181f, e);
+  const float e = exp_scaled(-fabsf(l), 0.f);
   const float big = __builtin_amdgcn_rcpf(1.0f + e), small = e * big;
   return l < 0.f ? Score{small, big} : Score{big, small};
 }
+
+// Quotients of scores whose sum is below SCORES_TINY are taken from 2^64 times the scores, or fp32 would hold
+// the scores in few bits or none while their quotients are ordinary numbers.  Every logit is below -44 then: the
+// sigmoid is exp(l), in full precision down to l = -131 and zero below that.
+constexpr float SCORES_TINY = 0x1p-64f;
+__device__ __forceinline__ float tiny_score(float l) { return exp_scaled(l, 64.f); }
 
 // sum over the wave, in every lane: rows of 16 lanes by lane permutations (xor 1, xor 2, mirrors of 8
 // and 16), the four rows by lane reads

@@ -847,3 +847,32 @@ def test_infinite_gradient_has_a_coefficient_of_zero(bad, max_norm):
     ws = torch.empty(plan.workspace_size, dtype=torch.uint8, device="cuda")
     moe.moe_grad_norm(plan, max_norm, norm, coef, ws, scale=0.5)
     assert np.isposinf(norm.item()) and coef.item() == 0
+
+
+@pytest.mark.parametrize("centre", [-60.0, -86.0, -88.0, -95.0, -103.0, -120.0])
+@pytest.mark.parametrize("E,K", [(64, 4), (512, 8), (1024, 16)])
+@pytest.mark.parametrize("T", [40, 700])
+def test_tokens_of_tiny_scores(T, E, K, centre):
+    """Shares are quotients of scores: they do not depend on whether fp32 holds the scores themselves (nor a large
+    gradient times a score's reciprocal).  Every third token is an ordinary one."""
+    g = gen(31)
+    cfg = config(E, K)
+    logits, idx, dw = torch.randn(T, E, generator=g) * 2, ids(g, T, E, K), torch.randn(T, K, generator=g)
+    logits[torch.arange(T) % 3 > 0] += centre
+    off, lens = sequences("padded", T)
+    B = len(off) - 1
+    o, n = on_gpu(off, lens)
+    counts, probs, loss = torch.empty(B, E, dtype=I32, device="cuda"), torch.empty(B, E, device="cuda"), torch.empty(1, device="cuda")
+    moe.moe_balance_loss(cfg, T, logits.cuda(), idx.cuda(), 0.25, counts, probs, loss, workspace(cfg, T, B), seq_offsets=o, seq_lens=n)
+    want = orc.balance_loss(f64(logits), idx.numpy(), K, 0.25, off, lens)
+    assert np.array_equal(counts.cpu().numpy(), want.counts)
+    rel = 2 * SCORE + (E / 64 + 8) * U32 + 264 * U32  # (as in test_balance_loss)
+    assert np.all(np.abs(f64(probs) - want.probs) <= rel * want.probs + 1e-37)
+    assert abs(loss.item() - want.loss) <= (rel + 4 * U32) * abs(want.loss)
+    dl = torch.empty(T, E, device="cuda")
+    scale = torch.tensor([65536.0], device="cuda")
+    for mix in (None, dw):
+        moe.moe_router_backward(cfg, T, logits.cuda(), idx.cuda(), dtopk_w=None if mix is None else mix.cuda(), counts=counts, coef=10.0,
+                                dloss=scale, seq_offsets=o, seq_lens=n, dlogits=dl)
+        check_dlogits(dl, orc.router_backward(f64(logits), idx.numpy(), K, 1, 2.5, None if mix is None else f64(mix), want.counts,
+                                              10.0 * 65536.0, off, lens))
