@@ -345,7 +345,8 @@ __global__ __launch_bounds__(WR* WC * 64, 2) void router_products_kernel(RouterG
 template <int BR, int BC, int WR, int WC, int KS, int NW, int NX>
 void run_products(const RouterGradArgs& a, hipStream_t s) {
   auto blocks = [&](int64_t rows, int n) { return (int)(((rows + BR - 1) / BR * ((a.H + BC - 1) / BC) * n + 7) / 8 * 8); };
-  const int dw = a.dw ? blocks(a.E, a.plan.nsplit) : 0, dx = a.dx && a.T > 0 ? blocks(a.T, 1) : 0;
+  // (no tokens: zeros, or what lay there to the bit)
+  const int dw = a.dw && (a.T > 0 || !a.acc_w) ? blocks(a.E, a.plan.nsplit) : 0, dx = a.dx && a.T > 0 ? blocks(a.T, 1) : 0;
   if (dw + dx == 0) return;
   if (a.dx_f32)
     hipLaunchKernelGGL((router_products_kernel<BR, BC, WR, WC, KS, NW, NX, true>), dim3((unsigned)(dw + dx)), dim3(WR * WC * 64), 0, s, a, dw);

@@ -876,3 +876,14 @@ def test_tokens_of_tiny_scores(T, E, K, centre):
                                 dloss=scale, seq_offsets=o, seq_lens=n, dlogits=dl)
         check_dlogits(dl, orc.router_backward(f64(logits), idx.numpy(), K, 1, 2.5, None if mix is None else f64(mix), want.counts,
                                               10.0 * 65536.0, off, lens))
+
+
+def test_no_tokens_leave_the_bits_of_a_gradient_added_to():
+    cfg = config(64, 4)
+    z = lambda *s, **k: torch.zeros(*s, device="cuda", **k)  # noqa: E731
+    drw = z(64, 128)
+    drw[::2] = -0.0
+    before = drw.view(I32).clone()
+    moe.moe_router_backward(cfg, 0, z(0, 64), z(0, 4, dtype=I32), dtopk_w=z(0, 4), x=z(0, 128, dtype=BF), router_w=z(64, 128),
+                            drouter_w=drw, accumulate_w=True, dx=z(0, 128), ws=workspace(cfg, 0))
+    assert torch.equal(drw.view(I32), before)
