@@ -542,7 +542,9 @@ typedef struct {
  * itself has no gradient, nor has the bias) and through the balance loss, whose counts are constants:
  *   dlogits = dw/dl^T dtopk_w + dloss dloss/dl;   drouter_w = dlogits^T x;   dx = dlogits router_w
  * dtopk_w or counts must be given, and one of the outputs.  ws may be NULL if only dlogits is wanted.
- * An infinity or NaN in a token's logits or gradients makes that token's dlogits and dx, and drouter_w, not finite.
+ * A token's dlogits and dx, and drouter_w, are not finite where its gradient depends on a NaN or an infinite gradient:
+ * at a chosen expert in its logits (NaN) or dtopk_w, and with a balance loss in any of its logits (NaN) or in dloss.
+ * An infinite logit is a score of one or zero, without a gradient of its own, and shows nowhere.
  * Padding (a token of no sequence and without a chosen expert) has a zero gradient whatever its logits, dtopk_w
  * and x hold; x is not read where a token's gradient is zero.
  * T = 0 writes zeros to drouter_w (or leaves it, accumulating).  Results have a fixed order of sums, in fp32;

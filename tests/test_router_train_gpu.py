@@ -887,3 +887,32 @@ def test_no_tokens_leave_the_bits_of_a_gradient_added_to():
     moe.moe_router_backward(cfg, 0, z(0, 64), z(0, 4, dtype=I32), dtopk_w=z(0, 4), x=z(0, 128, dtype=BF), router_w=z(64, 128),
                             drouter_w=drw, accumulate_w=True, dx=z(0, 128), ws=workspace(cfg, 0))
     assert torch.equal(drw.view(I32), before)
+
+
+@pytest.mark.parametrize("norm", [0, 1])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")], ids=str)
+def test_logits_that_are_not_finite(bad, norm):
+    """A NaN shows where the token's gradient depends on it: at a chosen expert, with a balance loss at any.  An infinity
+    is a score of one or zero like any other and shows nowhere."""
+    g = gen(32)
+    T, E, K, H = 70, 64, 4, 128
+    cfg = config(E, K, H, norm=norm)
+    x, rw, clean, idx, dw, counts, _, _, _ = backward_case(g, T, E, K, H, "one")
+    chosen, other = int(idx[33, 1]), int(next(e for e in range(E) if e not in idx[33].tolist()))
+    for e in (chosen, other):
+        logits = clean.clone()
+        logits[33, e] = bad
+        for mix, balance in ((True, False), (False, True), (True, True)):
+            dl, drw, dx = torch.empty(T, E, device="cuda"), torch.empty(E, H, device="cuda"), torch.empty(T, H, device="cuda")
+            moe.moe_router_backward(cfg, T, logits.cuda(), idx.cuda(), dtopk_w=dw.cuda() if mix else None,
+                                    counts=counts.cuda() if balance else None, coef=0.5, dlogits=dl, x=x.cuda(), router_w=rw.cuda(),
+                                    drouter_w=drw, dx=dx, ws=workspace(cfg, T))
+            shows = np.isnan(bad) and (balance or e == chosen)
+            assert bool(torch.isfinite(dl[33]).all()) != shows and bool(torch.isfinite(drw).all()) != shows
+            assert bool(torch.isfinite(dx[33]).all()) != shows
+            rest = (torch.arange(T) != 33).cuda()
+            assert torch.isfinite(dl[rest]).all() and torch.isfinite(dx[rest]).all()
+            if not np.isnan(bad):
+                want = orc.router_backward(f64(logits), idx.numpy(), K, norm, 2.5, f64(dw) if mix else None,
+                                           counts.numpy() if balance else None, 0.5, None, None)
+                check_dlogits(dl, want)
