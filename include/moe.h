@@ -134,7 +134,8 @@ typedef struct {
   const void* shared_down;
 } moe_expert_weights_t;
 
-/* Bytes of device workspace that any entry point needs for T tokens (host call). */
+/* Bytes of device workspace that any entry point needs for T tokens (host call).  More tokens may need less: a
+ * workspace for several T takes the largest of their sizes. */
 moe_status_t moe_workspace_size(const moe_config_t* cfg, int64_t T, size_t* bytes);
 
 /* Router (sections 三.1-三.3 and 四 of the routing walk-through page).
@@ -585,8 +586,9 @@ moe_status_t moe_grad_plan(int64_t n_tensors, const moe_grad_tensor_t* tensors, 
 moe_status_t moe_grad_norm(const moe_grad_plan_t* plan, const void* image, double max_norm, double scale, float* norm,
                            float* coef, void* ws, size_t ws_bytes, void* stream);
 
-/* out = *coef grad for every tensor of the plan, rounded once to out's type.  In place, a coef of 1 is
- * found on the device and nothing is read or written.  coef lies outside the plan's arrays. */
+/* out = *coef grad for every tensor of the plan: the product in fp32, then rounded to out's type (an infinite
+ * gradient times 0 is NaN).  In place, a coef of 1 is found on the device and nothing is read or written.  coef, and
+ * what moe_grad_norm writes, lie outside the plan's arrays (whose addresses only the image holds: not checked). */
 moe_status_t moe_grad_clip(const moe_grad_plan_t* plan, const void* image, const float* coef, void* stream);
 
 /* Static text for a status code. */

@@ -6,7 +6,7 @@
 // The gradients are read once, in chunks of GRAD_CHUNK values that a table lists; the workgroups are
 // as many as fit the card and take every grid-th chunk, each leaving one sum in 64 bits; a second
 // launch of one workgroup adds them in order.  Squares are summed in fp32 within a lane's share of a
-// chunk (64 values), in 64 bits from there on.  A share whose sum leaves 2^-60 .. 2^120 (all zeros
+// chunk (32 values), in 64 bits from there on.  A share whose sum leaves 2^-60 .. 2^120 (all zeros
 // apart) is read again with squares in 64 bits: gradients whose squares overflow or vanish in fp32 have
 // a norm too.
 //
