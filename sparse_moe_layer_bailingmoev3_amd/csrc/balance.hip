@@ -13,8 +13,8 @@
 //
 // Counts are integers: LDS atomics, whose order does not matter.
 //
-// What bounds it, on one MI355X: 8192 tokens of 512 experts 13.2 us, of which the logits' 17 MB are 3.  The
-// first launch takes 6.1 (about 2.8 of vector work, 80 cycles a score, behind the first loads), the second 5.6,
+// What bounds it, on one MI355X: 8192 tokens of 512 experts 13.8 us, of which the logits' 17 MB are 3.  The
+// first launch takes 6.2 (about 2.8 of vector work, 80 cycles a score, behind the first loads), the second 6.0,
 // a chain of latencies: the sequence's ends, its slots, the parts of the loss, the counter (2.5 with what
 // follows it), the parts again.
 #include "router_scores.h"
@@ -349,7 +349,7 @@ __device__ __forceinline__ void split_weight(const DlogitsArgs& a, int block, ui
 // asked for, and in the 16-bit pieces that the products take; other workgroups take router_w apart meanwhile.
 //
 // What bounds it, on one MI355X: 8192 tokens of 512 experts with both products' pieces 15.5-18 us, 28 MB read
-// and 50 written at the copy's rate; 16,384 tokens of 256 experts, fp32 alone, 11.5 us against 5 of traffic: latency
+// and 50 written at the copy's rate; 16,384 tokens of 256 experts, fp32 alone, 12.0 us against 5 of traffic: latency
 // and vector work of four tokens a wave.  router_w's part (512 x 2560) takes 8 alone, so it goes first.
 template <int EPL>
 __global__ __launch_bounds__(256) void dlogits_kernel(DlogitsArgs a) {
@@ -518,7 +518,7 @@ __global__ __launch_bounds__(256) void dlogits_kernel(DlogitsArgs a) {
 constexpr int BALANCE_SMALL_T = 256, BALANCE_SMALL_SEQ = 4;
 constexpr int64_t BALANCE_SMALL = 32768, BALANCE_SMALL_RUNS = 65536;
 
-// Tokens of a chunk: about one workgroup a compute unit, from 32 (four a wave, whose loads are under way at
+// Tokens of a chunk: about one workgroup for each of the MI355X's 256 compute units, from 32 (four a wave, whose loads are under way at
 // once) to 256.  Sides measured (us a call, 512 experts): 8192 tokens 16 14.2, 32 12.8, 64 15.1; 16,384 32
 // 17.7, 64 15.2, 128 20.4; 32,768 64 23.8, 128 22.5, 256 32.3; 200,000 128 107, 256 105.  But no longer than a
 // sequence on average, down to 4, as a workgroup takes its sequences one after another: 65 tokens in 16

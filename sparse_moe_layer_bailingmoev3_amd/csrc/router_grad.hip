@@ -27,14 +27,15 @@
 // back to back (the card's power then holds its clock down): 129 GFLOP of products, 1.06 to 0.77 PFLOP/s (the
 // library's bf16 product reaches 1.31 in short runs), matrix units busy 48 % of the cycles; LDS reads of a
 // step (16 KB a wave for 24 products of 32 x 32 x 16) and what the loads write there take about as long as the
-// products, no bank conflicts.  d router_w alone 48 us (6400 tokens), dx alone 54 in fp32, 26 in bf16.
+// products, no bank conflicts.  Calls for one product, 6400 tokens: d router_w 70 us, dx 59 in fp32, 54 in bf16.
 // Measured and not kept: 256 x 256 tiles, as 16 waves of 64 x 64 or 4 waves of 128 x 128 that read the next
 // fragments between the products (1.5 PFLOP/s within a tile, but 480 long items on 256 places end unevenly:
 // 157 against 158 us a call), 256 x 128, steps of 16; dx's planes in rows of E values instead of blocks
 // (dx alone 90 against 54 us: a load of 16 or 32 rows touched as many cache lines by halves or quarters);
 // the tiles of both products mixed, or dx's first (+15 to +40 %); two rounded bf16 pieces of dl (-20 us, see
 // above); the parts of d router_w added by the workgroup that finishes a tile last instead of a second launch
-// (its fences write back a whole L2: +50 us at 8192 tokens, +20 at 1333).
+// (its fences write back a whole L2: +50 us at 8192 tokens, +20 at 1333; a join without fences, as the balance loss
+// has it, is not tried); five stages for the 64 x 64 tiles (the same times).
 #include <type_traits>
 
 #include "moe_common.h"
@@ -371,7 +372,7 @@ int router_grad_parts_bound(int64_t T, int E, int H) {
 // Tile size and the parts of the weight gradient's reduction, by price: a step of one product of a tile
 // takes `full` us on a place with all `wgs` places of its compute unit taken, `alone` at least; `end` is a tile's
 // beginning and end, 5 us what a third launch costs, besides the parts' bytes.  The weight gradient's items
-// are started first, the others fill the places that they leave.  Fitted to sweeps over 16 to 8192 tokens at
+// are started first, the others fill the places that they leave.  For the MI355X's 256 compute units; fitted to sweeps over 16 to 8192 tokens at
 // 64 x 512 to 1024 x 2560.  Sides measured (us a call, 512 x 2560, fp32 dx):
 //   512 tokens:  128 26.4, 64 28.6     2048: 128 in 2 parts 50.5, 4 56.7; 64 62.4     8192: 128 148, 64 206
 //   512 tokens of 128 x 640: 64 in one part 14.5, 2 17.4; 4096: 64 in 8 parts 22.0, 128 24.6
