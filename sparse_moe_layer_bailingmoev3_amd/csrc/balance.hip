@@ -518,8 +518,8 @@ __global__ __launch_bounds__(256) void dlogits_kernel(DlogitsArgs a) {
 constexpr int BALANCE_SMALL_T = 256, BALANCE_SMALL_SEQ = 4;
 constexpr int64_t BALANCE_SMALL = 32768, BALANCE_SMALL_RUNS = 65536;
 
-// Tokens of a chunk: about one workgroup for each of the MI355X's 256 compute units, from 32 (four a wave, whose loads are under way at
-// once) to 256.  Sides measured (us a call, 512 experts): 8192 tokens 16 14.2, 32 12.8, 64 15.1; 16,384 32
+// Tokens of a chunk: about one workgroup for each of the MI355X's 256 compute units, from 32 (four a wave, whose
+// loads are under way at once) to 256.  Sides measured (us a call, 512 experts): 8192 tokens 16 14.2, 32 12.8, 64 15.1; 16,384 32
 // 17.7, 64 15.2, 128 20.4; 32,768 64 23.8, 128 22.5, 256 32.3; 200,000 128 107, 256 105.  But no longer than a
 // sequence on average, down to 4, as a workgroup takes its sequences one after another: 65 tokens in 16
 // sequences 10.8, in chunks of 32 25.3; 257 tokens of 64 experts in 64 sequences 10.0, 14.6.
@@ -530,7 +530,7 @@ int balance_chunk(int64_t T, int n_seq) {
   return c;
 }
 
-// Chunks do not grow with T where their size steps up: the most lie at the last T of each size.
+// The number of chunks falls where their size steps up: the most lie at the last T of each size.
 int64_t balance_chunks_bound(int64_t T, int n_seq) {
   auto chunks = [&](int64_t t) {
     const int c = balance_chunk(t, n_seq);

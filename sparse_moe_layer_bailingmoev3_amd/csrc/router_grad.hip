@@ -372,8 +372,8 @@ int router_grad_parts_bound(int64_t T, int E, int H) {
 // Tile size and the parts of the weight gradient's reduction, by price: a step of one product of a tile
 // takes `full` us on a place with all `wgs` places of its compute unit taken, `alone` at least; `end` is a tile's
 // beginning and end, 5 us what a third launch costs, besides the parts' bytes.  The weight gradient's items
-// are started first, the others fill the places that they leave.  For the MI355X's 256 compute units; fitted to sweeps over 16 to 8192 tokens at
-// 64 x 512 to 1024 x 2560.  Sides measured (us a call, 512 x 2560, fp32 dx):
+// are started first, the others fill the places that they leave.  For the MI355X's 256 compute units; fitted to
+// sweeps over 16 to 8192 tokens at 64 x 512 to 1024 x 2560.  Sides measured (us a call, 512 x 2560, fp32 dx):
 //   512 tokens:  128 26.4, 64 28.6     2048: 128 in 2 parts 50.5, 4 56.7; 64 62.4     8192: 128 148, 64 206
 //   512 tokens of 128 x 640: 64 in one part 14.5, 2 17.4; 4096: 64 in 8 parts 22.0, 128 24.6
 RouterGradPlan router_grad_plan(int64_t T, int E, int H, bool dw, bool dx) {
